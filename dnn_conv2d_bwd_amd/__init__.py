@@ -15,6 +15,9 @@ layout)` mirrors torch's convolution_backward with output_mask
 [True, False, False] (the call in the torch-IR listing of fusilli issue #101)
 and allocates dX.
 
+Next to it: the expert layer (ragged products grouped by expert and their
+gradients, experts.py) and the global gradient norm with clipping (grads.py).
+
 If libcbd.so is missing, importing this module raises ImportError: there is
 no fallback path.
 """
@@ -37,7 +40,11 @@ STATUS = {0: "CBD_OK", 1: "CBD_ERR_INVALID_ARG", 2: "CBD_ERR_UNSUPPORTED", 3: "C
 # Every symbol include/cbd.h declares.
 EXPORTS = ("cbd_plan", "cbd_plan_ex", "cbd_run", "cbd_run_ws", "cbd_run_noalloc", "cbd_plan_workspace_size",
            "cbd_plan_destroy", "cbd_status_string", "cbd_last_error", "cbd_plan_info",
-           "cbd_plan_subgemm", "cbd_plan_zero_region")
+           "cbd_plan_subgemm", "cbd_plan_zero_region",
+           "cbd_expert_plan", "cbd_expert_plan_destroy", "cbd_expert_plan_info", "cbd_expert_forward",
+           "cbd_expert_bwd_data", "cbd_expert_bwd_weight",
+           "cbd_grad_plan", "cbd_grad_plan_destroy", "cbd_grad_workspace_size", "cbd_grad_norm",
+           "cbd_grad_clip")
 
 
 class Problem(ctypes.Structure):
@@ -329,3 +336,10 @@ def conv2d_bwd_data(dy, w, input_size, stride=1, padding=0, dilation=1, groups=1
     dx = torch.empty(p.shapes()["dx"], dtype=dy.dtype, device=dy.device)
     run(p, dy, w, dx)
     return dx
+
+
+from .experts import (ECK, EKC, EXPERT_KERNEL_AUTO, EXPERT_KERNEL_GENERIC,  # noqa: E402,F401
+                      EXPERT_KERNEL_NAMES, BWD_DATA, BWD_WEIGHT, FORWARD, ExpertInfo, ExpertOptions,
+                      ExpertPlan, ExpertProblem, ExpertStrides, expert_bwd_data, expert_bwd_weight,
+                      expert_forward, expert_linear, expert_linear_bwd, expert_plan)
+from .grads import GradPlan, clip_grad_norm, clip_grads, grad_norm, grad_plan  # noqa: E402,F401

@@ -31,6 +31,10 @@ SOURCES = [
     "kern_grouped_wide.hip",
     "kern_zero_fill.hip",
     "kern_nchw_rows.hip",
+    "expert_api.cpp",
+    "kern_expert_generic.hip",
+    "grad_api.cpp",
+    "kern_grad_norm.hip",
 ]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

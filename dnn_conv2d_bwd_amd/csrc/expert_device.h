@@ -1,0 +1,126 @@
+// expert_device.h -- which rows a workgroup of an expert product owns.
+#pragma once
+#include "cbd_device.h"
+#include "expert_internal.h"
+
+namespace cbd {
+namespace dev {
+
+// Inclusive scans over the 64 lanes of a wave (values >= 0, so 0 is the
+// identity of both): shifts within rows of 16 lanes, then the last lane of
+// each row broadcast into the next ones.
+__device__ inline int wave_scan_sum(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31
+  return v;
+}
+__device__ inline int wave_scan_max(int v) {
+  auto mx = [](int a, int b) { return a > b ? a : b; };
+  v = mx(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));
+  v = mx(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));
+  v = mx(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));
+  v = mx(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));
+  v = mx(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));
+  v = mx(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));
+  return v;
+}
+
+// ends[i] clamped to [0, T].
+__device__ inline int clamped_end(const void* ends, int ends64, int i, int T) {
+  if (ends64) {
+    const int64_t v = ((const int64_t*)ends)[i];
+    return v < 0 ? 0 : v > T ? T : (int)v;
+  }
+  const int v = ((const int32_t*)ends)[i];
+  return v < 0 ? 0 : v > T ? T : v;
+}
+
+struct ExpertTile {
+  int e;           // expert; E for the rows past the last expert's
+  int begin, end;  // its rows
+  int m_tile, n_tile;
+  bool ok;         // false: no such tile (the grid is an upper bound)
+};
+
+// One chunk of 64 experts (and, as expert E, the rows past the last one's):
+// this lane's row range and its number of row tiles.
+__device__ inline void expert_chunk(const ExpertArgs& a, int base, int bn, int carry_max, int& lo, int& hi,
+                                    int& cnt) {
+  const int i = base + (int)(threadIdx.x & 63);
+  int v = i < a.E ? clamped_end(a.ends, a.ends64, i, a.T) : i == a.E ? a.T : 0;
+  hi = wave_scan_max(v);
+  hi = hi > carry_max ? hi : carry_max;
+  // The previous lane's hi: wave_shr:1 (lane 0 keeps the carry).
+  lo = __builtin_amdgcn_update_dpp(carry_max, hi, 0x138, 0xf, 0xf, false);
+  cnt = i <= a.E ? (hi - lo + bn - 1) / bn : 0;
+}
+
+// Tile of workgroup b of an AK / AM product with row tiles of bn rows.  Every
+// wave scans ends itself (64 experts a step), so no barrier is needed.  The
+// tiles of an expert are consecutive, in groups of 8 feature tiles by all row
+// tiles; consecutive workgroups of one XCD then share both operands' panels.
+__device__ inline ExpertTile find_row_tile(const ExpertArgs& a, int b, int bn) {
+  ExpertTile r;
+  r.ok = false;
+  r.e = 0;
+  r.begin = r.end = r.m_tile = r.n_tile = 0;
+  int lo, hi, cnt, sum;
+  int carry_max = 0, total = 0;
+  const int chunks = a.E / 64 + 1;  // E + 1 entries
+  for (int ch = 0; ch < chunks; ch++) {
+    expert_chunk(a, ch * 64, bn, carry_max, lo, hi, cnt);
+    sum = wave_scan_sum(cnt);
+    carry_max = __builtin_amdgcn_readlane(hi, 63);
+    total += __builtin_amdgcn_readlane(sum, 63);
+  }
+  const int64_t tiles = (int64_t)total * a.tiles_m;
+  if (b >= tiles) return r;
+  const int t = logical_tile(b, (int)tiles, tiles >= 64 ? 1 : 0);
+  int at = 0;  // row tiles before this chunk
+  if (chunks > 1) carry_max = 0;
+  for (int ch = 0; ch < chunks; ch++) {
+    if (chunks > 1) {
+      expert_chunk(a, ch * 64, bn, carry_max, lo, hi, cnt);
+      sum = wave_scan_sum(cnt);
+      carry_max = __builtin_amdgcn_readlane(hi, 63);
+    }
+    const unsigned long long hit = __ballot((int64_t)(at + sum) * a.tiles_m > t);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      const int n = __builtin_amdgcn_readlane(cnt, l);
+      const int first = at + __builtin_amdgcn_readlane(sum, l) - n;
+      r.e = ch * 64 + l;
+      r.begin = __builtin_amdgcn_readlane(lo, l);
+      r.end = __builtin_amdgcn_readlane(hi, l);
+      const int local = t - first * a.tiles_m;
+      const int g = local / (8 * n);
+      const int gm = a.tiles_m - 8 * g < 8 ? a.tiles_m - 8 * g : 8;
+      const int in = local - g * 8 * n;
+      r.n_tile = in / gm;
+      r.m_tile = 8 * g + in - r.n_tile * gm;
+      r.ok = true;
+      return r;
+    }
+    at += __builtin_amdgcn_readlane(sum, 63);
+  }
+  return r;
+}
+
+// Rows of expert e (a DW workgroup knows its expert).
+__device__ inline void expert_rows(const ExpertArgs& a, int e, int& begin, int& end) {
+  int v = 0;
+  for (int i = threadIdx.x & 63; i < e; i += 64) {
+    const int x = clamped_end(a.ends, a.ends64, i, a.T);
+    v = x > v ? x : v;
+  }
+  begin = __builtin_amdgcn_readlane(wave_scan_max(v), 63);
+  const int x = __builtin_amdgcn_readfirstlane(clamped_end(a.ends, a.ends64, e, a.T));
+  end = x > begin ? x : begin;
+}
+
+}  // namespace dev
+}  // namespace cbd

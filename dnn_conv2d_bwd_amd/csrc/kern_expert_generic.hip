@@ -1,0 +1,266 @@
+// kern_expert_generic.hip -- expert products of any type, size, stride and
+// alignment.
+//
+// A workgroup of 4 waves (2 x 2) computes a BM x BN tile (BM = BN = 128, or 64
+// where 128 would leave compute units idle) of one expert with
+// v_mfma_f32_16x16x4_f32; bf16 operands are widened while they are staged, so
+// every product is exact and every sum f32.  Operand tiles of 16 k are loaded
+// into registers one step ahead, then written to one of two LDS buffers, so a
+// step has one barrier.  Elements off an edge of the operand -- the expert's
+// rows, the features or the contracted length -- are staged as zeros on both
+// sides, so nothing beyond an edge (infinities and NaN included) takes part.
+//
+// k may be summed in any order as long as both operands agree: lane group
+// q = lane / 16 takes k = 4q + i at MFMA i.  A k-contiguous operand is staged
+// [row][16 k + 4 pad] and one 16-byte LDS read gives a lane its four k; an
+// operand whose features are contiguous is staged [k][features] and one read
+// gives a lane MB neighbouring features of one k, which makes feature
+// MB * i + block, instead of 16 * block + i, the row of lane i in a block.
+//
+// Bound: the f32 matrix rate (157 TFLOP/s; a 128 x 128 tile does 32 flops per
+// loaded byte in f32).
+#include "expert_device.h"
+
+namespace cbd {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint16_t u16x4u __attribute__((ext_vector_type(4), aligned(2)));
+
+constexpr int BK = 16;
+constexpr int THREADS = 256;
+
+// n (clamped to 0..4) elements from p, widened to f32; zeros after them.
+__device__ inline f32x4 load4(const float* p, int n) {
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  if (n >= 4) {
+    v = *(const f32x4u*)p;
+  } else {
+    if (n > 0) v[0] = p[0];
+    if (n > 1) v[1] = p[1];
+    if (n > 2) v[2] = p[2];
+  }
+  return v;
+}
+__device__ inline f32x4 load4(const uint16_t* p, int n) {
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  if (n >= 4) {
+    const u16x4u u = *(const u16x4u*)p;
+    for (int i = 0; i < 4; i++) v[i] = dev::bf16_to_f32(u[i]);
+  } else {
+    if (n > 0) v[0] = dev::bf16_to_f32(p[0]);
+    if (n > 1) v[1] = dev::bf16_to_f32(p[1]);
+    if (n > 2) v[2] = dev::bf16_to_f32(p[2]);
+  }
+  return v;
+}
+
+// Stores v[0..n) (n clamped to 0..4), rounded once.
+__device__ inline void store4(float* p, f32x4 v, int n, bool add) {
+  if (add) v += load4(p, n);
+  if (n >= 4) {
+    *(f32x4u*)p = v;
+  } else {
+    for (int i = 0; i < 3; i++)
+      if (i < n) p[i] = v[i];
+  }
+}
+__device__ inline void store4(uint16_t* p, f32x4 v, int n, bool add) {
+  if (add) v += load4(p, n);
+  u16x4u u;
+  for (int i = 0; i < 4; i++) u[i] = (uint16_t)dev::bf16_rne(v[i]);
+  if (n >= 4) {
+    *(u16x4u*)p = u;
+  } else {
+    for (int i = 0; i < 3; i++)
+      if (i < n) p[i] = u[i];
+  }
+}
+
+// One operand of a tile: R rows (features or tokens) by 16 k, R = 32 * NB.
+// KC: k is contiguous in memory.
+template <typename T, bool KC, int NB>
+struct Operand {
+  static constexpr int R = 32 * NB;
+  static constexpr int ROW = KC ? BK + 4 : R + 4;     // floats per LDS row
+  static constexpr int LDS = KC ? R * ROW : BK * ROW;  // floats
+  static constexpr int NV = R * BK / 4 / THREADS;      // 4-vectors per thread
+  const T* p;   // element (row 0, k 0) of the tile
+  int64_t ld;
+  int rows;     // rows inside the operand
+  f32x4 v[NV];
+
+  __device__ void load(int k0, int K) {
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+      const int idx = i * THREADS + (int)threadIdx.x;
+      if (KC) {
+        const int r = idx >> 2, k = k0 + 4 * (idx & 3);
+        v[i] = load4(p + r * ld + k, r < rows ? K - k : 0);
+      } else {
+        const int k = k0 + idx / (R / 4), r = 4 * (idx % (R / 4));
+        v[i] = load4(p + k * ld + r, k < K ? rows - r : 0);
+      }
+    }
+  }
+  __device__ void stage(float* lds) const {
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+      const int idx = i * THREADS + (int)threadIdx.x;
+      const int at = KC ? (idx >> 2) * ROW + 4 * (idx & 3) : (idx / (R / 4)) * ROW + 4 * (idx % (R / 4));
+      *(f32x4*)(lds + at) = v[i];
+    }
+  }
+  // Fragments of a wave's 16 * NB rows from row r0: f[block][i].
+  __device__ static void read(const float* lds, int r0, float (&f)[NB][4]) {
+    const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
+    if (KC) {
+#pragma unroll
+      for (int b = 0; b < NB; b++) {
+        const f32x4 x = *(const f32x4*)(lds + (r0 + 16 * b + r) * ROW + 4 * q);
+#pragma unroll
+        for (int i = 0; i < 4; i++) f[b][i] = x[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const float* s = lds + (4 * q + i) * ROW + r0 + NB * r;
+#pragma unroll
+        for (int b = 0; b < NB; b++) f[b][i] = s[b];
+      }
+    }
+  }
+  // Row of index i (0..15) of block b.
+  __device__ static int row(int i, int b) { return KC ? 16 * b + i : NB * i + b; }
+};
+
+template <typename T, typename TO, int FORM, int NB>
+__global__ __launch_bounds__(THREADS) void expert_generic_kernel(const ExpertArgs a) {
+  constexpr int BT = 32 * NB;
+  using OpA = Operand<T, FORM == EXPERT_AK, NB>;
+  using OpB = Operand<T, FORM != EXPERT_DW, NB>;
+  __shared__ __attribute__((aligned(16))) float lds[2][OpA::LDS + OpB::LDS];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = (wave & 1) * 16 * NB, wn = (wave >> 1) * 16 * NB;
+
+  OpA oa;
+  OpB ob;
+  TO* out;
+  int m0, K, mrows, nrows;
+  if constexpr (FORM == EXPERT_DW) {
+    const int per = a.tiles_m * a.tiles_n;
+    const int t = dev::logical_tile(blockIdx.x, per * a.E, 1);
+    const int e = t / per, in = t - e * per;
+    int begin, end;
+    dev::expert_rows(a, e, begin, end);
+    K = end - begin;
+    if (a.accumulate && K == 0) return;
+    m0 = (in % a.tiles_m) * BT;
+    const int n0 = (in / a.tiles_m) * BT;
+    mrows = a.M - m0;
+    nrows = a.N - n0;
+    oa.p = (const T*)a.a + (int64_t)begin * a.lda + m0;
+    ob.p = (const T*)a.b + (int64_t)begin * a.ldb + n0;
+    out = (TO*)a.out + e * a.o_expert + n0 * a.ldo + m0;
+  } else {
+    const dev::ExpertTile t = dev::find_row_tile(a, blockIdx.x, BT);
+    if (!t.ok) return;
+    K = t.e < a.E ? a.K : 0;  // rows past the last expert's: zeros
+    const int n0 = t.begin + t.n_tile * BT;
+    m0 = t.m_tile * BT;
+    mrows = a.M - m0;
+    nrows = t.end - n0;
+    oa.p = (const T*)a.a + (t.e < a.E ? t.e * a.a_expert : 0) + (FORM == EXPERT_AK ? m0 * a.lda : (int64_t)m0);
+    ob.p = (const T*)a.b + (int64_t)n0 * a.ldb;
+    out = (TO*)a.out + (int64_t)n0 * a.ldo + m0;
+  }
+  oa.ld = a.lda;
+  oa.rows = mrows;
+  ob.ld = a.ldb;
+  ob.rows = nrows;
+
+  f32x4 acc[NB][NB];
+#pragma unroll
+  for (int i = 0; i < NB; i++)
+#pragma unroll
+    for (int j = 0; j < NB; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  oa.load(0, K);
+  ob.load(0, K);
+  int buf = 0;
+  for (int k0 = 0; k0 < K; k0 += BK, buf ^= 1) {
+    float* la = lds[buf];
+    float* lb = la + OpA::LDS;
+    oa.stage(la);
+    ob.stage(lb);
+    // One barrier a step: buffer buf was last read two steps ago, before the
+    // previous step's barrier.
+    __syncthreads();
+    if (k0 + BK < K) {
+      oa.load(k0 + BK, K);
+      ob.load(k0 + BK, K);
+    }
+    float fa[NB][4], fb[NB][4];
+    OpA::read(la, wm, fa);
+    OpB::read(lb, wn, fb);
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+      for (int x = 0; x < NB; x++)
+#pragma unroll
+        for (int y = 0; y < NB; y++)
+          acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x4f32(fa[x][i], fb[y][i], acc[x][y], 0, 0, 0);
+  }
+
+  // Lane: column (n) lane % 16 of a block, rows (m) 4 * (lane / 16) + r.
+#pragma unroll
+  for (int y = 0; y < NB; y++) {
+    const int n = wn + OpB::row(lane & 15, y);
+    if (n >= nrows) continue;
+    TO* o = out + n * a.ldo;
+    if constexpr (FORM == EXPERT_AK) {
+#pragma unroll
+      for (int x = 0; x < NB; x++) {
+        const int m = wm + 16 * x + 4 * (lane >> 4);
+        store4(o + m, acc[x][y], mrows - m, a.accumulate);
+      }
+    } else {
+      // Features NB * (4q + r) + x: 4 * NB consecutive ones of a lane.
+      float v[4 * NB];
+#pragma unroll
+      for (int x = 0; x < NB; x++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) v[NB * r + x] = acc[x][y][r];
+#pragma unroll
+      for (int c = 0; c < NB; c++) {
+        const int m = wm + NB * 4 * (lane >> 4) + 4 * c;
+        store4(o + m, f32x4{v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]}, mrows - m, a.accumulate);
+      }
+    }
+  }
+}
+
+template <typename T, typename TO, int FORM>
+const void* pick(int bm) {
+  return bm == 128 ? (const void*)&expert_generic_kernel<T, TO, FORM, 4>
+                   : (const void*)&expert_generic_kernel<T, TO, FORM, 2>;
+}
+
+}  // namespace
+
+int launch_expert_generic(const ExpertArgs& a, const ExpertLaunch& l, void* stream) {
+  const void* k;
+  if (l.form == EXPERT_DW)
+    k = l.dtype == CBD_F32        ? pick<float, float, EXPERT_DW>(l.bm)
+        : l.out_dtype == CBD_F32  ? pick<uint16_t, float, EXPERT_DW>(l.bm)
+                                  : pick<uint16_t, uint16_t, EXPERT_DW>(l.bm);
+  else if (l.form == EXPERT_AK)
+    k = l.dtype == CBD_F32 ? pick<float, float, EXPERT_AK>(l.bm) : pick<uint16_t, uint16_t, EXPERT_AK>(l.bm);
+  else
+    k = l.dtype == CBD_F32 ? pick<float, float, EXPERT_AM>(l.bm) : pick<uint16_t, uint16_t, EXPERT_AM>(l.bm);
+  void* args[] = {const_cast<ExpertArgs*>(&a)};
+  return (int)hipLaunchKernel(k, dim3((unsigned)l.grid), dim3(THREADS), args, 0, (hipStream_t)stream);
+}
+
+}  // namespace cbd

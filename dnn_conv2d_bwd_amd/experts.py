@@ -1,0 +1,275 @@
+"""Expert layer: products grouped by expert with ragged row counts.
+
+    p = cbd.expert_plan(tokens=t, experts=e, c=c, k=k, dtype="bf16")
+    y  = cbd.expert_forward(p, x, w, ends)               # y[t] = W_e x[t]
+    dx = cbd.expert_bwd_data(p, dy, w, ends)             # dx[t] = W_e^T dy[t]
+    dw = cbd.expert_bwd_weight(p, dy, x, ends)           # dW_e = sum dy[t] x[t]^T
+
+Rows are sorted by expert; `ends[e]` (int32 or int64, on the GPU) is the row
+after expert e's last one.  Rows past the last end belong to no expert and
+come out as zeros; an expert without rows gets a zero gradient.  W is
+[E, K, C] ("ekc") or [E, C, K] ("eck").  Row tensors and weights may be
+strided views with a contiguous last dimension.  include/cbd.h states the
+operation in full.
+
+`expert_linear` and `expert_linear_bwd` build and cache the plan themselves.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import BF16, F32, _check, _dtype, _lib, _torch_dtype
+
+EKC, ECK = 0, 1
+FORWARD, BWD_DATA, BWD_WEIGHT = 0, 1, 2
+EXPERT_KERNEL_AUTO, EXPERT_KERNEL_GENERIC = -1, 0
+EXPERT_KERNEL_NAMES = {0: "generic"}
+
+
+class ExpertProblem(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("experts", ctypes.c_int64), ("c", ctypes.c_int64),
+                ("k", ctypes.c_int64), ("w_layout", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("dw_dtype", ctypes.c_int32), ("ends_bits", ctypes.c_int32)]
+
+
+class ExpertOptions(ctypes.Structure):
+    _fields_ = [("force_kernel", ctypes.c_int32), ("reserved", ctypes.c_int32 * 3)]
+
+
+class ExpertStrides(ctypes.Structure):
+    _fields_ = [("x_row", ctypes.c_int64), ("y_row", ctypes.c_int64), ("w_row", ctypes.c_int64),
+                ("w_expert", ctypes.c_int64)]
+
+
+class ExpertInfo(ctypes.Structure):
+    _fields_ = [("kernel", ctypes.c_int32), ("tile_m", ctypes.c_int32), ("tile_n", ctypes.c_int32),
+                ("threads", ctypes.c_int32), ("grid", ctypes.c_int64), ("flops", ctypes.c_int64)]
+
+
+def _bind():
+    P = ctypes.POINTER
+    V = ctypes.c_void_p
+    _lib.cbd_expert_plan.argtypes = [P(ExpertProblem), P(ExpertOptions), P(V)]
+    _lib.cbd_expert_plan_destroy.argtypes = [V]
+    _lib.cbd_expert_plan_destroy.restype = None
+    _lib.cbd_expert_plan_info.argtypes = [V, ctypes.c_int32, P(ExpertInfo)]
+    _lib.cbd_expert_forward.argtypes = [V, V, V, V, V, P(ExpertStrides), V]
+    _lib.cbd_expert_bwd_data.argtypes = [V, V, V, V, V, P(ExpertStrides), V]
+    _lib.cbd_expert_bwd_weight.argtypes = [V, V, V, V, V, ctypes.c_int32, P(ExpertStrides), V]
+    for f in ("plan", "plan_info", "forward", "bwd_data", "bwd_weight"):
+        getattr(_lib, "cbd_expert_" + f).restype = ctypes.c_int
+
+
+_bind()
+
+
+def _w_layout(v):
+    if isinstance(v, str):
+        return {"ekc": EKC, "eck": ECK}[v.lower()]
+    return int(v)
+
+
+class ExpertPlan:
+    """Owns cbd_expert_plan_t objects (one per width of ends); immutable; safe
+    to run from several streams."""
+
+    def __init__(self, tokens, experts, c, k, w_layout=EKC, dtype=BF16, dw_dtype=None,
+                 force_kernel=EXPERT_KERNEL_AUTO):
+        self.tokens, self.experts, self.c, self.k = int(tokens), int(experts), int(c), int(k)
+        self.w_layout, self.dtype = _w_layout(w_layout), _dtype(dtype)
+        self.dw_dtype = self.dtype if dw_dtype is None else _dtype(dw_dtype)
+        self._h = {}
+        opt = ExpertOptions(int(force_kernel))
+        for bits in (32, 64):
+            prob = ExpertProblem(self.tokens, self.experts, self.c, self.k, self.w_layout, self.dtype,
+                                 self.dw_dtype, bits)
+            h = ctypes.c_void_p()
+            _check(_lib.cbd_expert_plan(ctypes.byref(prob), ctypes.byref(opt), ctypes.byref(h)),
+                   "cbd_expert_plan")
+            self._h[bits] = h
+        self.w_shape = ((self.experts, self.k, self.c) if self.w_layout == EKC
+                        else (self.experts, self.c, self.k))
+        self._tdtype = _torch_dtype(self.dtype)
+        self._tdw = _torch_dtype(self.dw_dtype)
+
+    def info(self, op=FORWARD) -> ExpertInfo:
+        """What `op` launches on dense, 16-byte aligned tensors."""
+        out = ExpertInfo()
+        _check(_lib.cbd_expert_plan_info(self._h[32], op, ctypes.byref(out)), "cbd_expert_plan_info")
+        return out
+
+    def __del__(self):
+        lib = _lib  # None during interpreter shutdown
+        for h in getattr(self, "_h", {}).values():
+            if lib is not None and h.value:
+                lib.cbd_expert_plan_destroy(h)
+        self._h = {}
+
+
+def expert_plan(tokens, experts, c, k, w_layout="ekc", dtype="bf16", dw_dtype=None,
+                force_kernel=EXPERT_KERNEL_AUTO) -> ExpertPlan:
+    """dw_dtype: type of the weight gradient (default: dtype; "f32" keeps the
+    gradients of bf16 operands unrounded)."""
+    return ExpertPlan(tokens, experts, c, k, w_layout, dtype, dw_dtype, force_kernel)
+
+
+def _dense_strides(shape):
+    out, n = [], 1
+    for s in reversed(shape):
+        out.append(n)
+        n *= s
+    return tuple(reversed(out))
+
+
+def _strided(t, shape, dtype, device, name):
+    """Checks a tensor; its strides in elements but the last (0: dense)."""
+    if not hasattr(t, "data_ptr") or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU torch tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, plan wants {dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] != 1 and t.numel():
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    if t.is_contiguous():
+        return (0,) * (len(shape) - 1)
+    out, dense = [], _dense_strides(shape)
+    for n, s, d in zip(shape[:-1], st, dense):
+        if n > 1 and s < 1:
+            raise ValueError(f"{name} repeats rows (stride {s}); make it contiguous")
+        out.append(s if n > 1 else 0)
+    return tuple(out)
+
+
+def _handle(stream, device):
+    import torch
+
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on(device, stream):
+    """Context in which outputs are allocated and kernels launched: the
+    tensors' device and the call's stream (so that the caching allocator ties
+    new memory to the stream that writes it)."""
+    import contextlib
+
+    import torch
+
+    if stream is None:
+        if torch.cuda.current_device() == device.index:
+            return contextlib.nullcontext()
+        return torch.cuda.device(device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _ends(p, ends, device):
+    import torch
+
+    if not hasattr(ends, "data_ptr") or not ends.is_cuda or ends.device != device:
+        raise ValueError(f"ends must be a tensor on {device}")
+    if ends.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"ends must be int32 or int64, got {ends.dtype}")
+    if tuple(ends.shape) != (p.experts,) or not ends.is_contiguous():
+        raise ValueError(f"ends must be contiguous with shape ({p.experts},), got {tuple(ends.shape)}")
+    return 32 if ends.dtype == torch.int32 else 64
+
+
+def _strides(x, y, w):
+    if not (any(x) or any(y) or any(w)):
+        return None
+    return ctypes.byref(ExpertStrides(x[0], y[0], w[1], w[0]))
+
+
+def _product(p, op, rows, w, ends, out, stream):
+    import torch
+
+    fwd = op == FORWARD
+    wide_in, wide_out = (p.c, p.k) if fwd else (p.k, p.c)
+    in_name, out_name = ("x", "y") if fwd else ("dy", "dx")
+    s_in = _strided(rows, (p.tokens, wide_in), p._tdtype, None, in_name)
+    dev = rows.device
+    s_w = _strided(w, p.w_shape, p._tdtype, dev, "w")
+    bits = _ends(p, ends, dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((p.tokens, wide_out), dtype=p._tdtype, device=dev)
+        s_out = _strided(out, (p.tokens, wide_out), p._tdtype, dev, out_name)
+        st = _strides(s_in, s_out, s_w) if fwd else _strides(s_out, s_in, s_w)
+        f = _lib.cbd_expert_forward if fwd else _lib.cbd_expert_bwd_data
+        _check(f(p._h[bits], rows.data_ptr(), w.data_ptr(), ends.data_ptr(), out.data_ptr(), st,
+                 _handle(stream, dev)), "cbd_expert_forward" if fwd else "cbd_expert_bwd_data")
+    return out
+
+
+def expert_forward(p: ExpertPlan, x, w, ends, y=None, stream=None):
+    """y[t] = W_e x[t] on `stream` (default: torch's current one); y is
+    allocated unless given, and returned."""
+    return _product(p, FORWARD, x, w, ends, y, stream)
+
+
+def expert_bwd_data(p: ExpertPlan, dy, w, ends, dx=None, stream=None):
+    """dx[t] = W_e^T dy[t]."""
+    return _product(p, BWD_DATA, dy, w, ends, dx, stream)
+
+
+def expert_bwd_weight(p: ExpertPlan, dy, x, ends, dw=None, accumulate=False, stream=None):
+    """dW_e = sum over the rows of e of dy[t] x[t]^T, in the layout of W;
+    accumulate: added to the given dw."""
+    import torch
+
+    if accumulate and dw is None:
+        raise ValueError("accumulate needs dw")
+    s_y = _strided(dy, (p.tokens, p.k), p._tdtype, None, "dy")
+    dev = dy.device
+    s_x = _strided(x, (p.tokens, p.c), p._tdtype, dev, "x")
+    bits = _ends(p, ends, dev)
+    with _on(dev, stream):
+        if dw is None:
+            dw = torch.empty(p.w_shape, dtype=p._tdw, device=dev)
+        s_w = _strided(dw, p.w_shape, p._tdw, dev, "dw")
+        _check(_lib.cbd_expert_bwd_weight(p._h[bits], dy.data_ptr(), x.data_ptr(), ends.data_ptr(),
+                                          dw.data_ptr(), 1 if accumulate else 0, _strides(s_x, s_y, s_w),
+                                          _handle(stream, dev)), "cbd_expert_bwd_weight")
+    return dw
+
+
+_plans = {}
+
+
+def _cached(tokens, w_shape, w_layout, tdtype, dw_dtype):
+    import torch
+
+    lay = _w_layout(w_layout)
+    e, a, b = w_shape
+    c, k = (b, a) if lay == EKC else (a, b)
+    key = (tokens, e, c, k, lay, tdtype, dw_dtype)
+    p = _plans.get(key)
+    if p is None:
+        if len(_plans) >= 1024:  # served batches come in many sizes; a plan is rebuilt in microseconds
+            _plans.clear()
+        if tdtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"operands must be float32 or bfloat16, got {tdtype}")
+        p = _plans[key] = expert_plan(tokens, e, c, k, lay, F32 if tdtype == torch.float32 else BF16,
+                                      dw_dtype)
+    return p
+
+
+def expert_linear(x, w, ends, w_layout="ekc"):
+    """y[t] = W_e x[t] for x [T, C], w [E, K, C] or [E, C, K]."""
+    p = _cached(x.shape[0], tuple(w.shape), w_layout, w.dtype, None)
+    return expert_forward(p, x, w, ends)
+
+
+def expert_linear_bwd(dy, x, w, ends, w_layout="ekc", output_mask=(True, True), dw_dtype=None):
+    """(dx, dw) of expert_linear, each None where the mask leaves it out."""
+    p = _cached(x.shape[0], tuple(w.shape), w_layout, w.dtype, dw_dtype)
+    dx = expert_bwd_data(p, dy, w, ends) if output_mask[0] else None
+    dw = expert_bwd_weight(p, dy, x, ends) if output_mask[1] else None
+    return dx, dw

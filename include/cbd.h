@@ -332,6 +332,148 @@ cbd_status cbd_plan_info(const cbd_plan_t* plan, cbd_plan_info_t* out);
 cbd_status cbd_plan_subgemm(const cbd_plan_t* plan, int32_t i, cbd_subgemm_t* out);
 cbd_status cbd_plan_zero_region(const cbd_plan_t* plan, int32_t i, cbd_zero_region_t* out);
 
+/* ---- expert layer: products grouped by expert, ragged row counts ----
+ *
+ * A layer of E experts, each a K x C matrix W_e (C inputs, K outputs: a 1x1
+ * grouped convolution whose groups own ragged sets of rows instead of
+ * channel slices).  The T rows are sorted by expert and a device array
+ * `ends` of E integers gives each expert's last row + 1:
+ *
+ *   forward      y[t, k]  = sum_c x[t, c]  * W_e[k, c]       rows t of e
+ *   bwd_data     dx[t, c] = sum_k dy[t, k] * W_e[k, c]       rows t of e
+ *   bwd_weight   dW_e[k, c] = (dW_e[k, c] +) sum over the rows t of e of
+ *                             dy[t, k] * x[t, c]
+ *
+ * Rows of e: [B_{e-1}, B_e) with B_e = max over i <= e of ends[i] clamped to
+ * [0, T], B_{-1} = 0.  For non-decreasing ends in range that is the plain
+ * reading; any other contents (nothing on the host can check them) still
+ * give disjoint row sets inside the tensors.  Rows at or past B_{E-1} belong
+ * to no expert: y and dx are +0 there and bwd_weight does not read them.  An
+ * expert without rows gets dW_e = +0 (or keeps dW_e when accumulating).
+ * Sums are f32; each output element is rounded once, to nearest even (bf16
+ * accumulating: the f32 sum of the old value and the new sum).  A row's
+ * result does not depend on the other rows' values: no value of one row
+ * (infinity and NaN included) reaches another's y or dx, and none of an
+ * expert's rows reaches another expert's dW.
+ * Calls are stream-ordered, allocate nothing and can be captured in a graph:
+ * the launch depends on T, not on the contents of ends. */
+typedef enum {
+  CBD_EXPERT_EKC = 0, /* W [E][K][C]: an input row is contiguous  */
+  CBD_EXPERT_ECK = 1  /* W [E][C][K]: an output row is contiguous */
+} cbd_expert_layout;
+
+typedef enum {
+  CBD_EXPERT_FORWARD = 0,
+  CBD_EXPERT_BWD_DATA = 1,
+  CBD_EXPERT_BWD_WEIGHT = 2
+} cbd_expert_op;
+
+typedef struct {
+  int64_t tokens;    /* T >= 0: rows of x, y, dy and dx */
+  int64_t experts;   /* E, 1 .. 65536 */
+  int64_t c, k;      /* inputs and outputs of an expert, >= 1 */
+  int32_t w_layout;  /* cbd_expert_layout of W and dW */
+  int32_t dtype;     /* cbd_dtype of x, W, y, dy, dx */
+  int32_t dw_dtype;  /* cbd_dtype of dW: CBD_F32, or CBD_BF16 with bf16 operands */
+  int32_t ends_bits; /* 32 or 64: signed integers of that width in ends */
+} cbd_expert_problem;
+
+typedef enum {
+  CBD_EXPERT_KERNEL_AUTO = -1,
+  CBD_EXPERT_KERNEL_GENERIC = 0 /* any type, size, stride and alignment: f32 MFMA */
+} cbd_expert_kernel;
+
+typedef struct {
+  int32_t force_kernel; /* cbd_expert_kernel */
+  int32_t reserved[3];  /* must be zero */
+} cbd_expert_options;
+
+/* Row and expert strides in elements; 0 (or a NULL pointer): dense.  The
+ * innermost dimension is always contiguous.  A row stride is at least the
+ * row's width, an expert stride at least the slice's extent. */
+typedef struct {
+  int64_t x_row;    /* x (forward, bwd_weight) or dx (bwd_data) */
+  int64_t y_row;    /* y (forward) or dy */
+  int64_t w_row;    /* W, or dW: between the rows of one expert */
+  int64_t w_expert; /* W, or dW: between experts */
+} cbd_expert_strides;
+
+typedef struct {
+  int32_t kernel;         /* cbd_expert_kernel */
+  int32_t tile_m, tile_n; /* tile: output features (contiguous side) x rows
+                             (bwd_weight: x the other feature side) */
+  int32_t threads;
+  int64_t grid;           /* workgroups launched */
+  int64_t flops;          /* 2*T*C*K */
+} cbd_expert_info_t;
+
+typedef struct cbd_expert_plan_s cbd_expert_plan_t; /* opaque; immutable */
+
+/* Build a plan (host-only work; needs no GPU).  options may be NULL.
+ * INVALID_ARG: NULL problem or output, sizes out of the ranges above, an
+ * unknown layout, type or option; UNSUPPORTED: tokens > 2^30, an expert's W
+ * of 2^31 bytes or more, c or k > 2^20. */
+cbd_status cbd_expert_plan(const cbd_expert_problem* problem, const cbd_expert_options* options,
+                           cbd_expert_plan_t** out_plan);
+void cbd_expert_plan_destroy(cbd_expert_plan_t* plan); /* NULL is allowed */
+
+/* What a call on dense, 16-byte aligned tensors launches. */
+cbd_status cbd_expert_plan_info(const cbd_expert_plan_t* plan, int32_t op, cbd_expert_info_t* out);
+
+/* The three operators.  y, dx and dW are overwritten (dW added to with
+ * accumulate = 1).  Pointers need the alignment of their elements; every
+ * other alignment or stride only selects a kernel.  Errors: INVALID_ARG for
+ * NULL pointers (row tensors may be NULL when T = 0), strides below the
+ * width and an output that overlaps an operand or ends; UNSUPPORTED for
+ * pointers off their element's alignment and strides whose tiles pass 32-bit
+ * offsets; HIP for a launch error.  Nothing is launched on an error. */
+cbd_status cbd_expert_forward(const cbd_expert_plan_t* plan, const void* x, const void* w,
+                              const void* ends, void* y, const cbd_expert_strides* strides,
+                              void* stream);
+cbd_status cbd_expert_bwd_data(const cbd_expert_plan_t* plan, const void* dy, const void* w,
+                               const void* ends, void* dx, const cbd_expert_strides* strides,
+                               void* stream);
+cbd_status cbd_expert_bwd_weight(const cbd_expert_plan_t* plan, const void* dy, const void* x,
+                                 const void* ends, void* dw, int32_t accumulate,
+                                 const cbd_expert_strides* strides, void* stream);
+
+/* ---- global gradient norm and clipping over a list of tensors ----
+ *
+ *   norm  = sqrt( sum over every element g of every tensor of g^2 )
+ *   out_i = g_i * min(1, max_norm / (norm + 1e-6))
+ *
+ * Squares and sums are in 64 bits (no overflow or underflow for any f32 or
+ * bf16 values), and so is the factor; norm is rounded to f32, and each output
+ * element to f32 and, if it is bf16, from there to bf16.  The order of the sums is fixed by the list of sizes:
+ * the same inputs give the same bits.  A NaN or infinite gradient gives a
+ * NaN or infinite norm; the factor is then NaN or 0, by the formula, and
+ * callers that want to skip such a step test the norm.  Tensors are dense
+ * arrays of `counts[i]` elements in any order, f32 or bf16, mixed freely,
+ * empty ones allowed; an empty list has norm 0.  Where the factor is 1 and a
+ * tensor is clipped in place, nothing is written. */
+typedef struct cbd_grad_plan_s cbd_grad_plan_t; /* opaque; immutable */
+
+/* Host-only.  dtypes[i] is a cbd_dtype.  INVALID_ARG: NULL, negative counts,
+ * unknown types; UNSUPPORTED: n > 65536 or a count of 2^40 or more. */
+cbd_status cbd_grad_plan(const int64_t* counts, const int32_t* dtypes, int32_t n,
+                         cbd_grad_plan_t** out_plan);
+void cbd_grad_plan_destroy(cbd_grad_plan_t* plan); /* NULL is allowed */
+
+/* Device workspace both calls need (256-byte aligned; its contents need no
+ * initialisation and are not kept; one per stream in use). */
+cbd_status cbd_grad_workspace_size(const cbd_grad_plan_t* plan, uint64_t* bytes);
+
+/* grads: host array of n device pointers (read during the call only).  norm:
+ * one f32 on the device.  outs: as grads, NULL for in place; each out is its
+ * own gradient or overlaps no tensor of either list.  max_norm >= 0.  Errors
+ * as for the expert calls, plus INVALID_ARG for a short workspace, a NaN or
+ * negative max_norm and overlapping outputs. */
+cbd_status cbd_grad_norm(const cbd_grad_plan_t* plan, const void* const* grads, float* norm,
+                         void* workspace, uint64_t workspace_bytes, void* stream);
+cbd_status cbd_grad_clip(const cbd_grad_plan_t* plan, const void* const* grads, void* const* outs,
+                         double max_norm, float* norm, void* workspace, uint64_t workspace_bytes,
+                         void* stream);
+
 #ifdef __cplusplus
 }
 #endif
