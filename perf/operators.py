@@ -181,7 +181,7 @@ def prepare(case, seed):
         else:
             state["plan"] = cbd.expert_plan(tokens=case["tokens"], experts=case["experts"], c=case["c"],
                                             k=case["k"], w_layout=case["w_layout"], dtype=case["dtype"],
-                                            dw_dtype=case["dw"])
+                                            dw_dtype=case["dw"] if case["op"] == "bwd_weight" else None)
     return state
 
 
