@@ -33,6 +33,7 @@ SOURCES = [
     "kern_nchw_rows.hip",
     "expert_api.cpp",
     "kern_expert_generic.hip",
+    "kern_expert_mfma.hip",
     "grad_api.cpp",
     "kern_grad_norm.hip",
 ]

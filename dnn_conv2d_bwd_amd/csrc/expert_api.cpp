@@ -48,13 +48,11 @@ bool share(const Block& a, const Block& b) {
 
 constexpr int64_t kMaxSlice = int64_t(1) << 31;  // bytes: offsets within a slice or tile are 32-bit
 
-// Launch of an operator.  `aligned`: every row of every operand starts on a
-// 16-byte boundary.
-ExpertLaunch choose(const cbd_expert_plan_s& plan, int op, bool aligned) {
+// Launch of an operator.  `dma`: both inputs start every row on a 16-byte
+// boundary and (32 rows of W) stay within 32-bit offsets.
+ExpertLaunch choose(const cbd_expert_plan_s& plan, int op, bool dma) {
   const cbd_expert_problem& p = plan.prob;
-  (void)aligned;
   ExpertLaunch l;
-  l.kernel = CBD_EXPERT_KERNEL_GENERIC;
   l.dtype = p.dtype;
   l.out_dtype = op == CBD_EXPERT_BWD_WEIGHT ? p.dw_dtype : p.dtype;
   l.form = op == CBD_EXPERT_BWD_WEIGHT ? cbd::EXPERT_DW
@@ -71,8 +69,19 @@ ExpertLaunch choose(const cbd_expert_plan_s& plan, int op, bool aligned) {
     const int64_t spans = p.experts + 1 < p.tokens ? p.experts + 1 : p.tokens;
     return tm * (p.tokens / bn + spans);
   };
-  l.bm = l.bn = 128;
-  if (grid(128, 128) < 512) l.bm = l.bn = 64;
+  l.kernel = plan.opt.force_kernel;
+  if (l.kernel == CBD_EXPERT_KERNEL_AUTO)
+    l.kernel = p.dtype == CBD_BF16 ? CBD_EXPERT_KERNEL_MFMA : CBD_EXPERT_KERNEL_GENERIC;
+  l.dma = 0;
+  if (l.kernel == CBD_EXPERT_KERNEL_MFMA) {
+    // k runs along the rows of x (dy), and of W in the AK form.
+    l.dma = dma && (op == CBD_EXPERT_BWD_WEIGHT || n % 8 == 0);
+    l.bm = 256;
+    l.bn = grid(256, 256) >= 512 ? 256 : 128;
+  } else {
+    l.bm = l.bn = 128;
+    if (grid(128, 128) < 512) l.bm = l.bn = 64;
+  }
   l.grid = grid(l.bm, l.bn);
   return l;
 }
@@ -137,7 +146,10 @@ cbd_status run(const cbd_expert_plan_t* plan, int op, const void* row_in, const 
   auto on16 = [](const Block& b) {
     return (((uintptr_t)b.p | (uint64_t)(b.ld * b.es) | (uint64_t)(b.count > 1 ? b.stride * b.es : 0)) & 15u) == 0;
   };
-  const ExpertLaunch l = choose(*plan, op, on16(bx) && on16(by) && on16(bw));
+  bool dma = true;
+  for (const Block* b : {&bx, &by, &bw})
+    if (b != &bo) dma = dma && on16(*b) && b->ld * 32 * b->es < kMaxSlice;
+  const ExpertLaunch l = choose(*plan, op, dma);
   if (l.grid > INT32_MAX) return fail(CBD_ERR_UNSUPPORTED, "too many tiles for one launch");
 
   ExpertArgs a = {};
@@ -171,7 +183,8 @@ cbd_status run(const cbd_expert_plan_t* plan, int op, const void* row_in, const 
     a.ldo = bo.ld;
   }
   a.tiles_m = (a.M + l.bm - 1) / l.bm;
-  const int err = cbd::launch_expert_generic(a, l, stream);
+  const int err = l.kernel == CBD_EXPERT_KERNEL_MFMA ? cbd::launch_expert_mfma(a, l, stream)
+                                                     : cbd::launch_expert_generic(a, l, stream);
   if (err) {
     cbd::set_error(std::string("expert kernel launch failed: ") + cbd::hip_error_name(err));
     return CBD_ERR_HIP;
@@ -202,10 +215,12 @@ cbd_status make_plan(const cbd_expert_problem* q, const cbd_expert_options* opt,
     return fail(CBD_ERR_INVALID_ARG, "dw_dtype must be f32, or bf16 with bf16 operands");
   if (q->ends_bits != 32 && q->ends_bits != 64) return fail(CBD_ERR_INVALID_ARG, "ends_bits must be 32 or 64");
   if (opt) {
-    if (opt->force_kernel < CBD_EXPERT_KERNEL_AUTO || opt->force_kernel > CBD_EXPERT_KERNEL_GENERIC)
+    if (opt->force_kernel < CBD_EXPERT_KERNEL_AUTO || opt->force_kernel > CBD_EXPERT_KERNEL_MFMA)
       return fail(CBD_ERR_INVALID_ARG, "unknown force_kernel");
     for (int32_t r : opt->reserved)
       if (r) return fail(CBD_ERR_INVALID_ARG, "reserved options must be zero");
+    if (opt->force_kernel > CBD_EXPERT_KERNEL_GENERIC && q->dtype != CBD_BF16)
+      return fail(CBD_ERR_UNSUPPORTED, "the forced kernel takes bf16 operands only");
   }
   if (q->experts > 65536) return fail(CBD_ERR_UNSUPPORTED, "more than 65536 experts");
   if (q->tokens > (int64_t(1) << 30)) return fail(CBD_ERR_UNSUPPORTED, "more than 2^30 tokens");

@@ -59,6 +59,15 @@ __device__ inline void expert_chunk(const ExpertArgs& a, int base, int bn, int c
   cnt = i <= a.E ? (hi - lo + bn - 1) / bn : 0;
 }
 
+// Logical tile of hardware workgroup b: XCD x (b % 8) gets tiles 32 x .. 32 x
+// + 31 of every 256, and its share of what is left, so neighbouring tiles meet
+// in one L2 while the XCDs' loads stay alike however the experts' sizes vary.
+__device__ inline int spread_tile(int b, int tiles) {
+  const int full = tiles & ~255;
+  if (b < full) return (b & ~255) + ((b & 7) << 5) + ((b & 255) >> 3);
+  return full + logical_tile(b - full, tiles - full, tiles - full >= 64 ? 1 : 0);
+}
+
 // Tile of workgroup b of an AK / AM product with row tiles of bn rows.  Every
 // wave scans ends itself (64 experts a step), so no barrier is needed.  The
 // tiles of an expert are consecutive, in groups of 8 feature tiles by all row
@@ -79,7 +88,7 @@ __device__ inline ExpertTile find_row_tile(const ExpertArgs& a, int b, int bn) {
   }
   const int64_t tiles = (int64_t)total * a.tiles_m;
   if (b >= tiles) return r;
-  const int t = logical_tile(b, (int)tiles, tiles >= 64 ? 1 : 0);
+  const int t = spread_tile(b, (int)tiles);
   int at = 0;  // row tiles before this chunk
   if (chunks > 1) carry_max = 0;
   for (int ch = 0; ch < chunks; ch++) {
@@ -120,6 +129,24 @@ __device__ inline void expert_rows(const ExpertArgs& a, int e, int& begin, int& 
   begin = __builtin_amdgcn_readlane(wave_scan_max(v), 63);
   const int x = __builtin_amdgcn_readfirstlane(clamped_end(a.ends, a.ends64, e, a.T));
   end = x > begin ? x : begin;
+}
+
+// Tile of workgroup b of a DW product (m_tile and n_tile in groups of 8 feature
+// tiles by all tiles of the other side, as above).
+__device__ inline ExpertTile find_weight_tile(const ExpertArgs& a, int b) {
+  ExpertTile r;
+  const int per = a.tiles_m * a.tiles_n;
+  const int t = spread_tile(b, per * a.E);
+  r.e = t / per;
+  const int local = t - r.e * per;
+  const int g = local / (8 * a.tiles_n);
+  const int gm = a.tiles_m - 8 * g < 8 ? a.tiles_m - 8 * g : 8;
+  const int in = local - g * 8 * a.tiles_n;
+  r.n_tile = in / gm;
+  r.m_tile = 8 * g + in - r.n_tile * gm;
+  r.ok = true;
+  expert_rows(a, r.e, r.begin, r.end);
+  return r;
 }
 
 }  // namespace dev

@@ -43,9 +43,11 @@ struct ExpertLaunch {
   int32_t dtype, out_dtype;
   int32_t bm, bn;  // tile
   int32_t threads;
+  int32_t dma;     // operands go straight to LDS
   int64_t grid;
 };
 
 int launch_expert_generic(const ExpertArgs& a, const ExpertLaunch& l, void* stream);
+int launch_expert_mfma(const ExpertArgs& a, const ExpertLaunch& l, void* stream);
 
 }  // namespace cbd

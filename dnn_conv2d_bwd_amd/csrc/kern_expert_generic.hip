@@ -149,20 +149,16 @@ __global__ __launch_bounds__(THREADS) void expert_generic_kernel(const ExpertArg
   TO* out;
   int m0, K, mrows, nrows;
   if constexpr (FORM == EXPERT_DW) {
-    const int per = a.tiles_m * a.tiles_n;
-    const int t = dev::logical_tile(blockIdx.x, per * a.E, 1);
-    const int e = t / per, in = t - e * per;
-    int begin, end;
-    dev::expert_rows(a, e, begin, end);
-    K = end - begin;
+    const dev::ExpertTile t = dev::find_weight_tile(a, blockIdx.x);
+    K = t.end - t.begin;
     if (a.accumulate && K == 0) return;
-    m0 = (in % a.tiles_m) * BT;
-    const int n0 = (in / a.tiles_m) * BT;
+    m0 = t.m_tile * BT;
+    const int n0 = t.n_tile * BT;
     mrows = a.M - m0;
     nrows = a.N - n0;
-    oa.p = (const T*)a.a + (int64_t)begin * a.lda + m0;
-    ob.p = (const T*)a.b + (int64_t)begin * a.ldb + n0;
-    out = (TO*)a.out + e * a.o_expert + n0 * a.ldo + m0;
+    oa.p = (const T*)a.a + (int64_t)t.begin * a.lda + m0;
+    ob.p = (const T*)a.b + (int64_t)t.begin * a.ldb + n0;
+    out = (TO*)a.out + t.e * a.o_expert + n0 * a.ldo + m0;
   } else {
     const dev::ExpertTile t = dev::find_row_tile(a, blockIdx.x, BT);
     if (!t.ok) return;

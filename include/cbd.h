@@ -380,7 +380,8 @@ typedef struct {
 
 typedef enum {
   CBD_EXPERT_KERNEL_AUTO = -1,
-  CBD_EXPERT_KERNEL_GENERIC = 0 /* any type, size, stride and alignment: f32 MFMA */
+  CBD_EXPERT_KERNEL_GENERIC = 0, /* any type, size, stride and alignment: f32 MFMA */
+  CBD_EXPERT_KERNEL_MFMA = 1     /* bf16: 256 features x many rows a tile */
 } cbd_expert_kernel;
 
 typedef struct {
@@ -412,7 +413,8 @@ typedef struct cbd_expert_plan_s cbd_expert_plan_t; /* opaque; immutable */
 /* Build a plan (host-only work; needs no GPU).  options may be NULL.
  * INVALID_ARG: NULL problem or output, sizes out of the ranges above, an
  * unknown layout, type or option; UNSUPPORTED: tokens > 2^30, an expert's W
- * of 2^31 bytes or more, c or k > 2^20. */
+ * of 2^31 bytes or more, c or k > 2^20, a forced kernel that does not take
+ * the type. */
 cbd_status cbd_expert_plan(const cbd_expert_problem* problem, const cbd_expert_options* options,
                            cbd_expert_plan_t** out_plan);
 void cbd_expert_plan_destroy(cbd_expert_plan_t* plan); /* NULL is allowed */
