@@ -1,5 +1,6 @@
 // expert_api.cpp -- plans, argument checks and kernel choice of the expert
 // layer (forward, bwd_data, bwd_weight).
+#include <algorithm>
 #include <cstdint>
 #include <new>
 #include <string>
@@ -49,8 +50,9 @@ bool share(const Block& a, const Block& b) {
 constexpr int64_t kMaxSlice = int64_t(1) << 31;  // bytes: offsets within a slice or tile are 32-bit
 
 // Launch of an operator.  `dma`: both inputs start every row on a 16-byte
-// boundary and (32 rows of W) stay within 32-bit offsets.
-ExpertLaunch choose(const cbd_expert_plan_s& plan, int op, bool dma) {
+// boundary and (256 rows of W) stay within 32-bit
+// offsets; `whole_out`: so does the output, in 16-byte multiples.
+ExpertLaunch choose(const cbd_expert_plan_s& plan, int op, bool dma, bool whole_out) {
   const cbd_expert_problem& p = plan.prob;
   ExpertLaunch l;
   l.dtype = p.dtype;
@@ -76,13 +78,14 @@ ExpertLaunch choose(const cbd_expert_plan_s& plan, int op, bool dma) {
   if (l.kernel == CBD_EXPERT_KERNEL_MFMA) {
     // k runs along the rows of x (dy), and of W in the AK form.
     l.dma = dma && (op == CBD_EXPERT_BWD_WEIGHT || n % 8 == 0);
-    l.bm = 256;
-    l.bn = grid(256, 256) >= 512 ? 256 : 128;
+    l.bm = l.bn = l.dma && whole_out && grid(256, 256) >= 512 ? 256 : 128;
   } else {
     l.bm = l.bn = 128;
     if (grid(128, 128) < 512) l.bm = l.bn = 64;
   }
   l.grid = grid(l.bm, l.bn);
+  // Workgroups that stay: one (256 x 256: its LDS) or two a compute unit.
+  if (l.kernel == CBD_EXPERT_KERNEL_MFMA) l.grid = std::min<int64_t>(l.grid, l.bm == 256 ? 256 : 512);
   return l;
 }
 
@@ -146,10 +149,11 @@ cbd_status run(const cbd_expert_plan_t* plan, int op, const void* row_in, const 
   auto on16 = [](const Block& b) {
     return (((uintptr_t)b.p | (uint64_t)(b.ld * b.es) | (uint64_t)(b.count > 1 ? b.stride * b.es : 0)) & 15u) == 0;
   };
+  const bool whole_out = on16(bo) && bo.width % (16 / bo.es) == 0;
   bool dma = true;
   for (const Block* b : {&bx, &by, &bw})
-    if (b != &bo) dma = dma && on16(*b) && b->ld * 32 * b->es < kMaxSlice;
-  const ExpertLaunch l = choose(*plan, op, dma);
+    if (b != &bo) dma = dma && on16(*b) && b->ld * 256 * b->es < kMaxSlice;
+  const ExpertLaunch l = choose(*plan, op, dma, whole_out);
   if (l.grid > INT32_MAX) return fail(CBD_ERR_UNSUPPORTED, "too many tiles for one launch");
 
   ExpertArgs a = {};
@@ -159,6 +163,7 @@ cbd_status run(const cbd_expert_plan_t* plan, int op, const void* row_in, const 
   a.E = (int32_t)p.experts;
   a.out = out;
   a.accumulate = accumulate;
+  a.whole_out = whole_out;
   if (op == CBD_EXPERT_BWD_WEIGHT) {
     const Block& ba = p.w_layout == CBD_EXPERT_EKC ? bx : by;
     const Block& bb = p.w_layout == CBD_EXPERT_EKC ? by : bx;
@@ -253,7 +258,8 @@ extern "C" cbd_status cbd_expert_plan_info(const cbd_expert_plan_t* plan, int32_
     const cbd_expert_problem& p = plan->prob;
     // Dense rows are 16-byte multiples when the widths are.
     const int64_t q = 16 / esize(p.dtype);
-    const ExpertLaunch l = choose(*plan, op, p.c % q == 0 && p.k % q == 0);
+    const bool whole = p.c % q == 0 && p.k % q == 0;
+    const ExpertLaunch l = choose(*plan, op, whole, whole);
     out->kernel = l.kernel;
     out->tile_m = l.bm;
     out->tile_n = l.bn;

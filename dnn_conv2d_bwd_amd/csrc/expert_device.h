@@ -3,6 +3,10 @@
 #include "cbd_device.h"
 #include "expert_internal.h"
 
+// Inlined always: a kernel's by-value arguments would otherwise be copied to
+// memory to be passed by reference.
+#define CBD_INLINE __attribute__((always_inline))
+
 namespace cbd {
 namespace dev {
 
@@ -30,13 +34,19 @@ __device__ inline int wave_scan_max(int v) {
 }
 
 // ends[i] clamped to [0, T].
-__device__ inline int clamped_end(const void* ends, int ends64, int i, int T) {
+CBD_INLINE __device__ inline int clamped_end(const void* ends, int ends64, int i, int T) {
   if (ends64) {
     const int64_t v = ((const int64_t*)ends)[i];
     return v < 0 ? 0 : v > T ? T : (int)v;
   }
   const int v = ((const int32_t*)ends)[i];
   return v < 0 ? 0 : v > T ? T : v;
+}
+
+// A value that is the same in every lane, in scalar registers.
+CBD_INLINE __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+CBD_INLINE __device__ inline uint64_t uniform(uint64_t v) {
+  return (uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)(uint32_t)v);
 }
 
 struct ExpertTile {
@@ -48,7 +58,7 @@ struct ExpertTile {
 
 // One chunk of 64 experts (and, as expert E, the rows past the last one's):
 // this lane's row range and its number of row tiles.
-__device__ inline void expert_chunk(const ExpertArgs& a, int base, int bn, int carry_max, int& lo, int& hi,
+CBD_INLINE __device__ inline void expert_chunk(const ExpertArgs& a, int base, int bn, int carry_max, int& lo, int& hi,
                                     int& cnt) {
   const int i = base + (int)(threadIdx.x & 63);
   int v = i < a.E ? clamped_end(a.ends, a.ends64, i, a.T) : i == a.E ? a.T : 0;
@@ -68,59 +78,65 @@ __device__ inline int spread_tile(int b, int tiles) {
   return full + logical_tile(b - full, tiles - full, tiles - full >= 64 ? 1 : 0);
 }
 
-// Tile of workgroup b of an AK / AM product with row tiles of bn rows.  Every
-// wave scans ends itself (64 experts a step), so no barrier is needed.  The
-// tiles of an expert are consecutive, in groups of 8 feature tiles by all row
-// tiles; consecutive workgroups of one XCD then share both operands' panels.
-__device__ inline ExpertTile find_row_tile(const ExpertArgs& a, int b, int bn) {
-  ExpertTile r;
-  r.ok = false;
-  r.e = 0;
-  r.begin = r.end = r.m_tile = r.n_tile = 0;
-  int lo, hi, cnt, sum;
-  int carry_max = 0, total = 0;
-  const int chunks = a.E / 64 + 1;  // E + 1 entries
-  for (int ch = 0; ch < chunks; ch++) {
-    expert_chunk(a, ch * 64, bn, carry_max, lo, hi, cnt);
-    sum = wave_scan_sum(cnt);
-    carry_max = __builtin_amdgcn_readlane(hi, 63);
-    total += __builtin_amdgcn_readlane(sum, 63);
-  }
-  const int64_t tiles = (int64_t)total * a.tiles_m;
-  if (b >= tiles) return r;
-  const int t = spread_tile(b, (int)tiles);
-  int at = 0;  // row tiles before this chunk
-  if (chunks > 1) carry_max = 0;
-  for (int ch = 0; ch < chunks; ch++) {
-    if (chunks > 1) {
+// Row tiles (of bn rows) of an AK / AM product.  Every wave scans ends itself,
+// 64 experts a step, so no barrier is needed.  The tiles of an expert are
+// consecutive, in groups of 8 feature tiles by all row tiles; neighbouring
+// workgroups of one XCD then share both operands' panels.
+struct RowTiles {
+  int lo, hi, cnt, sum;  // the only chunk, where 63 experts or fewer make one
+  int64_t tiles;
+
+  CBD_INLINE __device__ void init(const ExpertArgs& a, int bn) {
+    int carry_max = 0, total = 0;
+    for (int ch = 0; ch <= a.E / 64; ch++) {  // E + 1 entries
       expert_chunk(a, ch * 64, bn, carry_max, lo, hi, cnt);
       sum = wave_scan_sum(cnt);
       carry_max = __builtin_amdgcn_readlane(hi, 63);
+      total += __builtin_amdgcn_readlane(sum, 63);
     }
-    const unsigned long long hit = __ballot((int64_t)(at + sum) * a.tiles_m > t);
-    if (hit) {
-      const int l = __builtin_ctzll(hit);
-      const int n = __builtin_amdgcn_readlane(cnt, l);
-      const int first = at + __builtin_amdgcn_readlane(sum, l) - n;
-      r.e = ch * 64 + l;
-      r.begin = __builtin_amdgcn_readlane(lo, l);
-      r.end = __builtin_amdgcn_readlane(hi, l);
-      const int local = t - first * a.tiles_m;
-      const int g = local / (8 * n);
-      const int gm = a.tiles_m - 8 * g < 8 ? a.tiles_m - 8 * g : 8;
-      const int in = local - g * 8 * n;
-      r.n_tile = in / gm;
-      r.m_tile = 8 * g + in - r.n_tile * gm;
-      r.ok = true;
-      return r;
-    }
-    at += __builtin_amdgcn_readlane(sum, 63);
+    tiles = (int64_t)total * a.tiles_m;
   }
-  return r;
-}
+  // Tile of hardware workgroup b.
+  CBD_INLINE __device__ ExpertTile at(const ExpertArgs& a, int b, int bn) {
+    ExpertTile r;
+    r.ok = false;
+    r.e = 0;
+    r.begin = r.end = r.m_tile = r.n_tile = 0;
+    if (b >= tiles) return r;
+    const int t = spread_tile(b, (int)tiles);
+    const int chunks = a.E / 64 + 1;
+    int before = 0, carry_max = 0;  // row tiles before this chunk
+    for (int ch = 0; ch < chunks; ch++) {
+      if (chunks > 1) {
+        expert_chunk(a, ch * 64, bn, carry_max, lo, hi, cnt);
+        sum = wave_scan_sum(cnt);
+        carry_max = __builtin_amdgcn_readlane(hi, 63);
+      }
+      const unsigned long long hit = __ballot((int64_t)(before + sum) * a.tiles_m > t);
+      if (hit) {
+        const int l = __builtin_ctzll(hit);
+        const int n = __builtin_amdgcn_readlane(cnt, l);
+        const int first = before + __builtin_amdgcn_readlane(sum, l) - n;
+        r.e = ch * 64 + l;
+        r.begin = __builtin_amdgcn_readlane(lo, l);
+        r.end = __builtin_amdgcn_readlane(hi, l);
+        const int local = t - first * a.tiles_m;
+        const int g = local / (8 * n);
+        const int gm = a.tiles_m - 8 * g < 8 ? a.tiles_m - 8 * g : 8;
+        const int in = local - g * 8 * n;
+        r.n_tile = uniform(in / gm);
+        r.m_tile = uniform(8 * g + in - r.n_tile * gm);
+        r.ok = true;
+        return r;
+      }
+      before += __builtin_amdgcn_readlane(sum, 63);
+    }
+    return r;
+  }
+};
 
 // Rows of expert e (a DW workgroup knows its expert).
-__device__ inline void expert_rows(const ExpertArgs& a, int e, int& begin, int& end) {
+CBD_INLINE __device__ inline void expert_rows(const ExpertArgs& a, int e, int& begin, int& end) {
   int v = 0;
   for (int i = threadIdx.x & 63; i < e; i += 64) {
     const int x = clamped_end(a.ends, a.ends64, i, a.T);
@@ -131,23 +147,37 @@ __device__ inline void expert_rows(const ExpertArgs& a, int e, int& begin, int& 
   end = x > begin ? x : begin;
 }
 
-// Tile of workgroup b of a DW product (m_tile and n_tile in groups of 8 feature
-// tiles by all tiles of the other side, as above).
-__device__ inline ExpertTile find_weight_tile(const ExpertArgs& a, int b) {
-  ExpertTile r;
-  const int per = a.tiles_m * a.tiles_n;
-  const int t = spread_tile(b, per * a.E);
-  r.e = t / per;
-  const int local = t - r.e * per;
-  const int g = local / (8 * a.tiles_n);
-  const int gm = a.tiles_m - 8 * g < 8 ? a.tiles_m - 8 * g : 8;
-  const int in = local - g * 8 * a.tiles_n;
-  r.n_tile = in / gm;
-  r.m_tile = 8 * g + in - r.n_tile * gm;
-  r.ok = true;
-  expert_rows(a, r.e, r.begin, r.end);
-  return r;
-}
+// Tiles of a DW product: groups of 8 feature tiles by all tiles of the other
+// side, as above.
+struct WeightTiles {
+  int lo, hi, cnt;  // rows of 64 experts or fewer
+
+  CBD_INLINE __device__ void init(const ExpertArgs& a, int bn) {
+    if (a.E <= 64) expert_chunk(a, 0, bn, 0, lo, hi, cnt);
+  }
+  CBD_INLINE __device__ ExpertTile at(const ExpertArgs& a, int b, int) const {
+    ExpertTile r;
+    const int per = a.tiles_m * a.tiles_n;
+    r.ok = b < per * a.E;
+    r.e = r.begin = r.end = r.m_tile = r.n_tile = 0;
+    if (!r.ok) return r;
+    const int t = spread_tile(b, per * a.E);
+    r.e = uniform(t / per);
+    const int local = t - r.e * per;
+    const int g = local / (8 * a.tiles_n);
+    const int gm = a.tiles_m - 8 * g < 8 ? a.tiles_m - 8 * g : 8;
+    const int in = local - g * 8 * a.tiles_n;
+    r.n_tile = uniform(in / gm);
+    r.m_tile = uniform(8 * g + in - r.n_tile * gm);
+    if (a.E <= 64) {
+      r.begin = __builtin_amdgcn_readlane(lo, r.e);
+      r.end = __builtin_amdgcn_readlane(hi, r.e);
+    } else {
+      expert_rows(a, r.e, r.begin, r.end);
+    }
+    return r;
+  }
+};
 
 }  // namespace dev
 }  // namespace cbd

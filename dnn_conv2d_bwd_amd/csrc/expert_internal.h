@@ -33,6 +33,7 @@ struct ExpertArgs {
   int32_t M, N, K;   // N: DW only; K: AK and AM only
   int32_t ends64;    // ends holds 64-bit integers
   int32_t accumulate;
+  int32_t whole_out;  // rows of out are 16-byte chunks on 16-byte boundaries
   int32_t tiles_m, tiles_n;
 };
 

@@ -149,7 +149,9 @@ __global__ __launch_bounds__(THREADS) void expert_generic_kernel(const ExpertArg
   TO* out;
   int m0, K, mrows, nrows;
   if constexpr (FORM == EXPERT_DW) {
-    const dev::ExpertTile t = dev::find_weight_tile(a, blockIdx.x);
+    dev::WeightTiles tiles;
+    tiles.init(a, BT);
+    const dev::ExpertTile t = tiles.at(a, blockIdx.x, BT);
     K = t.end - t.begin;
     if (a.accumulate && K == 0) return;
     m0 = t.m_tile * BT;
@@ -160,7 +162,9 @@ __global__ __launch_bounds__(THREADS) void expert_generic_kernel(const ExpertArg
     ob.p = (const T*)a.b + (int64_t)t.begin * a.ldb + n0;
     out = (TO*)a.out + t.e * a.o_expert + n0 * a.ldo + m0;
   } else {
-    const dev::ExpertTile t = dev::find_row_tile(a, blockIdx.x, BT);
+    dev::RowTiles tiles;
+    tiles.init(a, BT);
+    const dev::ExpertTile t = tiles.at(a, blockIdx.x, BT);
     if (!t.ok) return;
     K = t.e < a.E ? a.K : 0;  // rows past the last expert's: zeros
     const int n0 = t.begin + t.n_tile * BT;

@@ -1,23 +1,32 @@
 // kern_expert_mfma.hip -- bf16 expert products with many rows, on
 // v_mfma_f32_32x32x16_bf16.
 //
-// A workgroup of 4 waves computes 256 features (m, the contiguous side of the
-// output) x 32 * NB rows (n) of one expert in steps of 32 k; wave w owns
-// features 64 w .. 64 w + 63 of all rows, so a tile that the expert's rows do
-// not fill costs matrix time only for the 32-row blocks it has (rounded up to
-// an even number), the same for every wave, and a wave's results leave through
-// a staging buffer of its own without a barrier.
+// A workgroup of 4 waves (2 x 2) computes 64 * MB features (m, the contiguous
+// side of the output) x 64 * NB rows (n) of one expert in steps of 64 k.  Waves
+// own half the features each and take turns in the 32-row blocks, so a tile
+// that the expert's rows do not fill costs matrix time only for the 64 rows it
+// has begun, the same for every wave; and a wave's results leave through a
+// staging buffer of its own without a barrier.
 //
-// Operand tiles go into a ring of NS LDS stages.  DMA: buffer_load ... lds,
-// 16 bytes a lane, NS - 1 steps ahead, one barrier a step; the reads of the
-// next 16 k and the loads are spread between the MFMAs.  Without DMA (rows off
-// 16-byte alignment, or a contracted length that is no multiple of 8 where k
-// is contiguous): through registers, one step ahead.  Lanes past an edge fetch
-// zeros on both operands, so nothing beyond the rows of an expert or the
-// contracted length takes part.
+// Workgroups stay: each takes tiles b, b + grid, ... and issues the first loads
+// of its next tile before it writes the results of the last one, which then
+// leave while the next tile's products run.
 //
-// A k-contiguous operand is staged [row][32 k], chunk c (16 bytes) of row r at
-// c ^ (r / 4 % 4), and read with ds_read_b128.  A feature-contiguous one is
+// Operand tiles go into two LDS stages.  DMA: buffer_load ... lds, 16 bytes a
+// lane, issued between the MFMAs of the first and last quarter of a step, one
+// barrier a step; the reads of the next 16 k are spread between the MFMAs.
+// Without DMA (rows off 16-byte alignment, or a contracted length that is no
+// multiple of 8 where k is contiguous): through registers, one step ahead.
+// Lanes past an edge fetch zeros on both operands, so nothing beyond the rows
+// of an expert or the contracted length takes part.
+//
+// A step is 64 k, since a k-contiguous row is then fetched in whole 128-byte
+// lines: with 32 k (64 bytes) the L2s' requests, one a clock and channel, take
+// as long as the MFMAs (256 x 256 tile: 16384 per step and XCD over 16
+// channels = 1024 clocks).
+//
+// A k-contiguous operand is staged [row][64 k], chunk c (16 bytes) of row r at
+// c ^ (r / 2 % 8), and read with ds_read_b128.  A feature-contiguous one is
 // staged [k][features] and read with ds_read_b64_tr_b16, which hands lane j of
 // 16 the four k of feature j; its chunks are moved by 64 bytes a row so that
 // the four k rows of a read sit in different banks.
@@ -40,32 +49,43 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
 
-constexpr int BM = 256;
-constexpr int BK = 32;
+constexpr int BK = 64;
+constexpr int STEPS = BK / 16;  // MFMA steps
 constexpr int THREADS = 256;
 
-// s_waitcnt immediate: vmcnt <= n, lgkmcnt 0 (gfx9 encoding).
-constexpr int waitcnt_vm_lgkm0(int n) { return (n & 15) | (7 << 4) | ((n >> 4) << 14); }
+// s_waitcnt immediate: vmcnt <= n (at most 63), lgkmcnt 0 (gfx9 encoding).
+constexpr int waitcnt_vm_lgkm0(int n) {
+  n = n > 63 ? 63 : n;
+  return (n & 15) | (7 << 4) | ((n >> 4) << 14);
+}
 
-// One operand: F features (or rows) by 32 k a stage.
-template <bool KC, int F, bool DMA>
+// The thread's index, opaque: what is computed from it once a tile is not kept
+// in registers through the main loop.
+__device__ inline int fresh_tid() {
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
+
+// One operand: F features (or rows) by 64 k a stage; the 32-row blocks that a
+// wave reads are EVERY blocks apart.
+template <bool KC, int F, int EVERY, bool DMA>
 struct Feed {
   static constexpr int BYTES = F * BK * 2;
   static constexpr int N = BYTES / 4096;  // 1 KiB blocks a wave fills
   static constexpr int CHUNKS = F / 8;    // 16-byte chunks of a k row (feature-contiguous)
 
   __device__ static int swz(int row) {
-    if (KC) return (row >> 2) & 3;
-    return F == 64 ? 4 * ((row >> 1) & 1) : 4 * (row & 3);
+    return KC ? (row >> 1) & 7 : 4 * (row & 3);
   }
   // Row (KC: of features; else of k) and chunk that a lane fills of block i.
-  __device__ static int fill_row(int i) {
-    const int lane = threadIdx.x & 63, j = N * (int)(threadIdx.x >> 6) + i;
-    return KC ? 16 * j + (lane >> 2) : (64 / CHUNKS) * j + lane / CHUNKS;
+  CBD_INLINE __device__ static int fill_row(int i, int tid) {
+    const int lane = tid & 63, j = N * (tid >> 6) + i;
+    return KC ? 8 * j + (lane >> 3) : (64 / CHUNKS) * j + lane / CHUNKS;
   }
-  __device__ static int fill_chunk(int i) {
-    const int lane = threadIdx.x & 63;
-    return (KC ? lane & 3 : lane % CHUNKS) ^ swz(fill_row(i));
+  CBD_INLINE __device__ static int fill_chunk(int i, int tid) {
+    const int lane = tid & 63;
+    return (KC ? lane & 7 : lane % CHUNKS) ^ swz(fill_row(i, tid));
   }
 
   const uint16_t* p;  // element (row 0, k 0)
@@ -79,19 +99,20 @@ struct Feed {
   // registers
   u32x4 v[N];
 
-  __device__ void init(const uint16_t* p_, int64_t ld_, int rows_, int K_) {
+  CBD_INLINE __device__ void init(const uint16_t* p_, int64_t ld_, int rows_, int K_) {
     p = p_;
     ld = ld_;
     rows = rows_;
     K = K_;
     if constexpr (DMA) {
-      base = (uint64_t)p;
+      base = dev::uniform((uint64_t)p);
       soff = 0;
       step = (uint32_t)(BK * ld * 2);
       left = K > 0 ? ((int64_t)(K - 1) * ld + rows) * 2 : 0;
+      const int tid = fresh_tid();
 #pragma unroll
       for (int i = 0; i < N; i++) {
-        const int r = fill_row(i), c = fill_chunk(i);
+        const int r = fill_row(i, tid), c = fill_chunk(i, tid);
         voff[i] = (KC ? r < rows : 8 * c < rows) ? (uint32_t)r * (uint32_t)ld * 2u + (uint32_t)c * 16u : dev::kOOB;
       }
       if constexpr (KC) {
@@ -102,21 +123,22 @@ struct Feed {
       }
     }
   }
-  // Step t is the last and part of its 32 k are past the end.
-  __device__ void mask_tail(int t) {
+  // Step t is the last and part of its 64 k are past the end.
+  CBD_INLINE __device__ void mask_tail(int t) {
     const int over = K - t * BK;
     if (over < BK) {
+      const int tid = fresh_tid();
 #pragma unroll
       for (int i = 0; i < N; i++)
-        if (8 * fill_chunk(i) >= over) voff[i] = dev::kOOB;
+        if (8 * fill_chunk(i, tid) >= over) voff[i] = dev::kOOB;
     }
   }
-  __device__ void clamp() {
+  CBD_INLINE __device__ void clamp() {
     const int64_t l = (left + 3) & ~(int64_t)3;
     rec = left <= 0 ? 0u : l > 0x7ffffffc ? 0x7ffffffcu : (uint32_t)l;
   }
   // To step t (of steps); past the last the record count is 0.
-  __device__ void advance(int t, int steps) {
+  CBD_INLINE __device__ void advance(int t, int steps) {
     if constexpr (KC) {
       soff += BK * 2;
       if (t == steps - 1) mask_tail(t);
@@ -127,11 +149,9 @@ struct Feed {
       clamp();
     }
   }
-  __device__ void issue(int i, uint32_t m0v) const {
-    const i32x4 d = {(int)__builtin_amdgcn_readfirstlane((uint32_t)base),
-                     (int)__builtin_amdgcn_readfirstlane((uint32_t)(base >> 32) & 0xffffu),
-                     (int)__builtin_amdgcn_readfirstlane(rec), 0x00020000};
-    const uint32_t so = __builtin_amdgcn_readfirstlane(KC ? soff : 0u);
+  CBD_INLINE __device__ void issue(int i, uint32_t m0v) const {
+    const i32x4 d = {(int)(uint32_t)base, (int)((uint32_t)(base >> 32) & 0xffffu), (int)rec, 0x00020000};
+    const uint32_t so = KC ? soff : 0u;
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds\n\ts_nop 0"
@@ -140,10 +160,11 @@ struct Feed {
   }
 
   // Through registers: step t, zeros past the edges.
-  __device__ void load(int t) {
+  CBD_INLINE __device__ void load(int t) {
+    const int tid = fresh_tid();
 #pragma unroll
     for (int i = 0; i < N; i++) {
-      const int r = fill_row(i), c = fill_chunk(i);
+      const int r = fill_row(i, tid), c = fill_chunk(i, tid);
       const int row = KC ? r : t * BK + r, col = KC ? t * BK + 8 * c : 8 * c;
       const int n = row < (KC ? rows : K) ? (KC ? K : rows) - col : 0;
       const uint16_t* s = p + row * ld + col;
@@ -158,7 +179,7 @@ struct Feed {
       v[i] = x;
     }
   }
-  __device__ void stage(char* lds) const {
+  CBD_INLINE __device__ void stage(char* lds) const {
 #pragma unroll
     for (int i = 0; i < N; i++)
       *(u32x4*)(lds + (N * (int)(threadIdx.x >> 6) + i) * 1024 + (threadIdx.x & 63) * 16) = v[i];
@@ -166,184 +187,307 @@ struct Feed {
 
   // ---- fragments: of 32 rows (block b from feature f0), 16 k (step ks).
   static constexpr int READS = KC ? 1 : 2;  // LDS reads a fragment takes
-  static constexpr int REGS = KC ? 2 : F >= 128 ? 4 : 2;
+  static constexpr int REGS = KC ? STEPS : 4 / EVERY;
   int at[REGS];
-  __device__ void init_reads(int f0) {
+  CBD_INLINE __device__ void init_reads(int f0) {
     const int lane = threadIdx.x & 63;
     if constexpr (KC) {
       const int row = f0 + (lane & 31);
 #pragma unroll
-      for (int ks = 0; ks < 2; ks++) at[ks] = row * 64 + (((2 * ks + (lane >> 5)) ^ swz(row)) << 4);
+      for (int ks = 0; ks < STEPS; ks++) at[ks] = row * 128 + (((2 * ks + (lane >> 5)) ^ swz(row)) << 4);
     } else {
       const int G = lane >> 4, j = lane & 15;
       const int row = 8 * (G >> 1) + (j >> 2);  // + 4 * half + 16 * ks: the same swizzle
 #pragma unroll
       for (int b = 0; b < REGS; b++) {
-        const int c = (f0 >> 3) + 4 * b + 2 * (G & 1) + ((j & 3) >> 1);
+        const int c = (f0 >> 3) + 4 * EVERY * b + 2 * (G & 1) + ((j & 3) >> 1);
         at[b] = row * (F * 2) + ((c ^ swz(row)) << 4) + ((j & 1) << 3);
       }
     }
   }
-  __device__ void read(char* lds, int b, int ks, int half, bf16x8& f) const {
+  CBD_INLINE __device__ void read(char* lds, int b, int ks, int half, bf16x8& f) const {
     if constexpr (KC) {
-      f = *(const bf16x8*)(lds + at[ks] + b * 2048);
+      f = *(const bf16x8*)(lds + at[ks] + b * (EVERY * 4096));
     } else {
-      // The swizzle changes the chunk's bits 2 and 3 (F = 64: bit 2): blocks
-      // that differ above them are a constant apart.
+      // The swizzle changes the chunk's bits 2 and 3: blocks that differ above
+      // them are a constant apart.
       const bf16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (lds_bf16x4*)((lds_char*)lds + at[b % REGS] + (b / REGS) * (REGS * 64) + (16 * ks + 4 * half) * (F * 2)));
+          (lds_bf16x4*)((lds_char*)lds + at[b % REGS] + (b / REGS) * (REGS * EVERY * 64) + (16 * ks + 4 * half) * (F * 2)));
 #pragma unroll
       for (int i = 0; i < 4; i++) f[4 * half + i] = x[i];
     }
   }
 };
 
-template <typename TO>
-__device__ inline void store_tail(TO* o, const float* v, int n, bool add) {
-#pragma unroll
-  for (int i = 0; i < 7; i++)
-    if (i < n) {
-      if constexpr (sizeof(TO) == 4)
-        o[i] = add ? o[i] + v[i] : v[i];
-      else
-        o[i] = (uint16_t)dev::bf16_rne(add ? dev::bf16_to_f32(o[i]) + v[i] : v[i]);
-    }
-}
+// How results are written: in whole 16-byte chunks on their boundaries; those
+// added to what is there; or at any alignment and width, added or not.
+enum Out { WHOLE, WHOLE_ADD, ANY };
 
-template <typename TO, int FORM, int NB, int NS, bool DMA>
-__global__ __launch_bounds__(THREADS, NB == 8 ? 1 : 2) void expert_mfma_kernel(const ExpertArgs a) {
-  constexpr int BN = 32 * NB;
-  using FeedA = Feed<FORM == EXPERT_AK, BM, DMA>;
-  using FeedB = Feed<FORM != EXPERT_DW, BN, DMA>;
-  constexpr int PER_STEP = FeedA::N + FeedB::N;
-  constexpr int BBASE = NS * FeedA::BYTES;
-  __shared__ __attribute__((aligned(1024))) char smem[NS * (FeedA::BYTES + FeedB::BYTES)];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-
-  FeedA fa;
-  FeedB fb;
-  TO* out;
-  int K, mrows, nrows;
-  if constexpr (FORM == EXPERT_DW) {
-    const dev::ExpertTile t = dev::find_weight_tile(a, blockIdx.x);
-    K = t.end - t.begin;
-    if (a.accumulate && K == 0) return;
-    const int m0 = t.m_tile * BM, n0 = t.n_tile * BN;
-    mrows = a.M - m0;
-    nrows = a.N - n0;
-    fa.init((const uint16_t*)a.a + t.begin * a.lda + m0, a.lda, mrows, K);
-    fb.init((const uint16_t*)a.b + t.begin * a.ldb + n0, a.ldb, nrows, K);
-    out = (TO*)a.out + t.e * a.o_expert + n0 * a.ldo + m0;
-  } else {
-    const dev::ExpertTile t = dev::find_row_tile(a, blockIdx.x, BN);
-    if (!t.ok) return;
-    K = t.e < a.E ? a.K : 0;  // rows past the last expert's: zeros
-    const int n0 = t.begin + t.n_tile * BN, m0 = t.m_tile * BM;
-    mrows = a.M - m0;
-    nrows = t.end - n0;
-    fa.init((const uint16_t*)a.a + (t.e < a.E ? t.e * a.a_expert : 0) + (FORM == EXPERT_AK ? m0 * a.lda : (int64_t)m0),
-            a.lda, mrows, K);
-    fb.init((const uint16_t*)a.b + n0 * a.ldb, a.ldb, nrows, K);
-    out = (TO*)a.out + n0 * a.ldo + m0;
-  }
-  fa.init_reads(64 * wave);
-  fb.init_reads(0);
-  const int KT = __builtin_amdgcn_readfirstlane((K + BK - 1) / BK);
-
-  f32x16 acc[2][NB];
-#pragma unroll
-  for (int i = 0; i < 2; i++)
-#pragma unroll
-    for (int j = 0; j < NB; j++)
-#pragma unroll
-      for (int v = 0; v < 16; v++) acc[i][j][v] = 0.f;
+template <typename TO, int FORM, int MB, int NB, bool DMA, Out OUT>
+__global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void expert_mfma_kernel(const ExpertArgs a) {
+  constexpr int BM = 64 * MB, BN = 64 * NB;
+  using FeedA = Feed<FORM == EXPERT_AK, BM, 1, DMA>;
+  using FeedB = Feed<FORM != EXPERT_DW, BN, 2, DMA>;
+  using Tiles = std::conditional_t<FORM == EXPERT_DW, dev::WeightTiles, dev::RowTiles>;
+  constexpr int BBASE = 2 * FeedA::BYTES;
+  constexpr int STAGES = BBASE + 2 * FeedB::BYTES;
+  // Results of a wave leave through SBUF buffers of 32 rows x 128 bytes.
+  constexpr int SBUF = MB == 4 ? 2 : 1;
+  __shared__ __attribute__((aligned(1024))) char smem[STAGES + 4 * SBUF * 4096];
+  // 32-feature blocks of a buffer; what is added to is staged in f32 and rounded after the sum.
+  constexpr bool F32 = sizeof(TO) == 4 || OUT == WHOLE_ADD;
+  constexpr int HM = F32 ? 1 : 2;
+  constexpr int STORES = NB * (MB / HM) * 4;    // of a wave's whole tile
+  const int wave = threadIdx.x >> 6, wm = wave & 1, wn = wave >> 1;
 
   const uint32_t smem_base = (uint32_t)(uintptr_t)(lds_char*)smem;
   const uint32_t ma = __builtin_amdgcn_readfirstlane(smem_base + (uint32_t)(wave * FeedA::N * 1024));
   const uint32_t mb = __builtin_amdgcn_readfirstlane(smem_base + (uint32_t)(BBASE + wave * FeedB::N * 1024));
-  auto issue_a = [&](int stage, int i) { fa.issue(i, ma + (uint32_t)(stage * FeedA::BYTES + i * 1024)); };
-  auto issue_b = [&](int stage, int i) { fb.issue(i, mb + (uint32_t)(stage * FeedB::BYTES + i * 1024)); };
+  FeedA fa;
+  FeedB fb;
+  fa.init_reads(32 * MB * wm);
+  fb.init_reads(32 * wn);
+  auto issue_a = [&](int stage, int i) CBD_INLINE { fa.issue(i, ma + (uint32_t)(stage * FeedA::BYTES + i * 1024)); };
+  auto issue_b = [&](int stage, int i) CBD_INLINE { fb.issue(i, mb + (uint32_t)(stage * FeedB::BYTES + i * 1024)); };
 
-  // The main loop over L of the NB row blocks.
-  auto product = [&](auto lc) {
+  // A tile: its contracted length, and where and how much it writes.
+  struct Tile {
+    TO* out;
+    int K, mrows, nrows;
+  };
+  // Points the feeds at tile t and issues its first two steps' loads.
+  auto begin = [&](const dev::ExpertTile& t) CBD_INLINE -> Tile {
+    Tile c;
+    const int m0 = t.m_tile * BM;
+    c.mrows = a.M - m0;
+    if constexpr (FORM == EXPERT_DW) {
+      const int n0 = t.n_tile * BN;
+      c.K = t.end - t.begin;
+      c.nrows = a.N - n0;
+      fa.init((const uint16_t*)a.a + t.begin * a.lda + m0, a.lda, c.mrows, c.K);
+      fb.init((const uint16_t*)a.b + t.begin * a.ldb + n0, a.ldb, c.nrows, c.K);
+      c.out = (TO*)a.out + t.e * a.o_expert + n0 * a.ldo + m0;
+    } else {
+      const int n0 = t.begin + t.n_tile * BN;
+      c.K = t.e < a.E ? a.K : 0;  // rows past the last expert's: zeros
+      c.nrows = t.end - n0;
+      fa.init((const uint16_t*)a.a + (t.e < a.E ? t.e * a.a_expert : 0) +
+                  (FORM == EXPERT_AK ? m0 * a.lda : (int64_t)m0),
+              a.lda, c.mrows, c.K);
+      fb.init((const uint16_t*)a.b + n0 * a.ldb, a.ldb, c.nrows, c.K);
+      c.out = (TO*)a.out + n0 * a.ldo + m0;
+    }
+    if constexpr (DMA) {
+      const int steps = (c.K + BK - 1) / BK;
+#pragma unroll
+      for (int s = 0; s < 2; s++) {
+#pragma unroll
+        for (int i = 0; i < FeedA::N; i++) issue_a(s, i);
+        fa.advance(s + 1, steps);
+#pragma unroll
+        for (int i = 0; i < FeedB::N; i++) issue_b(s, i);
+        fb.advance(s + 1, steps);
+      }
+    } else {
+      fa.load(0);
+      fb.load(0);
+    }
+    return c;
+  };
+
+  bool deep = false;  // a whole tile's stores were issued after this tile's first loads
+
+  // Results: HM blocks of 32 features of a 32-row block at a time through one
+  // of the wave's buffers, then 128 bytes of a row by 8 lanes.  A lane of a
+  // block holds row lane % 32, features 8 q + 4 (lane / 32) + 0..3.
+  auto finish = [&](const Tile& c, auto lc, f32x16 (&acc)[MB][decltype(lc)::value]) CBD_INLINE {
     constexpr int L = decltype(lc)::value;
-    constexpr int Q = 2 * L;                                         // MFMAs of 16 k
-    constexpr int R = 2 * FeedA::READS + L * FeedB::READS;           // fragment reads of 16 k
-    bf16x8 a0[2], a1[2], b0[L], b1[L];
-    auto read_one = [&](int stage, int ks, int r, bf16x8 (&ra)[2], bf16x8 (&rb)[L]) {
-      if (r < 2 * FeedA::READS)
-        fa.read(smem + stage * FeedA::BYTES, r / FeedA::READS, ks, r % FeedA::READS, ra[r / FeedA::READS]);
-      else {
-        const int s = r - 2 * FeedA::READS;
-        fb.read(smem + BBASE + stage * FeedB::BYTES, s / FeedB::READS, ks, s % FeedB::READS, rb[s / FeedB::READS]);
+    const int tid = fresh_tid(), lane = tid & 63;
+    const int wm = (tid >> 6) & 1, wn = tid >> 7;
+    char* const st0 = smem + STAGES + (tid >> 6) * (SBUF * 4096);
+    const auto ro = dev::rsrc(c.out, 0x7ffffffcu);
+    const int r = lane & 31, hi = lane >> 5;
+#pragma unroll
+    for (int i = 0; i < L * (MB / HM); i++) {
+      const int n = i / (MB / HM), h = i % (MB / HM);
+      const int fm = 32 * MB * wm + 32 * HM * h, rn = 64 * n + 32 * wn;
+      char* const st = st0 + (i % SBUF) * 4096;
+      // The sums stay in accumulation registers until they are converted.
+      if constexpr (MB == 4) {
+#pragma unroll
+        for (int m = 0; m < HM; m++) asm volatile("" : "+a"(acc[HM * h + m][n]));
+      }
+#pragma unroll
+      for (int m = 0; m < HM; m++)
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+          f32x4 v;
+#pragma unroll
+          for (int j = 0; j < 4; j++) v[j] = acc[HM * h + m][n][4 * q + j];
+          if (OUT == ANY && FORM == EXPERT_DW && a.accumulate && rn + r < c.nrows) {
+            const int f = fm + 32 * m + 8 * q + 4 * hi;
+            const TO* o = c.out + (rn + r) * a.ldo + f;
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+              if (f + j < c.mrows) {
+                if constexpr (sizeof(TO) == 4)
+                  v[j] += o[j];
+                else
+                  v[j] += dev::bf16_to_f32(o[j]);
+              }
+          }
+          if constexpr (F32)
+            *(f32x4*)(st + r * 128 + (((2 * q + hi) ^ (r & 7)) << 4)) = v;
+          else
+            *(u32x2*)(st + r * 128 + (((4 * m + q) ^ (r & 7)) << 4) + (hi << 3)) =
+                u32x2{dev::bf16_pack2(v[0], v[1]), dev::bf16_pack2(v[2], v[3])};
+        }
+      asm volatile("" ::: "memory");  // a wave's LDS accesses run in order
+      constexpr int PER = F32 ? 4 : 8;  // elements of a chunk
+#pragma unroll
+      for (int it = 0; it < 4; it++) {
+        const int row = 8 * it + (lane >> 3), ch = lane & 7;
+        u32x4 v = *(const u32x4*)(st + row * 128 + ((ch ^ (row & 7)) << 4));
+        const int f = fm + PER * ch;
+        if constexpr (OUT != ANY) {
+          // Past an edge: dropped.
+          const uint32_t off = rn + row < c.nrows && f < c.mrows
+                                   ? ((uint32_t)(rn + row) * (uint32_t)a.ldo + (uint32_t)f) * (uint32_t)sizeof(TO)
+                                   : dev::kOOB;
+          if constexpr (OUT == WHOLE_ADD && sizeof(TO) == 2) {
+            const u32x2 old = __builtin_amdgcn_raw_buffer_load_b64(ro, off, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b64(
+                u32x2{dev::bf16_pack2(__uint_as_float(v[0]) + dev::bf16_to_f32(old[0] & 0xffffu),
+                                      __uint_as_float(v[1]) + __uint_as_float(old[0] & 0xffff0000u)),
+                      dev::bf16_pack2(__uint_as_float(v[2]) + dev::bf16_to_f32(old[1] & 0xffffu),
+                                      __uint_as_float(v[3]) + __uint_as_float(old[1] & 0xffff0000u))},
+                ro, off, 0, 0);
+          } else {
+            if constexpr (OUT == WHOLE_ADD) {
+              const u32x4 old = __builtin_amdgcn_raw_buffer_load_b128(ro, off, 0, 0);
+#pragma unroll
+              for (int j = 0; j < 4; j++) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(old[j]));
+            }
+            __builtin_amdgcn_raw_buffer_store_b128(v, ro, off, 0, 0);
+          }
+        } else if (rn + row < c.nrows) {
+          TO* o = c.out + (rn + row) * a.ldo + f;
+          if (c.mrows - f >= PER) {
+            *(u32x4u*)o = v;
+          } else {
+#pragma unroll
+            for (int j = 0; j < PER - 1; j++)
+              if (f + j < c.mrows) {
+                if constexpr (sizeof(TO) == 4)
+                  o[j] = __uint_as_float(v[j]);
+                else
+                  o[j] = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
+              }
+          }
+        }
+      }
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    deep = OUT == WHOLE && L == NB;
+  };
+
+  Tiles tiles;
+  tiles.init(a, BN);
+  int b = blockIdx.x;
+  dev::ExpertTile t = tiles.at(a, b, BN);
+  if (!t.ok) return;
+  Tile c = begin(t);
+
+  // A tile with L of the NB row blocks.
+  auto product = [&](auto lc, int KT) CBD_INLINE {
+    f32x16 acc[MB][decltype(lc)::value];
+    constexpr int L = decltype(lc)::value;
+    constexpr int RA = FeedA::READS, RB = FeedB::READS;
+    constexpr int Q = MB * L;            // MFMAs of 16 k
+    constexpr int R = MB * RA + L * RB;  // fragment reads of 16 k
+    // The reads end some MFMAs before the wait that follows them.
+    constexpr int RQ = Q >= 8 ? Q - 4 : Q > 1 ? Q - 1 : 1;
+    bf16x8 a0[MB], a1[MB], b0[L], b1[L];
+    const f32x16 zero = {};
+    auto read_one = [&](int stage, int ks, int r, bf16x8 (&ra)[MB], bf16x8 (&rb)[L]) CBD_INLINE {
+      // In the order of use: A block 0, B block 0, the other A, the other B.
+      if (r < RA || (r >= RA + RB && r < MB * RA + RB)) {
+        const int i = r < RA ? r : r - RB;
+        fa.read(smem + stage * FeedA::BYTES, i / RA, ks, i % RA, ra[i / RA]);
+      } else {
+        const int i = r < RA + RB ? r - RA : r - MB * RA;
+        fb.read(smem + BBASE + stage * FeedB::BYTES, i / RB, ks, i % RB, rb[i / RB]);
       }
     };
     if constexpr (DMA) {
       // 16 k: MFMAs on (xa, xb), reading (ya, yb) of the next 16 k and
       // issuing an operand's loads in between.  The order is pinned: a wave
       // issues an instruction every four clocks at most, and an MFMA takes 32.
-      auto half = [&](const bf16x8 (&xa)[2], const bf16x8 (&xb)[L], int stage, int ks, bf16x8 (&ya)[2],
-                      bf16x8 (&yb)[L], int loads, auto&& load, auto&& step) {
+      auto part = [&](auto firstc, const bf16x8 (&xa)[MB], const bf16x8 (&xb)[L], int stage, int ks,
+                      bf16x8 (&ya)[MB], bf16x8 (&yb)[L], auto nc, auto&& load) CBD_INLINE {
+        constexpr int LOADS = decltype(nc)::value;
 #pragma unroll
         for (int q = 0; q < Q; q++) {
-          const int n = q >> 1, m = (n & 1) ? 1 - (q & 1) : q & 1;
-          acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[m], xb[n], acc[m][n], 0, 0, 0);
+          const int n = q / MB, m = (n & 1) ? MB - 1 - q % MB : q % MB;
+          acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[m], xb[n], firstc.value ? zero : acc[m][n], 0, 0, 0);
 #pragma unroll
-          for (int r = q * R / Q; r < (q + 1) * R / Q; r++) read_one(stage, ks, r, ya, yb);
+          for (int r = q * R / RQ; r < (q + 1) * R / RQ && r < R; r++) read_one(stage, ks, r, ya, yb);
 #pragma unroll
-          for (int i = q * loads / Q; i < (q + 1) * loads / Q; i++) load(i);
-          if (q == Q - 1) step();
+          for (int i = q * LOADS / Q; i < (q + 1) * LOADS / Q; i++) load(i);
           __builtin_amdgcn_sched_barrier(0);
         }
       };
-      // Step kt: during its first 16 k the rows of step kt + NS - 1 are
-      // loaded; then, once step kt + 1 has landed and every wave has read
-      // step kt's second 16 k (barrier), its stage takes step kt + NS's
-      // features.  Ahead of the loop: steps 0 .. NS - 2 and the features of
-      // step NS - 1.
-#pragma unroll
-      for (int s = 0; s < NS; s++) {
-#pragma unroll
-        for (int i = 0; i < FeedA::N; i++) issue_a(s, i);
-        fa.advance(s + 1, KT);
-        if (s < NS - 1) {
-#pragma unroll
-          for (int i = 0; i < FeedB::N; i++) issue_b(s, i);
-          fb.advance(s + 1, KT);
-        }
-      }
-      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0((NS - 2) * PER_STEP + FeedA::N));
+      constexpr std::integral_constant<int, 0> none{};
+      constexpr std::integral_constant<int, FeedA::N> all_a{};
+      constexpr int AHEAD = FeedA::N + FeedB::N;  // step 1's loads
+      if (deep)
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(AHEAD + STORES));
+      else
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(AHEAD));
       __builtin_amdgcn_s_barrier();
 #pragma unroll
       for (int r = 0; r < R; r++) read_one(0, 0, r, a0, b0);
-      auto iter = [&](int kt, auto sc) {
+      // Step kt, in stage S: its first quarter loads the rows of step kt + 1
+      // (step 1's came with the tile's first loads).  Before its last
+      // quarter, step kt + 1 has landed and every wave has read the rest of
+      // stage S (barrier); the last quarter loads the features of step kt + 2
+      // into it.  Loads past the last step fetch zeros (a record count of 0);
+      // the next tile's first loads follow them in order.
+      auto iter = [&](int kt, auto sc, auto firstc) CBD_INLINE {
         constexpr int S = decltype(sc)::value;
-        half(a0, b0, S, 1, a1, b1, FeedB::N, [&](int i) { issue_b((S + NS - 1) % NS, i); },
-             [&]() { fb.advance(kt + NS, KT); });
-        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0((NS - 2) * PER_STEP));
+        constexpr bool FIRST = decltype(firstc)::value;
+        part(firstc, a0, b0, S, 1, a1, b1, std::integral_constant<int, FIRST ? 0 : FeedB::N>(),
+             [&](int i) { issue_b(1 - S, i); });
+        if (!FIRST) fb.advance(kt + 2, KT);
+        part(std::false_type(), a1, b1, S, 2, a0, b0, none, [](int) {});
+        part(std::false_type(), a0, b0, S, 3, a1, b1, none, [](int) {});
+        if (FIRST && deep)
+          __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(STORES));
+        else
+          __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
         __builtin_amdgcn_s_barrier();
-        half(a1, b1, (S + 1) % NS, 0, a0, b0, FeedA::N, [&](int i) { issue_a(S, i); },
-             [&]() { fa.advance(kt + NS + 1, KT); });
+        part(std::false_type(), a1, b1, 1 - S, 0, a0, b0, all_a, [&](int i) { issue_a(S, i); });
+        fa.advance(kt + 3, KT);
       };
+      iter(0, std::integral_constant<int, 0>(), std::true_type());
 #pragma unroll 1
-      for (int kt = 0; kt < KT; kt += NS) {
-        iter(kt, std::integral_constant<int, 0>());
-        if (kt + 1 < KT) iter(kt + 1, std::integral_constant<int, 1>());
-        if (kt + 2 < KT) iter(kt + 2, std::integral_constant<int, 2>());
-        if constexpr (NS > 3)
-          if (kt + 3 < KT) iter(kt + 3, std::integral_constant<int, 3>());
+      for (int kt = 1; kt < KT; kt += 2) {
+        iter(kt, std::integral_constant<int, 1>(), std::false_type());
+        if (kt + 1 < KT) iter(kt + 1, std::integral_constant<int, 0>(), std::false_type());
       }
-      // Loads past the last step (zeros) land before the stages are reused.
-      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
-      __syncthreads();
     } else {
-      fa.load(0);
-      fb.load(0);
+#pragma unroll
+      for (int m = 0; m < MB; m++)
+#pragma unroll
+        for (int n = 0; n < L; n++) acc[m][n] = zero;
+      // Everyone has read the stages of the last tile.
+      __syncthreads();
       fa.stage(smem);
       fb.stage(smem + BBASE);
       fa.load(1);
       fb.load(1);
-      auto iter = [&](int kt, auto sc) {
+      auto iter = [&](int kt, auto sc) CBD_INLINE {
         constexpr int S = decltype(sc)::value;
         // Stage S is filled, and everyone has read stage 1 - S.
         __syncthreads();
@@ -352,147 +496,83 @@ __global__ __launch_bounds__(THREADS, NB == 8 ? 1 : 2) void expert_mfma_kernel(c
         fa.load(kt + 2);
         fb.load(kt + 2);
 #pragma unroll
-        for (int r = 0; r < R; r++) read_one(S, 0, r, a0, b0);
+        for (int ks = 0; ks < STEPS; ks++) {
 #pragma unroll
-        for (int r = 0; r < R; r++) read_one(S, 1, r, a1, b1);
+          for (int r = 0; r < R; r++) read_one(S, ks, r, a0, b0);
 #pragma unroll
-        for (int q = 0; q < Q; q++)
-          acc[q & 1][q >> 1] =
-              __builtin_amdgcn_mfma_f32_32x32x16_bf16(a0[q & 1], b0[q >> 1], acc[q & 1][q >> 1], 0, 0, 0);
-#pragma unroll
-        for (int q = 0; q < Q; q++)
-          acc[q & 1][q >> 1] =
-              __builtin_amdgcn_mfma_f32_32x32x16_bf16(a1[q & 1], b1[q >> 1], acc[q & 1][q >> 1], 0, 0, 0);
+          for (int q = 0; q < Q; q++)
+            acc[q % MB][q / MB] =
+                __builtin_amdgcn_mfma_f32_32x32x16_bf16(a0[q % MB], b0[q / MB], acc[q % MB][q / MB], 0, 0, 0);
+        }
       };
 #pragma unroll 1
       for (int kt = 0; kt < KT; kt += 2) {
         iter(kt, std::integral_constant<int, 0>());
         if (kt + 1 < KT) iter(kt + 1, std::integral_constant<int, 1>());
       }
-      __syncthreads();
+    }
+    const Tile done = c;
+    if (t.ok) c = begin(t);
+    finish(done, lc, acc);
+  };
+  // Zeros, where nothing is contracted (added: nothing to do).
+  auto blank = [&]() CBD_INLINE {
+    // The tile's loads (zeros) land before its stages' next ones.
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+    const Tile done = c;
+    if (t.ok) c = begin(t);
+    deep = false;
+    if (OUT == WHOLE_ADD || (OUT == ANY && a.accumulate)) return;
+    constexpr int PER = 16 / sizeof(TO), ROWS = THREADS / (BM / PER);
+    const int tid = fresh_tid(), f = PER * (tid % (BM / PER));
+#pragma unroll 1
+    for (int row = tid / (BM / PER); row < BN && row < done.nrows; row += ROWS) {
+      TO* o = done.out + row * a.ldo + f;
+      if (done.mrows - f >= PER) {
+        *(u32x4u*)o = u32x4{0u, 0u, 0u, 0u};
+      } else {
+#pragma unroll 1
+        for (int j = 0; f + j < done.mrows; j++) o[j] = TO(0);
+      }
     }
   };
-  if (KT > 0) {
-    if (NB <= 2 || nrows > 32 * (NB - 2)) {
-      product(std::integral_constant<int, NB>());
-    } else if (NB <= 4 || nrows > 32 * (NB - 4)) {
-      product(std::integral_constant<int, (NB > 2 ? NB - 2 : NB)>());
-    } else if (nrows > 64) {
-      product(std::integral_constant<int, (NB > 4 ? 4 : NB)>());
-    } else {
-      product(std::integral_constant<int, 2>());
-    }
-  }
 
-  // ---- results: block n of a wave (32 rows x 64 features) through its own
-  // staging buffer, then 128 bytes (f32: 256) of a row by 8 (16) lanes.  dW is
-  // staged in f32, since a value that is accumulated is rounded after the sum.
-  // A lane holds row lane % 32, features 32 m + 8 q + 4 (lane / 32) + 0..3.
-  constexpr bool WIDE = FORM == EXPERT_DW;
-  constexpr int SROW = WIDE ? 256 : 128;
-  constexpr int SBUF = WIDE ? 1 : 2;
-  static_assert(4 * 32 * SROW * SBUF <= (int)sizeof(smem), "staging fits the stages");
-  const int fm = 64 * wave;
-  if (fm >= mrows) return;
-  char* const st0 = smem + wave * (SBUF * 32 * SROW);
-#pragma unroll
-  for (int n = 0; n < NB; n++) {
-    if (32 * n >= nrows) break;
-    char* const st = st0 + (n % SBUF) * (32 * SROW);
-    const int r = lane & 31;
-#pragma unroll
-    for (int m = 0; m < 2; m++)
-#pragma unroll
-      for (int q = 0; q < 4; q++) {
-        const f32x16& c = acc[m][n];
-        if constexpr (WIDE) {
-          const int chunk = 8 * m + 2 * q + (lane >> 5);
-          *(f32x4*)(st + r * SROW + ((chunk ^ (r & 15)) << 4)) =
-              f32x4{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
-        } else {
-          const int chunk = 4 * m + q;
-          *(u32x2*)(st + r * SROW + ((chunk ^ (r & 7)) << 4) + ((lane >> 5) << 3)) =
-              u32x2{dev::bf16_pack2(c[4 * q], c[4 * q + 1]), dev::bf16_pack2(c[4 * q + 2], c[4 * q + 3])};
-        }
-      }
-    asm volatile("" ::: "memory");  // a wave's LDS accesses run in order
-    if constexpr (!WIDE) {
-#pragma unroll
-      for (int it = 0; it < 4; it++) {
-        const int row = 8 * it + (lane >> 3), c = lane & 7;
-        const u32x4 v = *(const u32x4*)(st + row * SROW + ((c ^ (row & 7)) << 4));
-        const int left = mrows - fm - 8 * c;
-        if (32 * n + row < nrows) {
-          uint16_t* o = (uint16_t*)out + (32 * n + row) * a.ldo + fm + 8 * c;
-          if (left >= 8) {
-            *(u32x4u*)o = v;
-          } else {
-#pragma unroll
-            for (int i = 0; i < 7; i++)
-              if (i < left) o[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
-          }
-        }
-      }
-    } else if constexpr (sizeof(TO) == 4) {
-#pragma unroll
-      for (int it = 0; it < 8; it++) {
-        const int row = 4 * it + (lane >> 4), c = lane & 15;
-        f32x4 v = *(const f32x4*)(st + row * SROW + ((c ^ (row & 15)) << 4));
-        const int left = mrows - fm - 4 * c;
-        if (32 * n + row < nrows) {
-          float* o = (float*)out + (32 * n + row) * a.ldo + fm + 4 * c;
-          if (left >= 4) {
-            if (a.accumulate) v += *(const f32x4u*)o;
-            *(f32x4u*)o = v;
-          } else {
-            store_tail(o, (const float*)&v, left, a.accumulate);
-          }
-        }
-      }
-    } else {
-#pragma unroll
-      for (int it = 0; it < 4; it++) {
-        const int row = 8 * it + (lane >> 3), c = lane & 7;
-        float v[8];
-        *(f32x4*)v = *(const f32x4*)(st + row * SROW + (((2 * c) ^ (row & 15)) << 4));
-        *(f32x4*)(v + 4) = *(const f32x4*)(st + row * SROW + (((2 * c + 1) ^ (row & 15)) << 4));
-        const int left = mrows - fm - 8 * c;
-        if (32 * n + row < nrows) {
-          uint16_t* o = (uint16_t*)out + (32 * n + row) * a.ldo + fm + 8 * c;
-          if (left >= 8) {
-            if (a.accumulate) {
-              const u32x4 old = *(const u32x4u*)o;
-#pragma unroll
-              for (int i = 0; i < 8; i++) v[i] += dev::bf16_to_f32((old[i >> 1] >> (16 * (i & 1))) & 0xffffu);
-            }
-            *(u32x4u*)o = u32x4{dev::bf16_pack2(v[0], v[1]), dev::bf16_pack2(v[2], v[3]),
-                                dev::bf16_pack2(v[4], v[5]), dev::bf16_pack2(v[6], v[7])};
-          } else {
-            store_tail(o, v, left, a.accumulate);
-          }
-        }
-      }
-    }
-    asm volatile("" ::: "memory");
-  }
+  do {
+    b += gridDim.x;
+    t = tiles.at(a, b, BN);
+    const int KT = __builtin_amdgcn_readfirstlane((c.K + BK - 1) / BK);
+    if (KT == 0)
+      blank();
+    else if (c.nrows > 64 * (NB - 1))
+      product(std::integral_constant<int, NB>(), KT);
+    else if (NB <= 2 || c.nrows <= 64)
+      product(std::integral_constant<int, 1>(), KT);
+    else if (c.nrows <= 128)
+      product(std::integral_constant<int, (NB > 1 ? 2 : 1)>(), KT);
+    else
+      product(std::integral_constant<int, (NB > 1 ? NB - 1 : 1)>(), KT);
+  } while (t.ok);
 }
 
 template <typename TO, int FORM>
-const void* pick(int bn, bool dma) {
-  if (bn == 256)
-    return dma ? (const void*)&expert_mfma_kernel<TO, FORM, 8, 4, true>
-               : (const void*)&expert_mfma_kernel<TO, FORM, 8, 2, false>;
-  return dma ? (const void*)&expert_mfma_kernel<TO, FORM, 4, 3, true>
-             : (const void*)&expert_mfma_kernel<TO, FORM, 4, 2, false>;
+const void* pick(const ExpertArgs& a, const ExpertLaunch& l) {
+  if (l.bn == 256) {  // with dma and whole_out
+    if constexpr (FORM == EXPERT_DW)
+      if (a.accumulate) return (const void*)&expert_mfma_kernel<TO, FORM, 4, 4, true, WHOLE_ADD>;
+    return (const void*)&expert_mfma_kernel<TO, FORM, 4, 4, true, WHOLE>;
+  }
+  if (l.dma && a.whole_out && !a.accumulate) return (const void*)&expert_mfma_kernel<TO, FORM, 2, 2, true, WHOLE>;
+  return l.dma ? (const void*)&expert_mfma_kernel<TO, FORM, 2, 2, true, ANY>
+               : (const void*)&expert_mfma_kernel<TO, FORM, 2, 2, false, ANY>;
 }
 
 }  // namespace
 
 int launch_expert_mfma(const ExpertArgs& a, const ExpertLaunch& l, void* stream) {
-  const void* k = l.form == EXPERT_AK   ? pick<uint16_t, EXPERT_AK>(l.bn, l.dma)
-                  : l.form == EXPERT_AM ? pick<uint16_t, EXPERT_AM>(l.bn, l.dma)
-                  : l.out_dtype == CBD_F32 ? pick<float, EXPERT_DW>(l.bn, l.dma)
-                                           : pick<uint16_t, EXPERT_DW>(l.bn, l.dma);
+  const void* k = l.form == EXPERT_AK   ? pick<uint16_t, EXPERT_AK>(a, l)
+                  : l.form == EXPERT_AM ? pick<uint16_t, EXPERT_AM>(a, l)
+                  : l.out_dtype == CBD_F32 ? pick<float, EXPERT_DW>(a, l)
+                                           : pick<uint16_t, EXPERT_DW>(a, l);
   void* args[] = {const_cast<ExpertArgs*>(&a)};
   return (int)hipLaunchKernel(k, dim3((unsigned)l.grid), dim3(THREADS), args, 0, (hipStream_t)stream);
 }
