@@ -338,7 +338,7 @@ def conv2d_bwd_data(dy, w, input_size, stride=1, padding=0, dilation=1, groups=1
     return dx
 
 
-from .experts import (ECK, EKC, EXPERT_KERNEL_AUTO, EXPERT_KERNEL_GENERIC, EXPERT_KERNEL_MFMA,  # noqa: E402,F401
+from .experts import (ECK, EKC, EXPERT_KERNEL_AUTO, EXPERT_KERNEL_GENERIC, EXPERT_KERNEL_MFMA, EXPERT_KERNEL_STREAM,  # noqa: E402,F401
                       EXPERT_KERNEL_NAMES, BWD_DATA, BWD_WEIGHT, FORWARD, ExpertInfo, ExpertOptions,
                       ExpertPlan, ExpertProblem, ExpertStrides, expert_bwd_data, expert_bwd_weight,
                       expert_forward, expert_linear, expert_linear_bwd, expert_plan)

@@ -34,6 +34,7 @@ SOURCES = [
     "expert_api.cpp",
     "kern_expert_generic.hip",
     "kern_expert_mfma.hip",
+    "kern_expert_stream.hip",
     "grad_api.cpp",
     "kern_grad_norm.hip",
 ]

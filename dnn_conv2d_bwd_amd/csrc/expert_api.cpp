@@ -49,10 +49,10 @@ bool share(const Block& a, const Block& b) {
 
 constexpr int64_t kMaxSlice = int64_t(1) << 31;  // bytes: offsets within a slice or tile are 32-bit
 
-// Launch of an operator.  `dma`: both inputs start every row on a 16-byte
-// boundary and (256 rows of W) stay within 32-bit
-// offsets; `whole_out`: so does the output, in 16-byte multiples.
-ExpertLaunch choose(const cbd_expert_plan_s& plan, int op, bool dma, bool whole_out) {
+// Launch of an operator.  narrow_strides: 256 rows of either input stay within
+// 32-bit offsets; dma: and both start every row on a 16-byte boundary;
+// whole_out: the output's rows are 16-byte multiples on 16-byte boundaries.
+ExpertLaunch choose(const cbd_expert_plan_s& plan, int op, bool narrow_strides, bool dma, bool whole_out) {
   const cbd_expert_problem& p = plan.prob;
   ExpertLaunch l;
   l.dtype = p.dtype;
@@ -72,13 +72,33 @@ ExpertLaunch choose(const cbd_expert_plan_s& plan, int op, bool dma, bool whole_
     return tm * (p.tokens / bn + spans);
   };
   l.kernel = plan.opt.force_kernel;
+  // Few rows an expert: 64 experts of 2048 x 1408, stream / mfma in us at 16
+  // rows an expert 92 / 97 (AK) and 68 / 77 (AM), at 32 rows 125 / 98 and 83 / 79.
+  const bool stream_ok = op != CBD_EXPERT_BWD_WEIGHT && narrow_strides;
   if (l.kernel == CBD_EXPERT_KERNEL_AUTO)
-    l.kernel = p.dtype == CBD_BF16 ? CBD_EXPERT_KERNEL_MFMA : CBD_EXPERT_KERNEL_GENERIC;
+    l.kernel = p.dtype != CBD_BF16 ? CBD_EXPERT_KERNEL_GENERIC
+               : stream_ok && p.tokens <= (l.form == cbd::EXPERT_AK ? 16 : 24) * p.experts
+                   ? CBD_EXPERT_KERNEL_STREAM
+                   : CBD_EXPERT_KERNEL_MFMA;
+  if (l.kernel == CBD_EXPERT_KERNEL_STREAM && !stream_ok) l.kernel = CBD_EXPERT_KERNEL_MFMA;
   l.dma = 0;
+  if (l.kernel == CBD_EXPERT_KERNEL_STREAM) {
+    l.bm = l.form == cbd::EXPERT_AK ? 32 : 128;
+    l.bn = 32;
+    l.grid = grid(l.bm, l.bn);
+    return l;
+  }
   if (l.kernel == CBD_EXPERT_KERNEL_MFMA) {
     // k runs along the rows of x (dy), and of W in the AK form.
     l.dma = dma && (op == CBD_EXPERT_BWD_WEIGHT || n % 8 == 0);
-    l.bm = l.bn = l.dma && whole_out && grid(256, 256) >= 512 ? 256 : 128;
+    // 256 x 256 tiles where they fill the card twice and, with rows an expert
+    // that vary, their last row tiles are few: 2048 -> 2048 wide, 256 rows an
+    // expert, 142 us against 169 with 128 x 128.  A last feature tile that is
+    // at most half used takes more rows to be worth it (1408 wide: 256 rows
+    // 171 / 160, 512 rows 252 / 280).
+    const bool half = (m + 127) / 128 % 2 != 0;
+    const bool many = op == CBD_EXPERT_BWD_WEIGHT || p.tokens >= (half ? 384 : 192) * p.experts;
+    l.bm = l.bn = l.dma && whole_out && many && grid(256, 256) >= 512 ? 256 : 128;
   } else {
     l.bm = l.bn = 128;
     if (grid(128, 128) < 512) l.bm = l.bn = 64;
@@ -150,10 +170,14 @@ cbd_status run(const cbd_expert_plan_t* plan, int op, const void* row_in, const 
     return (((uintptr_t)b.p | (uint64_t)(b.ld * b.es) | (uint64_t)(b.count > 1 ? b.stride * b.es : 0)) & 15u) == 0;
   };
   const bool whole_out = on16(bo) && bo.width % (16 / bo.es) == 0;
-  bool dma = true;
+  bool dma = true, narrow_strides = true;
   for (const Block* b : {&bx, &by, &bw})
-    if (b != &bo) dma = dma && on16(*b) && b->ld * 256 * b->es < kMaxSlice;
-  const ExpertLaunch l = choose(*plan, op, dma, whole_out);
+    if (b != &bo) {
+      narrow_strides = narrow_strides && b->ld * 256 * b->es < kMaxSlice;
+      dma = dma && on16(*b);
+    }
+  dma = dma && narrow_strides;
+  const ExpertLaunch l = choose(*plan, op, narrow_strides, dma, whole_out);
   if (l.grid > INT32_MAX) return fail(CBD_ERR_UNSUPPORTED, "too many tiles for one launch");
 
   ExpertArgs a = {};
@@ -188,8 +212,9 @@ cbd_status run(const cbd_expert_plan_t* plan, int op, const void* row_in, const 
     a.ldo = bo.ld;
   }
   a.tiles_m = (a.M + l.bm - 1) / l.bm;
-  const int err = l.kernel == CBD_EXPERT_KERNEL_MFMA ? cbd::launch_expert_mfma(a, l, stream)
-                                                     : cbd::launch_expert_generic(a, l, stream);
+  const int err = l.kernel == CBD_EXPERT_KERNEL_MFMA     ? cbd::launch_expert_mfma(a, l, stream)
+                  : l.kernel == CBD_EXPERT_KERNEL_STREAM ? cbd::launch_expert_stream(a, l, stream)
+                                                         : cbd::launch_expert_generic(a, l, stream);
   if (err) {
     cbd::set_error(std::string("expert kernel launch failed: ") + cbd::hip_error_name(err));
     return CBD_ERR_HIP;
@@ -220,7 +245,7 @@ cbd_status make_plan(const cbd_expert_problem* q, const cbd_expert_options* opt,
     return fail(CBD_ERR_INVALID_ARG, "dw_dtype must be f32, or bf16 with bf16 operands");
   if (q->ends_bits != 32 && q->ends_bits != 64) return fail(CBD_ERR_INVALID_ARG, "ends_bits must be 32 or 64");
   if (opt) {
-    if (opt->force_kernel < CBD_EXPERT_KERNEL_AUTO || opt->force_kernel > CBD_EXPERT_KERNEL_MFMA)
+    if (opt->force_kernel < CBD_EXPERT_KERNEL_AUTO || opt->force_kernel > CBD_EXPERT_KERNEL_STREAM)
       return fail(CBD_ERR_INVALID_ARG, "unknown force_kernel");
     for (int32_t r : opt->reserved)
       if (r) return fail(CBD_ERR_INVALID_ARG, "reserved options must be zero");
@@ -259,7 +284,7 @@ extern "C" cbd_status cbd_expert_plan_info(const cbd_expert_plan_t* plan, int32_
     // Dense rows are 16-byte multiples when the widths are.
     const int64_t q = 16 / esize(p.dtype);
     const bool whole = p.c % q == 0 && p.k % q == 0;
-    const ExpertLaunch l = choose(*plan, op, whole, whole);
+    const ExpertLaunch l = choose(*plan, op, true, whole, whole);
     out->kernel = l.kernel;
     out->tile_m = l.bm;
     out->tile_n = l.bn;

@@ -49,6 +49,7 @@ struct ExpertLaunch {
 };
 
 int launch_expert_generic(const ExpertArgs& a, const ExpertLaunch& l, void* stream);
+int launch_expert_stream(const ExpertArgs& a, const ExpertLaunch& l, void* stream);
 int launch_expert_mfma(const ExpertArgs& a, const ExpertLaunch& l, void* stream);
 
 }  // namespace cbd

@@ -22,8 +22,8 @@ from . import BF16, F32, _check, _dtype, _lib, _torch_dtype
 
 EKC, ECK = 0, 1
 FORWARD, BWD_DATA, BWD_WEIGHT = 0, 1, 2
-EXPERT_KERNEL_AUTO, EXPERT_KERNEL_GENERIC, EXPERT_KERNEL_MFMA = -1, 0, 1
-EXPERT_KERNEL_NAMES = {0: "generic", 1: "mfma"}
+EXPERT_KERNEL_AUTO, EXPERT_KERNEL_GENERIC, EXPERT_KERNEL_MFMA, EXPERT_KERNEL_STREAM = -1, 0, 1, 2
+EXPERT_KERNEL_NAMES = {0: "generic", 1: "mfma", 2: "stream"}
 
 
 class ExpertProblem(ctypes.Structure):

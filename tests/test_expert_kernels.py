@@ -11,7 +11,7 @@ import dnn_conv2d_bwd_amd as cbd
 
 from test_experts import ALL, Call, split
 
-KERNELS = [cbd.EXPERT_KERNEL_GENERIC, cbd.EXPERT_KERNEL_MFMA]
+KERNELS = [cbd.EXPERT_KERNEL_GENERIC, cbd.EXPERT_KERNEL_MFMA, cbd.EXPERT_KERNEL_STREAM]
 NAMES = [cbd.EXPERT_KERNEL_NAMES[k] for k in KERNELS]
 
 # rows, experts, c, k: contracted lengths around one step and the ring of
