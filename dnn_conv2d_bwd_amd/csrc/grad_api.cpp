@@ -49,6 +49,7 @@ cbd_status make_plan(const int64_t* counts, const int32_t* dtypes, int32_t n, cb
     cbd::GradBatch& b = p->batches.back();
     if (chunks > (uint64_t(1) << 30)) return fail(CBD_ERR_UNSUPPORTED, "a tensor is too large");
     p->index.push_back(i);
+    p->bytes += counts[i] * esize(dtypes[i]);
     p->chunk_begin.push_back(b.chunks);
     b.n++;
     b.chunks += (uint32_t)chunks;
@@ -127,14 +128,20 @@ cbd_status run(const cbd_grad_plan_t* plan, const void* const* grads, void* cons
     a.chunks = b.chunks;
     a.first = b.first;
   };
+  const bool small = plan->batches.size() == 1 && plan->batches[0].chunks <= cbd::kGradSmallChunks &&
+                     plan->bytes <= (clip ? cbd::kGradSmallClip : cbd::kGradSmallNorm);
   for (const cbd::GradBatch& b : plan->batches) {
     fill(b);
-    if (!err) err = cbd::launch_grad_partial(a, b.grid, stream);
+    if (!err) err = small ? cbd::launch_grad_small(a, clip, stream) : cbd::launch_grad_partial(a, b.grid, stream);
   }
-  if (!clip || plan->batches.empty()) {
+  if (small) {
+    // done
+  } else if (!clip || plan->batches.empty()) {
     if (!err) err = cbd::launch_grad_finish(a, stream);
   } else {
-    for (const cbd::GradBatch& b : plan->batches) {
+    // Backwards: what the norm read last is still in the caches.
+    for (size_t j = plan->batches.size(); j-- > 0;) {
+      const cbd::GradBatch& b = plan->batches[j];
       fill(b);
       if (!err) err = cbd::launch_grad_scale(a, b.grid, stream);
     }

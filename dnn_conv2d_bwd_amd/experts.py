@@ -148,7 +148,8 @@ def _handle(stream, device):
     import torch
 
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        # The raw handle: a Stream object costs 2 us, a seventh of a small call.
+        return torch._C._cuda_getCurrentRawStream(device.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 

@@ -100,17 +100,15 @@ def _dense(t):
 def _pointers(p, tensors, name, device):
     if len(tensors) != len(p.counts):
         raise ValueError(f"{len(tensors)} {name}, the plan is for {len(p.counts)}")
-    ptrs = []
-    for t, n, dt in zip(tensors, p.counts, p._tdtypes):
-        if t.dtype != dt or t.numel() != n:
-            raise ValueError(f"{name} {len(ptrs)} has {t.numel()} elements of {t.dtype}, "
-                             f"the plan is for {n} of {dt}")
-        if t.device != device:
-            raise ValueError(f"{name} {len(ptrs)} is on {t.device}, not on the GPU {device}")
+    index = device.index
+    for i, (t, n, dt) in enumerate(zip(tensors, p.counts, p._tdtypes)):
+        if t.dtype is not dt or t.numel() != n:
+            raise ValueError(f"{name} {i} has {t.numel()} elements of {t.dtype}, the plan is for {n} of {dt}")
+        if t.get_device() != index:
+            raise ValueError(f"{name} {i} is on {t.device}, not on the GPU {device}")
         if not t.is_contiguous() and not _dense(t):
-            raise ValueError(f"{name} {len(ptrs)} is not dense in memory")
-        ptrs.append(t.data_ptr())
-    return p.list_type(*ptrs)
+            raise ValueError(f"{name} {i} is not dense in memory")
+    return p.list_type(*[t.data_ptr() for t in tensors])
 
 
 def _device(grads, norm, workspace):

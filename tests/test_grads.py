@@ -225,3 +225,20 @@ def test_python_refuses_host_tensors():
         cbd.grad_norm(cbd.grad_plan(g), g)
     with pytest.raises(ValueError, match="float32 and bfloat16"):
         cbd.grad_plan([torch.zeros(4, dtype=torch.float16)])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("total", [1000, 30_000, 33_000, 130_000, 132_000, 300_000])
+def test_around_one_workgroup(total):
+    """Sizes around which one workgroup does the whole list."""
+    for n in (1, 12, 16, 17):
+        grads = make([total // n] * n, ["bf16" if i % 4 == 3 else "f32" for i in range(n)], shift=1, seed=n)
+        want = exact_norm(grads)
+        p = cbd.grad_plan(grads)
+        check_norm(cbd.grad_norm(p, grads), want)
+        norm, outs = cbd.clip_grads(p, grads, 0.5 * want, out=True)
+        check_norm(norm, want)
+        check_scaled(outs, grads, 0.5 * want, want)
+        mine = [g.clone() for g in grads]
+        cbd.clip_grads(p, mine, 0.5 * want)
+        assert all(torch.equal(a, b) for a, b in zip(mine, outs))
