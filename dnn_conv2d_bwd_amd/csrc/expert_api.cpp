@@ -105,7 +105,8 @@ ExpertLaunch choose(const cbd_expert_plan_s& plan, int op, bool narrow_strides, 
   }
   l.grid = grid(l.bm, l.bn);
   // Workgroups that stay: one (256 x 256: its LDS) or two a compute unit.
-  if (l.kernel == CBD_EXPERT_KERNEL_MFMA) l.grid = std::min<int64_t>(l.grid, l.bm == 256 ? 256 : 512);
+  if (l.kernel == CBD_EXPERT_KERNEL_MFMA && l.grid <= INT32_MAX)
+    l.grid = std::min<int64_t>(l.grid, l.bm == 256 ? 256 : 512);
   return l;
 }
 

@@ -56,77 +56,87 @@ struct ExpertTile {
   bool ok;         // false: no such tile (the grid is an upper bound)
 };
 
-// One chunk of 64 experts (and, as expert E, the rows past the last one's):
-// this lane's row range and its number of row tiles.
-CBD_INLINE __device__ inline void expert_chunk(const ExpertArgs& a, int base, int bn, int carry_max, int& lo, int& hi,
-                                    int& cnt) {
+// One chunk of 64 experts: this lane's row range [lo, hi).  last: the end of
+// the chunk before on entry, of this one on exit.
+CBD_INLINE __device__ inline void expert_chunk(const ExpertArgs& a, int base, int& last, int& lo, int& hi) {
   const int i = base + (int)(threadIdx.x & 63);
-  int v = i < a.E ? clamped_end(a.ends, a.ends64, i, a.T) : i == a.E ? a.T : 0;
-  hi = wave_scan_max(v);
-  hi = hi > carry_max ? hi : carry_max;
-  // The previous lane's hi: wave_shr:1 (lane 0 keeps the carry).
-  lo = __builtin_amdgcn_update_dpp(carry_max, hi, 0x138, 0xf, 0xf, false);
-  cnt = i <= a.E ? (hi - lo + bn - 1) / bn : 0;
+  hi = wave_scan_max(i < a.E ? clamped_end(a.ends, a.ends64, i, a.T) : 0);
+  hi = hi > last ? hi : last;
+  // The previous lane's hi: wave_shr:1 (lane 0 keeps the last chunk's).
+  lo = __builtin_amdgcn_update_dpp(last, hi, 0x138, 0xf, 0xf, false);
+  last = __builtin_amdgcn_readlane(hi, 63);
 }
 
 // Logical tile of hardware workgroup b: XCD x (b % 8) gets tiles 32 x .. 32 x
 // + 31 of every 256, and its share of what is left, so neighbouring tiles meet
 // in one L2 while the XCDs' loads stay alike however the experts' sizes vary.
-__device__ inline int spread_tile(int b, int tiles) {
+// (Taking the tiles in descending order of their rows instead evens the
+// workgroups' loads out better, but reads the weights twice: 256 rows an
+// expert 160 -> 177 us.)
+CBD_INLINE __device__ inline int spread_tile(int b, int tiles) {
   const int full = tiles & ~255;
   if (b < full) return (b & ~255) + ((b & 7) << 5) + ((b & 255) >> 3);
   return full + logical_tile(b - full, tiles - full, tiles - full >= 64 ? 1 : 0);
 }
 
 // Row tiles (of bn rows) of an AK / AM product.  Every wave scans ends itself,
-// 64 experts a step, so no barrier is needed.  The tiles of an expert are
-// consecutive, in groups of 8 feature tiles by all row tiles; neighbouring
-// workgroups of one XCD then share both operands' panels.
+// 64 experts a step, so no barrier is needed; up to 64 experts stay in
+// registers.  The tiles of an expert are consecutive, in groups of 8 feature
+// tiles by all row tiles; neighbouring workgroups of one XCD then share both
+// operands' panels.  Rows past the last expert's come last.
 struct RowTiles {
-  int lo, hi, cnt, sum;  // the only chunk, where 63 experts or fewer make one
+  int lo, hi, n, sum;  // of this lane's expert: rows, row tiles; row tiles of all up to it
+  int total, last;     // row tiles of the experts; the last one's end
   int64_t tiles;
 
   CBD_INLINE __device__ void init(const ExpertArgs& a, int bn) {
-    int carry_max = 0, total = 0;
-    for (int ch = 0; ch <= a.E / 64; ch++) {  // E + 1 entries
-      expert_chunk(a, ch * 64, bn, carry_max, lo, hi, cnt);
-      sum = wave_scan_sum(cnt);
-      carry_max = __builtin_amdgcn_readlane(hi, 63);
+    last = total = 0;
+    for (int base = 0; base < a.E; base += 64) {
+      expert_chunk(a, base, last, lo, hi);
+      n = (hi - lo + bn - 1) / bn;
+      sum = wave_scan_sum(n);
       total += __builtin_amdgcn_readlane(sum, 63);
     }
-    tiles = (int64_t)total * a.tiles_m;
+    tiles = (int64_t)(total + (a.T - last + bn - 1) / bn) * a.tiles_m;
   }
   // Tile of hardware workgroup b.
-  CBD_INLINE __device__ ExpertTile at(const ExpertArgs& a, int b, int bn) {
+  CBD_INLINE __device__ ExpertTile at(const ExpertArgs& a, int64_t b, int bn) {
     ExpertTile r;
-    r.ok = false;
-    r.e = 0;
-    r.begin = r.end = r.m_tile = r.n_tile = 0;
-    if (b >= tiles) return r;
-    const int t = spread_tile(b, (int)tiles);
-    const int chunks = a.E / 64 + 1;
-    int before = 0, carry_max = 0;  // row tiles before this chunk
-    for (int ch = 0; ch < chunks; ch++) {
-      if (chunks > 1) {
-        expert_chunk(a, ch * 64, bn, carry_max, lo, hi, cnt);
-        sum = wave_scan_sum(cnt);
-        carry_max = __builtin_amdgcn_readlane(hi, 63);
+    r.ok = b < tiles;
+    r.e = a.E;
+    r.begin = last;
+    r.end = a.T;
+    r.m_tile = r.n_tile = 0;
+    if (!r.ok) return r;
+    const int t = spread_tile((int)b, (int)tiles);
+    if (t >= (int64_t)total * a.tiles_m) {
+      const int local = t - total * a.tiles_m;
+      r.n_tile = uniform(local / a.tiles_m);
+      r.m_tile = uniform(local - r.n_tile * a.tiles_m);
+      return r;
+    }
+    int before = 0, end = 0;  // row tiles and rows before the chunk
+    for (int base = 0; base < a.E; base += 64) {
+      if (a.E > 64) {
+        expert_chunk(a, base, end, lo, hi);
+        n = (hi - lo + bn - 1) / bn;
+        sum = wave_scan_sum(n);
       }
       const unsigned long long hit = __ballot((int64_t)(before + sum) * a.tiles_m > t);
       if (hit) {
         const int l = __builtin_ctzll(hit);
-        const int n = __builtin_amdgcn_readlane(cnt, l);
-        const int first = before + __builtin_amdgcn_readlane(sum, l) - n;
-        r.e = ch * 64 + l;
+        const int k = __builtin_amdgcn_readlane(n, l);
+        const int first = before + __builtin_amdgcn_readlane(sum, l) - k;
+        r.e = base + l;
         r.begin = __builtin_amdgcn_readlane(lo, l);
         r.end = __builtin_amdgcn_readlane(hi, l);
         const int local = t - first * a.tiles_m;
-        const int g = local / (8 * n);
+        const int g = local / (8 * k);
         const int gm = a.tiles_m - 8 * g < 8 ? a.tiles_m - 8 * g : 8;
-        const int in = local - g * 8 * n;
-        r.n_tile = uniform(in / gm);
-        r.m_tile = uniform(8 * g + in - r.n_tile * gm);
-        r.ok = true;
+        const int in = local - g * 8 * k;
+        const int row = in / gm;
+        r.n_tile = uniform(row);
+        r.m_tile = uniform(8 * g + in - row * gm);
         return r;
       }
       before += __builtin_amdgcn_readlane(sum, 63);
@@ -150,25 +160,29 @@ CBD_INLINE __device__ inline void expert_rows(const ExpertArgs& a, int e, int& b
 // Tiles of a DW product: groups of 8 feature tiles by all tiles of the other
 // side, as above.
 struct WeightTiles {
-  int lo, hi, cnt;  // rows of 64 experts or fewer
+  int lo, hi;  // rows of up to 64 experts
+  int tiles;
 
-  CBD_INLINE __device__ void init(const ExpertArgs& a, int bn) {
-    if (a.E <= 64) expert_chunk(a, 0, bn, 0, lo, hi, cnt);
+  CBD_INLINE __device__ void init(const ExpertArgs& a, int) {
+    tiles = a.tiles_m * a.tiles_n * a.E;
+    int last = 0;
+    if (a.E <= 64) expert_chunk(a, 0, last, lo, hi);
   }
-  CBD_INLINE __device__ ExpertTile at(const ExpertArgs& a, int b, int) const {
+  CBD_INLINE __device__ ExpertTile at(const ExpertArgs& a, int64_t b, int) const {
     ExpertTile r;
-    const int per = a.tiles_m * a.tiles_n;
-    r.ok = b < per * a.E;
+    r.ok = b < tiles;
     r.e = r.begin = r.end = r.m_tile = r.n_tile = 0;
     if (!r.ok) return r;
-    const int t = spread_tile(b, per * a.E);
+    const int t = spread_tile((int)b, tiles);
+    const int per = a.tiles_m * a.tiles_n;
     r.e = uniform(t / per);
     const int local = t - r.e * per;
     const int g = local / (8 * a.tiles_n);
     const int gm = a.tiles_m - 8 * g < 8 ? a.tiles_m - 8 * g : 8;
     const int in = local - g * 8 * a.tiles_n;
-    r.n_tile = uniform(in / gm);
-    r.m_tile = uniform(8 * g + in - r.n_tile * gm);
+    const int row = in / gm;
+    r.n_tile = uniform(row);
+    r.m_tile = uniform(8 * g + in - row * gm);
     if (a.E <= 64) {
       r.begin = __builtin_amdgcn_readlane(lo, r.e);
       r.end = __builtin_amdgcn_readlane(hi, r.e);

@@ -49,8 +49,6 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
 
-constexpr int BK = 64;
-constexpr int STEPS = BK / 16;  // MFMA steps
 constexpr int THREADS = 256;
 
 // s_waitcnt immediate: vmcnt <= n (at most 63), lgkmcnt 0 (gfx9 encoding).
@@ -67,25 +65,25 @@ __device__ inline int fresh_tid() {
   return t;
 }
 
-// One operand: F features (or rows) by 64 k a stage; the 32-row blocks that a
+// One operand: F features (or rows) by BK k a stage; the 32-row blocks that a
 // wave reads are EVERY blocks apart.
-template <bool KC, int F, int EVERY, bool DMA>
+template <bool KC, int F, int BK, int EVERY, bool DMA>
 struct Feed {
   static constexpr int BYTES = F * BK * 2;
   static constexpr int N = BYTES / 4096;  // 1 KiB blocks a wave fills
-  static constexpr int CHUNKS = F / 8;    // 16-byte chunks of a k row (feature-contiguous)
+  static constexpr int CHUNKS = (KC ? BK : F) / 8;  // 16-byte chunks of a row
 
   __device__ static int swz(int row) {
-    return KC ? (row >> 1) & 7 : 4 * (row & 3);
+    return KC ? (BK == 64 ? (row >> 1) & 7 : (row >> 2) & 3) : 4 * (row & 3);
   }
   // Row (KC: of features; else of k) and chunk that a lane fills of block i.
   CBD_INLINE __device__ static int fill_row(int i, int tid) {
     const int lane = tid & 63, j = N * (tid >> 6) + i;
-    return KC ? 8 * j + (lane >> 3) : (64 / CHUNKS) * j + lane / CHUNKS;
+    return (64 / CHUNKS) * j + lane / CHUNKS;
   }
   CBD_INLINE __device__ static int fill_chunk(int i, int tid) {
     const int lane = tid & 63;
-    return (KC ? lane & 7 : lane % CHUNKS) ^ swz(fill_row(i, tid));
+    return (lane % CHUNKS) ^ swz(fill_row(i, tid));
   }
 
   const uint16_t* p;  // element (row 0, k 0)
@@ -123,7 +121,7 @@ struct Feed {
       }
     }
   }
-  // Step t is the last and part of its 64 k are past the end.
+  // Step t is the last and part of its k are past the end.
   CBD_INLINE __device__ void mask_tail(int t) {
     const int over = K - t * BK;
     if (over < BK) {
@@ -187,14 +185,14 @@ struct Feed {
 
   // ---- fragments: of 32 rows (block b from feature f0), 16 k (step ks).
   static constexpr int READS = KC ? 1 : 2;  // LDS reads a fragment takes
-  static constexpr int REGS = KC ? STEPS : 4 / EVERY;
+  static constexpr int REGS = KC ? BK / 16 : 4 / EVERY;
   int at[REGS];
   CBD_INLINE __device__ void init_reads(int f0) {
     const int lane = threadIdx.x & 63;
     if constexpr (KC) {
       const int row = f0 + (lane & 31);
 #pragma unroll
-      for (int ks = 0; ks < STEPS; ks++) at[ks] = row * 128 + (((2 * ks + (lane >> 5)) ^ swz(row)) << 4);
+      for (int ks = 0; ks < BK / 16; ks++) at[ks] = row * (BK * 2) + (((2 * ks + (lane >> 5)) ^ swz(row)) << 4);
     } else {
       const int G = lane >> 4, j = lane & 15;
       const int row = 8 * (G >> 1) + (j >> 2);  // + 4 * half + 16 * ks: the same swizzle
@@ -207,7 +205,7 @@ struct Feed {
   }
   CBD_INLINE __device__ void read(char* lds, int b, int ks, int half, bf16x8& f) const {
     if constexpr (KC) {
-      f = *(const bf16x8*)(lds + at[ks] + b * (EVERY * 4096));
+      f = *(const bf16x8*)(lds + at[ks] + b * (EVERY * 64 * BK));
     } else {
       // The swizzle changes the chunk's bits 2 and 3: blocks that differ above
       // them are a constant apart.
@@ -226,11 +224,13 @@ enum Out { WHOLE, WHOLE_ADD, ANY };
 template <typename TO, int FORM, int MB, int NB, bool DMA, Out OUT>
 __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void expert_mfma_kernel(const ExpertArgs a) {
   constexpr int BM = 64 * MB, BN = 64 * NB;
-  using FeedA = Feed<FORM == EXPERT_AK, BM, 1, DMA>;
-  using FeedB = Feed<FORM != EXPERT_DW, BN, 2, DMA>;
+  // Two stages of 64 k, or four of 32.
+  constexpr int BK = FORM != EXPERT_DW ? 64 : 32, NS = 128 / BK;
+  using FeedA = Feed<FORM == EXPERT_AK, BM, BK, 1, DMA>;
+  using FeedB = Feed<FORM != EXPERT_DW, BN, BK, 2, DMA>;
   using Tiles = std::conditional_t<FORM == EXPERT_DW, dev::WeightTiles, dev::RowTiles>;
-  constexpr int BBASE = 2 * FeedA::BYTES;
-  constexpr int STAGES = BBASE + 2 * FeedB::BYTES;
+  constexpr int BBASE = NS * FeedA::BYTES;
+  constexpr int STAGES = BBASE + NS * FeedB::BYTES;
   // Results of a wave leave through SBUF buffers of 32 rows x 128 bytes.
   constexpr int SBUF = MB == 4 ? 2 : 1;
   __shared__ __attribute__((aligned(1024))) char smem[STAGES + 4 * SBUF * 4096];
@@ -255,7 +255,8 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void expert_mfma_kernel(c
     TO* out;
     int K, mrows, nrows;
   };
-  // Points the feeds at tile t and issues its first two steps' loads.
+  // Points the feeds at tile t and issues its first loads: of NS steps, but
+  // with more than two stages not the rows of the last.
   auto begin = [&](const dev::ExpertTile& t) CBD_INLINE -> Tile {
     Tile c;
     const int m0 = t.m_tile * BM;
@@ -280,10 +281,11 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void expert_mfma_kernel(c
     if constexpr (DMA) {
       const int steps = (c.K + BK - 1) / BK;
 #pragma unroll
-      for (int s = 0; s < 2; s++) {
+      for (int s = 0; s < NS; s++) {
 #pragma unroll
         for (int i = 0; i < FeedA::N; i++) issue_a(s, i);
         fa.advance(s + 1, steps);
+        if (NS > 2 && s == NS - 1) break;
 #pragma unroll
         for (int i = 0; i < FeedB::N; i++) issue_b(s, i);
         fb.advance(s + 1, steps);
@@ -394,7 +396,7 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void expert_mfma_kernel(c
 
   Tiles tiles;
   tiles.init(a, BN);
-  int b = blockIdx.x;
+  int64_t b = blockIdx.x;
   dev::ExpertTile t = tiles.at(a, b, BN);
   if (!t.ok) return;
   Tile c = begin(t);
@@ -440,7 +442,11 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void expert_mfma_kernel(c
       };
       constexpr std::integral_constant<int, 0> none{};
       constexpr std::integral_constant<int, FeedA::N> all_a{};
-      constexpr int AHEAD = FeedA::N + FeedB::N;  // step 1's loads
+      constexpr std::integral_constant<int, NS == 2 ? 0 : FeedB::N> all_b{};
+      (void)all_b;
+      constexpr int STEP = FeedA::N + FeedB::N;  // loads of a step
+      // Step 0 has landed: of the tile's first loads, all but these are done.
+      constexpr int AHEAD = NS == 2 ? STEP : (NS - 2) * STEP + FeedA::N;
       if (deep)
         __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(AHEAD + STORES));
       else
@@ -448,33 +454,57 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void expert_mfma_kernel(c
       __builtin_amdgcn_s_barrier();
 #pragma unroll
       for (int r = 0; r < R; r++) read_one(0, 0, r, a0, b0);
-      // Step kt, in stage S: its first quarter loads the rows of step kt + 1
-      // (step 1's came with the tile's first loads).  Before its last
+      // Loads past the last step fetch zeros (a record count of 0); the next
+      // tile's first loads follow them in order.
+      //
+      // 64 k, step kt in stage S: the first quarter loads the rows of step
+      // kt + 1 (step 1's came with the tile's first loads).  Before the last
       // quarter, step kt + 1 has landed and every wave has read the rest of
       // stage S (barrier); the last quarter loads the features of step kt + 2
-      // into it.  Loads past the last step fetch zeros (a record count of 0);
-      // the next tile's first loads follow them in order.
+      // into it.
+      //
+      // 32 k: the first half loads the rows of step kt + 3; before the second,
+      // step kt + 1 has landed (two more steps are on their way) and stage S
+      // is read; the second half loads the features of step kt + 4 into it.
+      // The last tile's stores are newer than what the first two steps wait
+      // for.
       auto iter = [&](int kt, auto sc, auto firstc) CBD_INLINE {
         constexpr int S = decltype(sc)::value;
         constexpr bool FIRST = decltype(firstc)::value;
-        part(firstc, a0, b0, S, 1, a1, b1, std::integral_constant<int, FIRST ? 0 : FeedB::N>(),
-             [&](int i) { issue_b(1 - S, i); });
-        if (!FIRST) fb.advance(kt + 2, KT);
-        part(std::false_type(), a1, b1, S, 2, a0, b0, none, [](int) {});
-        part(std::false_type(), a0, b0, S, 3, a1, b1, none, [](int) {});
-        if (FIRST && deep)
-          __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(STORES));
-        else
-          __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
-        __builtin_amdgcn_s_barrier();
-        part(std::false_type(), a1, b1, 1 - S, 0, a0, b0, all_a, [&](int i) { issue_a(S, i); });
-        fa.advance(kt + 3, KT);
+        if constexpr (NS == 2) {
+          part(firstc, a0, b0, S, 1, a1, b1, std::integral_constant<int, FIRST ? 0 : FeedB::N>(),
+               [&](int i) { issue_b(1 - S, i); });
+          if (!FIRST) fb.advance(kt + 2, KT);
+          part(std::false_type(), a1, b1, S, 2, a0, b0, none, [](int) {});
+          part(std::false_type(), a0, b0, S, 3, a1, b1, none, [](int) {});
+          if (FIRST && deep)
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(STORES));
+          else
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+          __builtin_amdgcn_s_barrier();
+          part(std::false_type(), a1, b1, 1 - S, 0, a0, b0, all_a, [&](int i) { issue_a(S, i); });
+          fa.advance(kt + 3, KT);
+        } else {
+          part(firstc, a0, b0, S, 1, a1, b1, all_b, [&](int i) { issue_b((S + NS - 1) % NS, i); });
+          fb.advance(kt + NS, KT);
+          if ((FIRST || kt == 1) && deep)
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0((NS - 2) * STEP + STORES));
+          else
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0((NS - 2) * STEP));
+          __builtin_amdgcn_s_barrier();
+          part(std::false_type(), a1, b1, (S + 1) % NS, 0, a0, b0, all_a, [&](int i) { issue_a(S, i); });
+          fa.advance(kt + NS + 1, KT);
+        }
       };
       iter(0, std::integral_constant<int, 0>(), std::true_type());
 #pragma unroll 1
-      for (int kt = 1; kt < KT; kt += 2) {
+      for (int kt = 1; kt < KT; kt += NS) {
         iter(kt, std::integral_constant<int, 1>(), std::false_type());
-        if (kt + 1 < KT) iter(kt + 1, std::integral_constant<int, 0>(), std::false_type());
+        if constexpr (NS > 2) {
+          if (kt + 1 < KT) iter(kt + 1, std::integral_constant<int, 2>(), std::false_type());
+          if (kt + 2 < KT) iter(kt + 2, std::integral_constant<int, 3>(), std::false_type());
+        }
+        if (kt + NS - 1 < KT) iter(kt + NS - 1, std::integral_constant<int, 0>(), std::false_type());
       }
     } else {
 #pragma unroll
@@ -496,7 +526,7 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void expert_mfma_kernel(c
         fa.load(kt + 2);
         fb.load(kt + 2);
 #pragma unroll
-        for (int ks = 0; ks < STEPS; ks++) {
+        for (int ks = 0; ks < BK / 16; ks++) {
 #pragma unroll
           for (int r = 0; r < R; r++) read_one(S, ks, r, a0, b0);
 #pragma unroll
