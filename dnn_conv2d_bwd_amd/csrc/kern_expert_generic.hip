@@ -4,21 +4,26 @@
 // A workgroup of 4 waves (2 x 2) computes a BM x BN tile (BM = BN = 128, or 64
 // where 128 would leave compute units idle) of one expert with
 // v_mfma_f32_16x16x4_f32; bf16 operands are widened while they are staged, so
-// every product is exact and every sum f32.  Operand tiles of 16 k are loaded
-// into registers one step ahead, then written to one of two LDS buffers, so a
-// step has one barrier.  Elements off an edge of the operand -- the expert's
-// rows, the features or the contracted length -- are staged as zeros on both
-// sides, so nothing beyond an edge (infinities and NaN included) takes part.
+// every product is exact and every sum f32.  Operand tiles of 16 k (64 x 64:
+// 32 k) are loaded into registers two steps ahead, then written to one of two
+// LDS buffers, so a step has one barrier.  Each thread keeps a pointer per
+// vector that steps along k: addresses worked out anew took longer than the
+// MFMAs.  Elements past the contracted length are staged as zeros on
+// both sides; rows and features past an edge repeat others, and what they give
+// is not stored.  So nothing beyond an edge (infinities and NaN included)
+// takes part.
 //
-// k may be summed in any order as long as both operands agree: lane group
-// q = lane / 16 takes k = 4q + i at MFMA i.  A k-contiguous operand is staged
-// [row][16 k + 4 pad] and one 16-byte LDS read gives a lane its four k; an
+// k may be summed in any order as long as both operands agree: of each 16 k,
+// lane group q = lane / 16 takes k = 4q + i at MFMA i.  A k-contiguous operand
+// is staged [row][k + 4 pad] and one 16-byte LDS read gives a lane its four k; an
 // operand whose features are contiguous is staged [k][features] and one read
 // gives a lane MB neighbouring features of one k, which makes feature
 // MB * i + block, instead of 16 * block + i, the row of lane i in a block.
 //
 // Bound: the f32 matrix rate (157 TFLOP/s; a 128 x 128 tile does 32 flops per
 // loaded byte in f32).
+#include <type_traits>
+
 #include "expert_device.h"
 
 namespace cbd {
@@ -28,7 +33,6 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint16_t u16x4u __attribute__((ext_vector_type(4), aligned(2)));
 
-constexpr int BK = 16;
 constexpr int THREADS = 256;
 
 // n (clamped to 0..4) elements from p, widened to f32; zeros after them.
@@ -80,52 +84,70 @@ __device__ inline void store4(uint16_t* p, f32x4 v, int n, bool add) {
 
 // One operand of a tile: R rows (features or tokens) by 16 k, R = 32 * NB.
 // KC: k is contiguous in memory.
-template <typename T, bool KC, int NB>
+template <typename T, bool KC, int NB, int BK>
 struct Operand {
   static constexpr int R = 32 * NB;
   static constexpr int ROW = KC ? BK + 4 : R + 4;     // floats per LDS row
   static constexpr int LDS = KC ? R * ROW : BK * ROW;  // floats
   static constexpr int NV = R * BK / 4 / THREADS;      // 4-vectors per thread
-  const T* p;   // element (row 0, k 0) of the tile
-  int64_t ld;
-  int rows;     // rows inside the operand
-  f32x4 v[NV];
+  static constexpr int QUADS = KC ? BK / 4 : R / 4;  // 4-vectors of a row
+  const T* q[NV];  // this thread's vectors of the next step
+  int64_t step;
+  int feats[NV];   // feature-contiguous: features of the vector inside the operand
+  f32x4 v[2][NV];  // two steps
 
-  __device__ void load(int k0, int K) {
+  // p: element (row 0, k 0) of the tile; rows: inside the operand, >= 1.
+  CBD_INLINE __device__ void init(const T* p, int64_t ld, int rows) {
+    step = KC ? BK : BK * ld;
 #pragma unroll
     for (int i = 0; i < NV; i++) {
       const int idx = i * THREADS + (int)threadIdx.x;
+      const int row = idx / QUADS, col = 4 * (idx % QUADS);
       if (KC) {
-        const int r = idx >> 2, k = k0 + 4 * (idx & 3);
-        v[i] = load4(p + r * ld + k, r < rows ? K - k : 0);
+        q[i] = p + (row < rows ? row : rows - 1) * ld + col;
+        feats[i] = 4;
       } else {
-        const int k = k0 + idx / (R / 4), r = 4 * (idx % (R / 4));
-        v[i] = load4(p + k * ld + r, k < K ? rows - r : 0);
+        const int f = col < rows ? col : 0;
+        q[i] = p + row * ld + f;
+        feats[i] = rows - f;
       }
     }
   }
-  __device__ void stage(float* lds) const {
+  // The next step, of which `left` k are inside, into registers `slot`.
+  CBD_INLINE __device__ void load(int slot, int left) {
 #pragma unroll
     for (int i = 0; i < NV; i++) {
       const int idx = i * THREADS + (int)threadIdx.x;
-      const int at = KC ? (idx >> 2) * ROW + 4 * (idx & 3) : (idx / (R / 4)) * ROW + 4 * (idx % (R / 4));
-      *(f32x4*)(lds + at) = v[i];
+      const int k = KC ? 4 * (idx % QUADS) : idx / QUADS;
+      if (left >= BK)
+        v[slot][i] = KC ? load4(q[i], 4) : load4(q[i], feats[i]);
+      else
+        v[slot][i] = load4(q[i], KC ? left - k : k < left ? feats[i] : 0);
+      q[i] += step;
+    }
+  }
+  CBD_INLINE __device__ void stage(int slot, float* lds) const {
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+      const int idx = i * THREADS + (int)threadIdx.x;
+      *(f32x4*)(lds + (idx / QUADS) * ROW + 4 * (idx % QUADS)) = v[slot][i];
     }
   }
   // Fragments of a wave's 16 * NB rows from row r0: f[block][i].
-  __device__ static void read(const float* lds, int r0, float (&f)[NB][4]) {
+  // of k kb .. kb + 15
+  CBD_INLINE __device__ static void read(const float* lds, int r0, int kb, float (&f)[NB][4]) {
     const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
     if (KC) {
 #pragma unroll
       for (int b = 0; b < NB; b++) {
-        const f32x4 x = *(const f32x4*)(lds + (r0 + 16 * b + r) * ROW + 4 * q);
+        const f32x4 x = *(const f32x4*)(lds + (r0 + 16 * b + r) * ROW + kb + 4 * q);
 #pragma unroll
         for (int i = 0; i < 4; i++) f[b][i] = x[i];
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        const float* s = lds + (4 * q + i) * ROW + r0 + NB * r;
+        const float* s = lds + (kb + 4 * q + i) * ROW + r0 + NB * r;
 #pragma unroll
         for (int b = 0; b < NB; b++) f[b][i] = s[b];
       }
@@ -136,10 +158,11 @@ struct Operand {
 };
 
 template <typename T, typename TO, int FORM, int NB>
-__global__ __launch_bounds__(THREADS) void expert_generic_kernel(const ExpertArgs a) {
+__global__ __launch_bounds__(THREADS, NB == 4 ? 3 : 4) void expert_generic_kernel(const ExpertArgs a) {
   constexpr int BT = 32 * NB;
-  using OpA = Operand<T, FORM == EXPERT_AK, NB>;
-  using OpB = Operand<T, FORM != EXPERT_DW, NB>;
+  constexpr int BK = NB == 4 ? 16 : 32;
+  using OpA = Operand<T, FORM == EXPERT_AK, NB, BK>;
+  using OpB = Operand<T, FORM != EXPERT_DW, NB, BK>;
   __shared__ __attribute__((aligned(16))) float lds[2][OpA::LDS + OpB::LDS];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = (wave & 1) * 16 * NB, wn = (wave >> 1) * 16 * NB;
@@ -158,8 +181,8 @@ __global__ __launch_bounds__(THREADS) void expert_generic_kernel(const ExpertArg
     const int n0 = t.n_tile * BT;
     mrows = a.M - m0;
     nrows = a.N - n0;
-    oa.p = (const T*)a.a + (int64_t)t.begin * a.lda + m0;
-    ob.p = (const T*)a.b + (int64_t)t.begin * a.ldb + n0;
+    oa.init((const T*)a.a + (int64_t)t.begin * a.lda + m0, a.lda, mrows);
+    ob.init((const T*)a.b + (int64_t)t.begin * a.ldb + n0, a.ldb, nrows);
     out = (TO*)a.out + t.e * a.o_expert + n0 * a.ldo + m0;
   } else {
     dev::RowTiles tiles;
@@ -171,46 +194,54 @@ __global__ __launch_bounds__(THREADS) void expert_generic_kernel(const ExpertArg
     m0 = t.m_tile * BT;
     mrows = a.M - m0;
     nrows = t.end - n0;
-    oa.p = (const T*)a.a + (t.e < a.E ? t.e * a.a_expert : 0) + (FORM == EXPERT_AK ? m0 * a.lda : (int64_t)m0);
-    ob.p = (const T*)a.b + (int64_t)n0 * a.ldb;
+    oa.init((const T*)a.a + (t.e < a.E ? t.e * a.a_expert : 0) + (FORM == EXPERT_AK ? m0 * a.lda : (int64_t)m0),
+            a.lda, mrows);
+    ob.init((const T*)a.b + (int64_t)n0 * a.ldb, a.ldb, nrows);
     out = (TO*)a.out + (int64_t)n0 * a.ldo + m0;
   }
-  oa.ld = a.lda;
-  oa.rows = mrows;
-  ob.ld = a.ldb;
-  ob.rows = nrows;
-
+  const int live = dev::uniform((nrows - wn + 15) >> 4);  // 16-row blocks of this wave (AK, AM)
   f32x4 acc[NB][NB];
 #pragma unroll
   for (int i = 0; i < NB; i++)
 #pragma unroll
     for (int j = 0; j < NB; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  oa.load(0, K);
-  ob.load(0, K);
-  int buf = 0;
-  for (int k0 = 0; k0 < K; k0 += BK, buf ^= 1) {
-    float* la = lds[buf];
+  auto step = [&](auto sc, int k0) CBD_INLINE {
+    constexpr int S = decltype(sc)::value;
+    float* la = lds[S];
     float* lb = la + OpA::LDS;
-    oa.stage(la);
-    ob.stage(lb);
-    // One barrier a step: buffer buf was last read two steps ago, before the
+    oa.stage(S, la);
+    ob.stage(S, lb);
+    // One barrier a step: buffer S was last read two steps ago, before the
     // previous step's barrier.
     __syncthreads();
-    if (k0 + BK < K) {
-      oa.load(k0 + BK, K);
-      ob.load(k0 + BK, K);
+    oa.load(S, K - k0 - 2 * BK);
+    ob.load(S, K - k0 - 2 * BK);
+#pragma unroll
+    for (int kb = 0; kb < BK; kb += 16) {
+      float fa[NB][4], fb[NB][4];
+      OpA::read(la, wm, kb, fa);
+      OpB::read(lb, wn, kb, fb);
+#pragma unroll
+      for (int y = 0; y < NB; y++) {
+        // Whole 16-row blocks past the expert's rows are left out.
+        if (FORM != EXPERT_DW && y >= live) break;
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+          for (int x = 0; x < NB; x++)
+            acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x4f32(fa[x][i], fb[y][i], acc[x][y], 0, 0, 0);
+      }
     }
-    float fa[NB][4], fb[NB][4];
-    OpA::read(la, wm, fa);
-    OpB::read(lb, wn, fb);
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-#pragma unroll
-      for (int x = 0; x < NB; x++)
-#pragma unroll
-        for (int y = 0; y < NB; y++)
-          acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x4f32(fa[x][i], fb[y][i], acc[x][y], 0, 0, 0);
+  };
+  oa.load(0, K);
+  ob.load(0, K);
+  oa.load(1, K - BK);
+  ob.load(1, K - BK);
+#pragma unroll 1
+  for (int k0 = 0; k0 < K; k0 += 2 * BK) {
+    step(std::integral_constant<int, 0>(), k0);
+    if (k0 + BK < K) step(std::integral_constant<int, 1>(), k0 + BK);
   }
 
   // Lane: column (n) lane % 16 of a block, rows (m) 4 * (lane / 16) + r.
