@@ -53,6 +53,7 @@ struct ExpertTile {
   int e;           // expert; E for the rows past the last expert's
   int begin, end;  // its rows
   int m_tile, n_tile;
+  int half;        // 0, 1: the first or second half of its rows only; -1: all
   bool ok;         // false: no such tile (the grid is an upper bound)
 };
 
@@ -99,20 +100,31 @@ struct RowTiles {
     }
     tiles = (int64_t)(total + (a.T - last + bn - 1) / bn) * a.tiles_m;
   }
-  // Tile of hardware workgroup b.
-  CBD_INLINE __device__ ExpertTile at(const ExpertArgs& a, int64_t b, int bn) {
+  // Tile of hardware workgroup b.  g > 0: workgroups take b, b + g, ...; where
+  // the last round's tiles are at most g / 2, each is taken as two halves of
+  // its rows.
+  CBD_INLINE __device__ ExpertTile at(const ExpertArgs& a, int64_t b, int bn, int g = 0) {
     ExpertTile r;
+    r.half = -1;
+    const int64_t whole = g > 0 ? (int)tiles / g * g : tiles;  // fewer than 2^31: the caller checks
+    const int left = (int)(tiles - whole);
+    if (b >= whole && 2 * left <= g) {
+      const int p = b - whole < 2 * left ? logical_tile((int)(b - whole), 2 * left, 1) : 2 * left;
+      r.half = p & 1;
+      b = whole + (p >> 1);
+    }
     r.ok = b < tiles;
     r.e = a.E;
     r.begin = last;
     r.end = a.T;
     r.m_tile = r.n_tile = 0;
     if (!r.ok) return r;
-    const int t = spread_tile((int)b, (int)tiles);
+    const int t = r.half < 0 ? spread_tile((int)b, (int)tiles) : (int)b;
     if (t >= (int64_t)total * a.tiles_m) {
       const int local = t - total * a.tiles_m;
       r.n_tile = uniform(local / a.tiles_m);
       r.m_tile = uniform(local - r.n_tile * a.tiles_m);
+      if (r.half == 1 && r.begin + r.n_tile * bn + bn / 2 >= r.end) r.ok = false;
       return r;
     }
     int before = 0, end = 0;  // row tiles and rows before the chunk
@@ -131,12 +143,13 @@ struct RowTiles {
         r.begin = __builtin_amdgcn_readlane(lo, l);
         r.end = __builtin_amdgcn_readlane(hi, l);
         const int local = t - first * a.tiles_m;
-        const int g = local / (8 * k);
-        const int gm = a.tiles_m - 8 * g < 8 ? a.tiles_m - 8 * g : 8;
-        const int in = local - g * 8 * k;
+        const int grp = local / (8 * k);
+        const int gm = a.tiles_m - 8 * grp < 8 ? a.tiles_m - 8 * grp : 8;
+        const int in = local - grp * 8 * k;
         const int row = in / gm;
         r.n_tile = uniform(row);
-        r.m_tile = uniform(8 * g + in - row * gm);
+        r.m_tile = uniform(8 * grp + in - row * gm);
+        if (r.half == 1 && r.begin + r.n_tile * bn + bn / 2 >= r.end) r.ok = false;
         return r;
       }
       before += __builtin_amdgcn_readlane(sum, 63);
@@ -168,8 +181,9 @@ struct WeightTiles {
     int last = 0;
     if (a.E <= 64) expert_chunk(a, 0, last, lo, hi);
   }
-  CBD_INLINE __device__ ExpertTile at(const ExpertArgs& a, int64_t b, int) const {
+  CBD_INLINE __device__ ExpertTile at(const ExpertArgs& a, int64_t b, int, int) const {
     ExpertTile r;
+    r.half = -1;
     r.ok = b < tiles;
     r.e = r.begin = r.end = r.m_tile = r.n_tile = 0;
     if (!r.ok) return r;

@@ -174,7 +174,7 @@ __global__ __launch_bounds__(THREADS, NB == 4 ? 3 : 4) void expert_generic_kerne
   if constexpr (FORM == EXPERT_DW) {
     dev::WeightTiles tiles;
     tiles.init(a, BT);
-    const dev::ExpertTile t = tiles.at(a, blockIdx.x, BT);
+    const dev::ExpertTile t = tiles.at(a, blockIdx.x, BT, 0);
     K = t.end - t.begin;
     if (a.accumulate && K == 0) return;
     m0 = t.m_tile * BT;
