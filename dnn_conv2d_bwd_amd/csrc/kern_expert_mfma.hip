@@ -98,10 +98,19 @@ struct Feed {
   uint32_t soff, rec, step;
   int64_t left;       // feature-contiguous: bytes from the next step's first k row to the end
   uint64_t base;
-  // registers
+  // registers: the lane's 16 bytes of each block, where the next step's are
+  // and, feature-contiguous, the features from there to the edge
   u32x4 v[N];
+  const uint16_t* q[N];
+  int feats[N];
+  bool wide;    // 8 elements or more in a row of the operand
+  bool inside;  // every chunk of the wave's is loaded whole
+  bool edge;    // some of them from `back` features further down
+  int back[N];
 
-  CBD_INLINE __device__ void init(const uint16_t* p_, int64_t ld_, int rows_, int K_) {
+  // width: of the whole operand's features.
+  CBD_INLINE __device__ void init(const uint16_t* p_, int64_t ld_, int rows_, int K_, int width) {
+    wide = (KC ? K_ : width) >= 8;
     p = p_;
     ld = ld_;
     rows = rows_;
@@ -122,6 +131,30 @@ struct Feed {
         mask_tail(0);
       } else {
         clamp();
+      }
+    } else {
+      const int tid = fresh_tid();
+      inside = true;
+      edge = false;
+#pragma unroll
+      for (int i = 0; i < N; i++) {
+        const int r = fill_row(i, tid), c = 8 * fill_chunk(i, tid);
+        if (KC) {
+          q[i] = p + (r < rows ? r : rows - 1) * ld + c;
+        } else {
+          const int f = c < rows ? c : 0;
+          q[i] = p + r * ld + f;
+          feats[i] = rows - f;
+          // A chunk that passes the edge is loaded from further down, and
+          // moved when it is staged: no wait for it here.
+          back[i] = feats[i] < 8 && wide ? 8 - feats[i] : 0;
+          if (back[i]) {
+            q[i] -= back[i];
+            feats[i] = 8;
+          }
+          edge = edge || __any(back[i] != 0);
+          inside = inside && __all(feats[i] >= 8);
+        }
       }
     }
   }
@@ -161,30 +194,60 @@ struct Feed {
 #pragma clang diagnostic pop
   }
 
-  // Through registers: step t, zeros past the edges.
-  CBD_INLINE __device__ void load(int t) {
+  // y moved down by n < 8 elements.
+  CBD_INLINE __device__ static u32x4 down(u32x4 y, int n) {
+    uint64_t lo = (uint64_t)y[1] << 32 | y[0], hi = (uint64_t)y[3] << 32 | y[2];
+    if (n >= 4) {
+      lo = hi;
+      hi = 0;
+      n -= 4;
+    }
+    const int by = 16 * n;  // 0, 16, 32 or 48
+    lo = by > 0 ? lo >> by | hi << (64 - by) : lo;
+    hi >>= by;
+    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+  }
+  // The first n < 8 elements from s, zeros after them: by elements, or the 16
+  // bytes that end with them, moved down.
+  CBD_INLINE __device__ u32x4 first(const uint16_t* s, int n) const {
+    if (KC && wide) return down(*(const u32x4u*)(s - (8 - n)), 8 - n);
+    u32x4 x = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 7; j++)
+      if (j < n) x[j >> 1] |= (uint32_t)s[j] << (16 * (j & 1));
+    return x;
+  }
+  // Through registers: the next step, of which `left` k are inside, zeros past
+  // them.  Rows and features past an edge repeat others; what they give is not
+  // stored.
+  CBD_INLINE __device__ void load(int left) {
+    if (left >= BK && inside) {
+#pragma unroll
+      for (int i = 0; i < N; i++) {
+        v[i] = *(const u32x4u*)q[i];
+        q[i] += KC ? BK : BK * ld;
+      }
+      return;
+    }
     const int tid = fresh_tid();
 #pragma unroll
     for (int i = 0; i < N; i++) {
-      const int r = fill_row(i, tid), c = fill_chunk(i, tid);
-      const int row = KC ? r : t * BK + r, col = KC ? t * BK + 8 * c : 8 * c;
-      const int n = row < (KC ? rows : K) ? (KC ? K : rows) - col : 0;
-      const uint16_t* s = p + row * ld + col;
+      const int k = KC ? 8 * fill_chunk(i, tid) : fill_row(i, tid);
+      const int n = KC ? left - k : k < left ? feats[i] : 0;
       u32x4 x = {0u, 0u, 0u, 0u};
-      if (n >= 8) {
-        x = *(const u32x4u*)s;
-      } else if (n > 0) {
-#pragma unroll
-        for (int j = 0; j < 7; j++)
-          if (j < n) x[j >> 1] |= (uint32_t)s[j] << (16 * (j & 1));
-      }
+      if (n >= 8)
+        x = *(const u32x4u*)q[i];
+      else if (n > 0)
+        x = first(q[i], n);
       v[i] = x;
+      q[i] += KC ? BK : BK * ld;
     }
   }
   CBD_INLINE __device__ void stage(char* lds) const {
 #pragma unroll
     for (int i = 0; i < N; i++)
-      *(u32x4*)(lds + (N * (int)(threadIdx.x >> 6) + i) * 1024 + (threadIdx.x & 63) * 16) = v[i];
+      *(u32x4*)(lds + (N * (int)(threadIdx.x >> 6) + i) * 1024 + (threadIdx.x & 63) * 16) =
+          !KC && edge ? down(v[i], back[i]) : v[i];
   }
 
   // ---- fragments: of 32 rows (block b from feature f0), 16 k (step ks).
@@ -269,8 +332,8 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void expert_mfma_kernel(c
       const int n0 = t.n_tile * BN;
       c.K = t.end - t.begin;
       c.nrows = a.N - n0;
-      fa.init((const uint16_t*)a.a + t.begin * a.lda + m0, a.lda, c.mrows, c.K);
-      fb.init((const uint16_t*)a.b + t.begin * a.ldb + n0, a.ldb, c.nrows, c.K);
+      fa.init((const uint16_t*)a.a + t.begin * a.lda + m0, a.lda, c.mrows, c.K, a.M);
+      fb.init((const uint16_t*)a.b + t.begin * a.ldb + n0, a.ldb, c.nrows, c.K, a.N);
       c.out = (TO*)a.out + t.e * a.o_expert + n0 * a.ldo + m0;
     } else {
       const int n0 = t.begin + t.n_tile * BN + (t.half == 1 ? BN / 2 : 0);
@@ -279,8 +342,8 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void expert_mfma_kernel(c
       if (t.half == 0 && c.nrows > BN / 2) c.nrows = BN / 2;
       fa.init((const uint16_t*)a.a + (t.e < a.E ? t.e * a.a_expert : 0) +
                   (FORM == EXPERT_AK ? m0 * a.lda : (int64_t)m0),
-              a.lda, c.mrows, c.K);
-      fb.init((const uint16_t*)a.b + n0 * a.ldb, a.ldb, c.nrows, c.K);
+              a.lda, c.mrows, c.K, a.M);
+      fb.init((const uint16_t*)a.b + n0 * a.ldb, a.ldb, c.nrows, c.K, a.N);
       c.out = (TO*)a.out + n0 * a.ldo + m0;
     }
     if constexpr (DMA) {
@@ -296,8 +359,8 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void expert_mfma_kernel(c
         fb.advance(s + 1, steps);
       }
     } else {
-      fa.load(0);
-      fb.load(0);
+      fa.load(c.K);
+      fb.load(c.K);
     }
     return c;
   };
@@ -520,16 +583,16 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void expert_mfma_kernel(c
       __syncthreads();
       fa.stage(smem);
       fb.stage(smem + BBASE);
-      fa.load(1);
-      fb.load(1);
+      fa.load(fa.K - BK);
+      fb.load(fa.K - BK);
       auto iter = [&](int kt, auto sc) CBD_INLINE {
         constexpr int S = decltype(sc)::value;
         // Stage S is filled, and everyone has read stage 1 - S.
         __syncthreads();
         fa.stage(smem + (1 - S) * FeedA::BYTES);
         fb.stage(smem + BBASE + (1 - S) * FeedB::BYTES);
-        fa.load(kt + 2);
-        fb.load(kt + 2);
+        fa.load(fa.K - (kt + 2) * BK);
+        fb.load(fa.K - (kt + 2) * BK);
 #pragma unroll
         for (int ks = 0; ks < BK / 16; ks++) {
 #pragma unroll

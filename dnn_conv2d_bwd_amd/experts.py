@@ -16,6 +16,7 @@ operation in full.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 from . import BF16, F32, _check, _dtype, _lib, _torch_dtype
@@ -113,16 +114,14 @@ def expert_plan(tokens, experts, c, k, w_layout="ekc", dtype="bf16", dw_dtype=No
     return ExpertPlan(tokens, experts, c, k, w_layout, dtype, dw_dtype, force_kernel)
 
 
-def _dense_strides(shape):
-    out, n = [], 1
-    for s in reversed(shape):
-        out.append(n)
-        n *= s
-    return tuple(reversed(out))
+_DENSE = {2: (0,), 3: (0, 0)}
 
 
 def _strided(t, shape, dtype, device, name):
     """Checks a tensor; its strides in elements but the last (0: dense)."""
+    if (getattr(t, "dtype", None) is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()
+            and (device is None or t.get_device() == device.index)):
+        return _DENSE[len(shape)]
     if not hasattr(t, "data_ptr") or not t.is_cuda:
         raise ValueError(f"{name} must be a GPU torch tensor")
     if t.dtype != dtype:
@@ -135,9 +134,9 @@ def _strided(t, shape, dtype, device, name):
     if st[-1] != 1 and shape[-1] != 1 and t.numel():
         raise ValueError(f"the last dimension of {name} must be contiguous")
     if t.is_contiguous():
-        return (0,) * (len(shape) - 1)
-    out, dense = [], _dense_strides(shape)
-    for n, s, d in zip(shape[:-1], st, dense):
+        return _DENSE[len(shape)]
+    out = []
+    for n, s in zip(shape[:-1], st):
         if n > 1 and s < 1:
             raise ValueError(f"{name} repeats rows (stride {s}); make it contiguous")
         out.append(s if n > 1 else 0)
@@ -153,18 +152,17 @@ def _handle(stream, device):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(device, stream):
     """Context in which outputs are allocated and kernels launched: the
     tensors' device and the call's stream (so that the caching allocator ties
     new memory to the stream that writes it)."""
-    import contextlib
-
     import torch
 
     if stream is None:
-        if torch.cuda.current_device() == device.index:
-            return contextlib.nullcontext()
-        return torch.cuda.device(device)
+        return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     return torch.cuda.stream(stream)
@@ -173,17 +171,17 @@ def _on(device, stream):
 def _ends(p, ends, device):
     import torch
 
-    if not hasattr(ends, "data_ptr") or not ends.is_cuda or ends.device != device:
+    if not hasattr(ends, "data_ptr") or not ends.is_cuda or ends.get_device() != device.index:
         raise ValueError(f"ends must be a tensor on {device}")
     if ends.dtype not in (torch.int32, torch.int64):
         raise ValueError(f"ends must be int32 or int64, got {ends.dtype}")
-    if tuple(ends.shape) != (p.experts,) or not ends.is_contiguous():
+    if ends.shape != (p.experts,) or not ends.is_contiguous():
         raise ValueError(f"ends must be contiguous with shape ({p.experts},), got {tuple(ends.shape)}")
     return 32 if ends.dtype == torch.int32 else 64
 
 
 def _strides(x, y, w):
-    if not (any(x) or any(y) or any(w)):
+    if x is y is _DENSE[2] and w is _DENSE[3]:
         return None
     return ctypes.byref(ExpertStrides(x[0], y[0], w[1], w[0]))
 
