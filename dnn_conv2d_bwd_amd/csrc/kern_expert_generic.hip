@@ -94,11 +94,16 @@ struct Operand {
   const T* q[NV];  // this thread's vectors of the next step
   int64_t step;
   int feats[NV];   // feature-contiguous: features of the vector inside the operand
+  int back[NV];    // and by how many it is loaded early
+  bool edge;       // some of the wave's are
   f32x4 v[2][NV];  // two steps
 
   // p: element (row 0, k 0) of the tile; rows: inside the operand, >= 1.
-  CBD_INLINE __device__ void init(const T* p, int64_t ld, int rows) {
+  // width: features of the whole operand.
+  CBD_INLINE __device__ void init(const T* p, int64_t ld, int rows, int width) {
     step = KC ? BK : BK * ld;
+    const bool wide = width >= 4;
+    edge = false;
 #pragma unroll
     for (int i = 0; i < NV; i++) {
       const int idx = i * THREADS + (int)threadIdx.x;
@@ -106,10 +111,15 @@ struct Operand {
       if (KC) {
         q[i] = p + (row < rows ? row : rows - 1) * ld + col;
         feats[i] = 4;
+        back[i] = 0;
       } else {
         const int f = col < rows ? col : 0;
-        q[i] = p + row * ld + f;
-        feats[i] = rows - f;
+        // A vector that passes the edge is loaded from further down and moved
+        // when it is staged: no wait for it in between.
+        back[i] = rows - f < 4 && wide ? 4 - (rows - f) : 0;
+        edge = edge || __any(back[i] != 0);
+        q[i] = p + row * ld + f - back[i];
+        feats[i] = rows - f + back[i];
       }
     }
   }
@@ -130,7 +140,12 @@ struct Operand {
 #pragma unroll
     for (int i = 0; i < NV; i++) {
       const int idx = i * THREADS + (int)threadIdx.x;
-      *(f32x4*)(lds + (idx / QUADS) * ROW + 4 * (idx % QUADS)) = v[slot][i];
+      f32x4 x = v[slot][i];
+      if (!KC && edge) {
+        if (back[i] & 1) x = f32x4{x[1], x[2], x[3], 0.f};
+        if (back[i] & 2) x = f32x4{x[2], x[3], 0.f, 0.f};
+      }
+      *(f32x4*)(lds + (idx / QUADS) * ROW + 4 * (idx % QUADS)) = x;
     }
   }
   // Fragments of a wave's 16 * NB rows from row r0: f[block][i].
@@ -181,8 +196,8 @@ __global__ __launch_bounds__(THREADS, NB == 4 ? 3 : 4) void expert_generic_kerne
     const int n0 = t.n_tile * BT;
     mrows = a.M - m0;
     nrows = a.N - n0;
-    oa.init((const T*)a.a + (int64_t)t.begin * a.lda + m0, a.lda, mrows);
-    ob.init((const T*)a.b + (int64_t)t.begin * a.ldb + n0, a.ldb, nrows);
+    oa.init((const T*)a.a + (int64_t)t.begin * a.lda + m0, a.lda, mrows, a.M);
+    ob.init((const T*)a.b + (int64_t)t.begin * a.ldb + n0, a.ldb, nrows, a.N);
     out = (TO*)a.out + t.e * a.o_expert + n0 * a.ldo + m0;
   } else {
     dev::RowTiles tiles;
@@ -195,8 +210,8 @@ __global__ __launch_bounds__(THREADS, NB == 4 ? 3 : 4) void expert_generic_kerne
     mrows = a.M - m0;
     nrows = t.end - n0;
     oa.init((const T*)a.a + (t.e < a.E ? t.e * a.a_expert : 0) + (FORM == EXPERT_AK ? m0 * a.lda : (int64_t)m0),
-            a.lda, mrows);
-    ob.init((const T*)a.b + (int64_t)n0 * a.ldb, a.ldb, nrows);
+            a.lda, mrows, a.M);
+    ob.init((const T*)a.b + (int64_t)n0 * a.ldb, a.ldb, nrows, a.N);
     out = (TO*)a.out + (int64_t)n0 * a.ldo + m0;
   }
   const int live = dev::uniform((nrows - wn + 15) >> 4);  // 16-row blocks of this wave (AK, AM)
