@@ -100,6 +100,8 @@ ExpertLaunch choose(const cbd_expert_plan_s& plan, int op, bool narrow_strides, 
     const bool many = op == CBD_EXPERT_BWD_WEIGHT || p.tokens >= (half ? 384 : 192) * p.experts;
     l.bm = l.bn = l.dma && whole_out && many && grid(256, 256) >= 512 ? 256 : 128;
   } else {
+    // 64 x 64 where 128 x 128 would leave compute units idle: 64 / 128 in us at
+    // 320 tiles of 128 114 / 153, at 192 29 / 49; at 512 and more the same.
     l.bm = l.bn = 128;
     if (grid(128, 128) < 512) l.bm = l.bn = 64;
   }

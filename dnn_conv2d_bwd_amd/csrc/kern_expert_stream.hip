@@ -18,7 +18,12 @@
 // Rows of the activations are read straight from L2 (every workgroup of an
 // expert reads the same few).  Any alignment of 2 bytes will do.
 //
-// Bound: HBM, one pass over the weights of the experts that have rows.
+// Bound: HBM, one pass over the weights of the experts that have rows.  64
+// experts of 2048 x 1408 with 8 rows each: AK 73 us (5.1 TB/s), AM 66 us (5.6);
+// 8 of them with a row each 12.5 us, where the way to the first load (row
+// ranges, tile, addresses) counts.  AK has one step in flight a wave and 8
+// waves a SIMD: with two and 5 waves 77 us, four and 3 waves 80, seven and 2
+// waves 103; non-temporal loads 87.
 #include <type_traits>
 
 #include "expert_device.h"

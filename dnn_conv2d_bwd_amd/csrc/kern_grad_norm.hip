@@ -87,12 +87,12 @@ __device__ inline void square16(u32x4 v, double (&s)[4]) {
   }
 }
 
-template <bool F32, int T>
-__device__ inline void square_chunk(const Chunk& c, double (&s)[4]) {
+template <bool F32>
+__device__ inline void square_chunk(const Chunk& c, uint32_t tid, double (&s)[4]) {
   constexpr int U = 4;
-  constexpr uint32_t STEP = T * VEC;
+  constexpr uint32_t STEP = THREADS * VEC;
   const uint32_t whole = c.bytes / VEC * VEC;
-  uint32_t at = threadIdx.x * VEC;
+  uint32_t at = tid * VEC;
   for (; at + (U - 1) * STEP < whole; at += U * STEP) {
     u32x4 v[U];
 #pragma unroll
@@ -103,26 +103,25 @@ __device__ inline void square_chunk(const Chunk& c, double (&s)[4]) {
   for (; at < whole; at += STEP) square16<F32>(*(const u32x4u*)(c.in + at), s);
   // Fewer than 16 bytes are left: an element a thread.
   constexpr uint32_t ES = F32 ? 4 : 2;
-  const uint32_t e = whole + threadIdx.x * ES;
+  const uint32_t e = whole + tid * ES;
   if (e < c.bytes) {
     const double d = F32 ? (double)*(const float*)(c.in + e) : (double)dev::bf16_to_f32(*(const uint16_t*)(c.in + e));
     s[0] = __builtin_fma(d, d, s[0]);
   }
 }
 
-template <int T>
-__device__ inline void square_chunk(const Chunk& c, double (&s)[4]) {
+__device__ inline void square_chunk(const Chunk& c, uint32_t tid, double (&s)[4]) {
   if (c.dtype == CBD_F32)
-    square_chunk<true, T>(c, s);
+    square_chunk<true>(c, tid, s);
   else
-    square_chunk<false, T>(c, s);
+    square_chunk<false>(c, tid, s);
 }
 
 __global__ __launch_bounds__(THREADS) void grad_partial_kernel(const GradArgs a) {
   double s[4] = {0.0, 0.0, 0.0, 0.0};
   for (uint32_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
     const Chunk k = chunk_of(a, c);
-    square_chunk<THREADS>(k, s);
+    square_chunk(k, threadIdx.x, s);
   }
   const double t = block_sum<THREADS>((s[0] + s[1]) + (s[2] + s[3]));
   if (threadIdx.x == 0) a.partial[a.first + blockIdx.x] = t;
@@ -152,12 +151,12 @@ __device__ inline u32x4 scale16(u32x4 v, double f) {
   return v;
 }
 
-template <bool F32, int T>
-__device__ inline void scale_chunk(const Chunk& c, double f) {
+template <bool F32>
+__device__ inline void scale_chunk(const Chunk& c, uint32_t tid, double f) {
   constexpr int U = 4;
-  constexpr uint32_t STEP = T * VEC;
+  constexpr uint32_t STEP = THREADS * VEC;
   const uint32_t whole = c.bytes / VEC * VEC;
-  uint32_t at = threadIdx.x * VEC;
+  uint32_t at = tid * VEC;
   for (; at + (U - 1) * STEP < whole; at += U * STEP) {
     u32x4 v[U];
 #pragma unroll
@@ -167,7 +166,7 @@ __device__ inline void scale_chunk(const Chunk& c, double f) {
   }
   for (; at < whole; at += STEP) *(u32x4u*)(c.out + at) = scale16<F32>(*(const u32x4u*)(c.in + at), f);
   constexpr uint32_t ES = F32 ? 4 : 2;
-  const uint32_t e = whole + threadIdx.x * ES;
+  const uint32_t e = whole + tid * ES;
   if (e < c.bytes) {
     if (F32)
       *(float*)(c.out + e) = times(*(const float*)(c.in + e), f);
@@ -176,13 +175,12 @@ __device__ inline void scale_chunk(const Chunk& c, double f) {
   }
 }
 
-template <int T>
-__device__ inline void scale_chunk(const Chunk& c, double f) {
+__device__ inline void scale_chunk(const Chunk& c, uint32_t tid, double f) {
   if (f == 1.0 && c.in == c.out) return;  // g * 1 is g
   if (c.dtype == CBD_F32)
-    scale_chunk<true, T>(c, f);
+    scale_chunk<true>(c, tid, f);
   else
-    scale_chunk<false, T>(c, f);
+    scale_chunk<false>(c, tid, f);
 }
 
 // By comparison, so that a NaN norm gives a NaN factor.
@@ -197,21 +195,22 @@ __global__ __launch_bounds__(THREADS) void grad_scale_kernel(const GradArgs a) {
   if (a.first == 0 && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)n;
   for (uint32_t i = blockIdx.x; i < a.chunks; i += gridDim.x) {
     const Chunk k = chunk_of(a, a.chunks - 1 - i);
-    scale_chunk<THREADS>(k, f);
+    scale_chunk(k, threadIdx.x, f);
   }
 }
 
 // A list of few chunks: norm and, with clip, scaling by one workgroup, in one
-// launch.
+// launch; four waves a chunk.
 constexpr int SMALL_THREADS = 1024;
 __global__ __launch_bounds__(SMALL_THREADS) void grad_small_kernel(const GradArgs a, int clip) {
   double s[4] = {0.0, 0.0, 0.0, 0.0};
-  for (uint32_t c = 0; c < a.chunks; c++) square_chunk<SMALL_THREADS>(chunk_of(a, c), s);
+  const uint32_t group = threadIdx.x / THREADS, tid = threadIdx.x % THREADS;
+  for (uint32_t c = group; c < a.chunks; c += SMALL_THREADS / THREADS) square_chunk(chunk_of(a, c), tid, s);
   const double n = __builtin_sqrt(block_sum<SMALL_THREADS>((s[0] + s[1]) + (s[2] + s[3])));
   if (threadIdx.x == 0) *a.norm = (float)n;
   if (!clip) return;
   const double f = factor_of(a, n);
-  for (uint32_t c = 0; c < a.chunks; c++) scale_chunk<SMALL_THREADS>(chunk_of(a, c), f);
+  for (uint32_t c = group; c < a.chunks; c += SMALL_THREADS / THREADS) scale_chunk(chunk_of(a, c), tid, f);
 }
 
 int launch(const void* k, const GradArgs& a, uint32_t grid, void* stream) {
