@@ -100,10 +100,14 @@ ExpertLaunch choose(const cbd_expert_plan_s& plan, int op, bool narrow_strides, 
     const bool many = op == CBD_EXPERT_BWD_WEIGHT || p.tokens >= (half ? 384 : 192) * p.experts;
     l.bm = l.bn = l.dma && whole_out && many && grid(256, 256) >= 512 ? 256 : 128;
   } else {
-    // 64 x 64 where 128 x 128 would leave compute units idle: 64 / 128 in us at
-    // 320 tiles of 128 114 / 153, at 192 29 / 49; at 512 and more the same.
-    l.bm = l.bn = 128;
-    if (grid(128, 128) < 512) l.bm = l.bn = 64;
+    // 64 x 64 where 128 x 128 would leave compute units idle (64 / 128 in us: at
+    // 320 tiles of 128 114 / 153, at 192 29 / 49) or compute a tenth more for
+    // nothing (59801 rows, 176 wide: 849 / 1033; 320 wide 443 / 465); otherwise
+    // they are alike (256 wide 1090 / 1063, 2048 wide 716 / 748).
+    auto covered = [&](int64_t b) {
+      return (m + b - 1) / b * b * (op == CBD_EXPERT_BWD_WEIGHT ? (n + b - 1) / b * b : 1);
+    };
+    l.bm = l.bn = grid(128, 128) < 512 || covered(128) * 10 > covered(64) * 11 ? 64 : 128;
   }
   l.grid = grid(l.bm, l.bn);
   // Workgroups that stay: one (256 x 256: its LDS) or two a compute unit.

@@ -382,7 +382,7 @@ typedef enum {
   CBD_EXPERT_KERNEL_AUTO = -1,
   CBD_EXPERT_KERNEL_GENERIC = 0, /* any type, size, stride and alignment: f32 MFMA */
   CBD_EXPERT_KERNEL_MFMA = 1,    /* bf16: many rows, LDS tiles */
-  CBD_EXPERT_KERNEL_STREAM = 2   /* bf16 forward and bwd_data: few rows an expert */
+  CBD_EXPERT_KERNEL_STREAM = 2   /* bf16: few rows an expert (bwd_weight: as MFMA) */
 } cbd_expert_kernel;
 
 typedef struct {
