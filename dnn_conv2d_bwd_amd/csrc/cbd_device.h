@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include "cbd_kernarg.h"
+#include "cbd_tile.h"
 
 namespace cbd {
 namespace dev {
@@ -35,15 +36,6 @@ typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 __device__ inline uint32_t bf16_pack2(float lo, float hi) {
   const bf16x2_t v = {(__bf16)lo, (__bf16)hi};
   return __builtin_bit_cast(uint32_t, v);
-}
-
-// Logical tile of hardware workgroup b.  Workgroups are dealt round-robin to
-// the 8 XCDs (each with its own L2); with remap on, XCD x receives the
-// contiguous logical range [x*q + min(x, r), ...), so neighbouring tiles --
-// which share operand panels -- meet in one L2.
-__device__ inline int logical_tile(int b, int total, int remap) {
-  const int q = total >> 3, r = total & 7, x = b & 7, idx = b >> 3;
-  return remap ? x * q + (x < r ? x : r) + idx : b;
 }
 
 // Logical block of hardware workgroup b for the grouped row kernels:

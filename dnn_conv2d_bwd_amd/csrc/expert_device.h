@@ -1,6 +1,8 @@
-// expert_device.h -- which rows a workgroup of an expert product owns.
+// expert_device.h -- which rows a workgroup of an expert product owns.  Only
+// integers and wave operations, so that a host program can run it too: kernels
+// include cbd_device.h first.
 #pragma once
-#include "cbd_device.h"
+#include "cbd_tile.h"
 #include "expert_internal.h"
 
 // Inlined always: a kernel's by-value arguments would otherwise be copied to
@@ -51,9 +53,8 @@ CBD_INLINE __device__ inline uint64_t uniform(uint64_t v) {
 
 struct ExpertTile {
   int e;           // expert; E for the rows past the last expert's
-  int begin, end;  // its rows
+  int begin, end;  // AK, AM: the tile's rows; DW: the expert's
   int m_tile, n_tile;
-  int half;        // 0, 1: the first or second half of its rows only; -1: all
   bool ok;         // false: no such tile (the grid is an upper bound)
 };
 
@@ -100,17 +101,25 @@ struct RowTiles {
     }
     tiles = (int64_t)(total + (a.T - last + bn - 1) / bn) * a.tiles_m;
   }
+  // Cuts r's rows down to those of row tile n_tile, or (half 0, 1; -1: all) to
+  // a half of it.  A second half may have none.
+  CBD_INLINE __device__ static void cut(ExpertTile& r, int bn, int half) {
+    r.begin += r.n_tile * bn + (half == 1 ? bn / 2 : 0);
+    const int most = half < 0 ? bn : bn / 2;
+    r.ok = r.begin < r.end;
+    if (r.end - r.begin > most) r.end = r.begin + most;
+  }
   // Tile of hardware workgroup b.  g > 0: workgroups take b, b + g, ...; where
   // the last round's tiles are at most g / 2, each is taken as two halves of
   // its rows.
   CBD_INLINE __device__ ExpertTile at(const ExpertArgs& a, int64_t b, int bn, int g = 0) {
     ExpertTile r;
-    r.half = -1;
+    int half = -1;
     const int64_t whole = g > 0 ? (int)tiles / g * g : tiles;  // fewer than 2^31: the caller checks
     const int left = (int)(tiles - whole);
     if (b >= whole && 2 * left <= g) {
       const int p = b - whole < 2 * left ? logical_tile((int)(b - whole), 2 * left, 1) : 2 * left;
-      r.half = p & 1;
+      half = p & 1;
       b = whole + (p >> 1);
     }
     r.ok = b < tiles;
@@ -119,12 +128,12 @@ struct RowTiles {
     r.end = a.T;
     r.m_tile = r.n_tile = 0;
     if (!r.ok) return r;
-    const int t = r.half < 0 ? spread_tile((int)b, (int)tiles) : (int)b;
+    const int t = half < 0 ? spread_tile((int)b, (int)tiles) : (int)b;
     if (t >= (int64_t)total * a.tiles_m) {
       const int local = t - total * a.tiles_m;
       r.n_tile = uniform(local / a.tiles_m);
       r.m_tile = uniform(local - r.n_tile * a.tiles_m);
-      if (r.half == 1 && r.begin + r.n_tile * bn + bn / 2 >= r.end) r.ok = false;
+      cut(r, bn, half);
       return r;
     }
     int before = 0, end = 0;  // row tiles and rows before the chunk
@@ -149,7 +158,7 @@ struct RowTiles {
         const int row = in / gm;
         r.n_tile = uniform(row);
         r.m_tile = uniform(8 * grp + in - row * gm);
-        if (r.half == 1 && r.begin + r.n_tile * bn + bn / 2 >= r.end) r.ok = false;
+        cut(r, bn, half);
         return r;
       }
       before += __builtin_amdgcn_readlane(sum, 63);
@@ -183,7 +192,6 @@ struct WeightTiles {
   }
   CBD_INLINE __device__ ExpertTile at(const ExpertArgs& a, int64_t b, int, int) const {
     ExpertTile r;
-    r.half = -1;
     r.ok = b < tiles;
     r.e = r.begin = r.end = r.m_tile = r.n_tile = 0;
     if (!r.ok) return r;

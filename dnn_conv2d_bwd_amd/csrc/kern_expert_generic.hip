@@ -26,6 +26,7 @@
 // MFMAs of the compute units that get two of the 357 tiles.
 #include <type_traits>
 
+#include "cbd_device.h"
 #include "expert_device.h"
 
 namespace cbd {
@@ -207,7 +208,7 @@ __global__ __launch_bounds__(THREADS, NB == 4 ? 3 : 4) void expert_generic_kerne
     const dev::ExpertTile t = tiles.at(a, blockIdx.x, BT);
     if (!t.ok) return;
     K = t.e < a.E ? a.K : 0;  // rows past the last expert's: zeros
-    const int n0 = t.begin + t.n_tile * BT;
+    const int n0 = t.begin;
     m0 = t.m_tile * BT;
     mrows = a.M - m0;
     nrows = t.end - n0;

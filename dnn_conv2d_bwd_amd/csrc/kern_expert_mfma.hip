@@ -45,6 +45,7 @@
 // outputs and 1024 rows each 443 / 476 us.
 #include <type_traits>
 
+#include "cbd_device.h"
 #include "expert_device.h"
 
 namespace cbd {
@@ -349,10 +350,9 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void expert_mfma_kernel(c
       fb.init((const uint16_t*)a.b + t.begin * a.ldb + n0, a.ldb, c.nrows, c.K, a.N);
       c.out = (TO*)a.out + t.e * a.o_expert + n0 * a.ldo + m0;
     } else {
-      const int n0 = t.begin + t.n_tile * BN + (t.half == 1 ? BN / 2 : 0);
+      const int n0 = t.begin;
       c.K = t.e < a.E ? a.K : 0;  // rows past the last expert's: zeros
       c.nrows = t.end - n0;
-      if (t.half == 0 && c.nrows > BN / 2) c.nrows = BN / 2;
       fa.init((const uint16_t*)a.a + (t.e < a.E ? t.e * a.a_expert : 0) +
                   (FORM == EXPERT_AK ? m0 * a.lda : (int64_t)m0),
               a.lda, c.mrows, c.K, a.M);

@@ -26,6 +26,7 @@
 // waves 103; non-temporal loads 87.
 #include <type_traits>
 
+#include "cbd_device.h"
 #include "expert_device.h"
 
 namespace cbd {
@@ -83,8 +84,8 @@ __global__ __launch_bounds__(THREADS, FORM == EXPERT_AK ? 8 : 2) void expert_str
   const int lane = threadIdx.x & 63, wave = dev::uniform((int)(threadIdx.x >> 6));
   const int g = lane >> 4, i16 = lane & 15;
   const int K = t.e < a.E ? a.K : 0;  // rows past the last expert's: zeros
-  const int n0 = t.begin + t.n_tile * BN;
-  const int nrows = t.end - n0 < BN ? t.end - n0 : BN;
+  const int n0 = t.begin;
+  const int nrows = t.end - n0;
   // AM: the last slice starts earlier, so that no 16 bytes pass the row's end
   // (features of two slices are then written twice, with the same values).
   int m0 = t.m_tile * S::BM;
