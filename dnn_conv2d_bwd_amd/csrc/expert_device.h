@@ -179,6 +179,17 @@ CBD_INLINE __device__ inline void expert_rows(const ExpertArgs& a, int e, int& b
   end = x > begin ? x : begin;
 }
 
+// Features of slice i of M by a kernel that loads slices of bm features whole:
+// the last one starts early, where there are as many, so that it ends with the
+// row; its first `skip` features are the slice's before, which stores them.
+struct FeatureSlice {
+  int m0, skip;
+};
+CBD_INLINE __device__ inline FeatureSlice feature_slice(int i, int bm, int M) {
+  const int own = i * bm, m0 = own + bm > M && M >= bm ? M - bm : own;
+  return {m0, own - m0};
+}
+
 // Tiles of a DW product: groups of 8 feature tiles by all tiles of the other
 // side, as above.
 struct WeightTiles {

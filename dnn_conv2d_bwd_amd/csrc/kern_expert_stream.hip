@@ -50,15 +50,15 @@ __device__ inline u32x4 part8(const uint16_t* p, int n) {
   return x;
 }
 
-// 8 values of a row, rounded once; n < 8: the first n.
-__device__ inline void store8(uint16_t* o, const float* v, int n) {
-  if (n >= 8) {
+// Values [lo, n) of 8 of a row, rounded once.
+__device__ inline void store8(uint16_t* o, const float* v, int lo, int n) {
+  if (lo <= 0 && n >= 8) {
     *(u32x4u*)o = u32x4{dev::bf16_pack2(v[0], v[1]), dev::bf16_pack2(v[2], v[3]), dev::bf16_pack2(v[4], v[5]),
                         dev::bf16_pack2(v[6], v[7])};
   } else {
 #pragma unroll
-    for (int j = 0; j < 7; j++)
-      if (j < n) o[j] = (uint16_t)dev::bf16_rne(v[j]);
+    for (int j = 0; j < 8; j++)
+      if (j >= lo && j < n) o[j] = (uint16_t)dev::bf16_rne(v[j]);
   }
 }
 
@@ -86,10 +86,10 @@ __global__ __launch_bounds__(THREADS, FORM == EXPERT_AK ? 8 : 2) void expert_str
   const int K = t.e < a.E ? a.K : 0;  // rows past the last expert's: zeros
   const int n0 = t.begin;
   const int nrows = t.end - n0;
-  // AM: the last slice starts earlier, so that no 16 bytes pass the row's end
-  // (features of two slices are then written twice, with the same values).
-  int m0 = t.m_tile * S::BM;
-  if (!AK && m0 + S::BM > a.M && a.M >= S::BM) m0 = a.M - S::BM;
+  // AM: the last slice starts earlier, so that no 16 bytes pass the row's end.
+  const dev::FeatureSlice slice =
+      AK ? dev::FeatureSlice{t.m_tile * S::BM, 0} : dev::feature_slice(t.m_tile, S::BM, a.M);
+  const int m0 = slice.m0;
   const uint16_t* const w =
       (const uint16_t*)a.a + (t.e < a.E ? t.e * a.a_expert : 0) + (AK ? m0 * a.lda : (int64_t)m0);
   const uint16_t* const x = (const uint16_t*)a.b + n0 * a.ldb;
@@ -274,7 +274,8 @@ __global__ __launch_bounds__(THREADS, FORM == EXPERT_AK ? 8 : 2) void expert_str
 #pragma unroll
           for (int q = 1; q < WAVES; q++) v[j] += ((const float*)&sums[q][j][lane])[wave];
         }
-        if (row < nrows && f < mrows) store8(out + row * a.ldo + f, v, mrows - f);
+        if (row < nrows && f + 8 > slice.skip && f < mrows)
+          store8(out + row * a.ldo + f, v, slice.skip - f, mrows - f);
       }
     }
   };

@@ -1,7 +1,8 @@
 // The tile enumeration of the expert products (csrc/expert_device.h), run on
 // the host: 64 contexts stand for a wave's lanes and swap at every operation
-// that crosses lanes.  Every row of every feature tile, and every tile of a
-// weight gradient, has to have exactly one workgroup.
+// that crosses lanes.  Every row of every feature tile, every feature of a row
+// of slices that start early, and every tile of a weight gradient has to have
+// exactly one workgroup.
 //
 //   expert_tiles SEED COUNT
 #include <setjmp.h>
@@ -194,10 +195,25 @@ static int weights(ExpertArgs a, const std::vector<int>& ends, int cap) {
   return 0;
 }
 
+static int slices(int bm, int M) {
+  std::vector<uint8_t> owned(M);
+  for (int i = 0; i * bm < M; i++) {
+    const cbd::dev::FeatureSlice s = cbd::dev::feature_slice(i, bm, M);
+    if (s.m0 < 0 || s.skip < 0 || (M >= bm && s.m0 + bm > M))
+      return std::fprintf(stderr, "slice %d of %d features leaves the row\n", i, M), 1;
+    for (int f = s.m0 + s.skip; f < std::min(s.m0 + bm, M); f++)
+      if (owned[f]++) return std::fprintf(stderr, "feature %d of %d has two workgroups\n", f, M), 1;
+  }
+  if (std::count(owned.begin(), owned.end(), 1) != M) return std::fprintf(stderr, "a feature of %d is left out\n", M), 1;
+  return 0;
+}
+
 int main(int argc, char** argv) {
   std::mt19937 rng(argc > 1 ? std::atoi(argv[1]) : 1);
   const int count = argc > 2 ? std::atoi(argv[2]) : 20;
   auto uni = [&](int lo, int hi) { return lo + (int)(rng() % (unsigned)(hi - lo + 1)); };
+  for (int m = 1; m < 1000; m++)
+    if (slices(128, m)) return 1;
   ExpertArgs a = {};
   // Tiles left for the last round of 256 workgroups that stay: at and around a
   // half of them, of one expert and of two that end inside a tile, with and
