@@ -49,6 +49,11 @@ bool share(const Block& a, const Block& b) {
 
 constexpr int64_t kMaxSlice = int64_t(1) << 31;  // bytes: offsets within a slice or tile are 32-bit
 
+// Threads of a workgroup, and the most workgroups of a launch (a grid has fewer
+// than 2^32 threads).
+constexpr int kThreads = 256;
+constexpr int64_t kMaxGrid = UINT32_MAX / kThreads;
+
 // Launch of an operator.  narrow_strides: 256 rows of either input stay within
 // 32-bit offsets; dma: and both start every row on a 16-byte boundary;
 // whole_out: the output's rows are 16-byte multiples on 16-byte boundaries.
@@ -60,7 +65,7 @@ ExpertLaunch choose(const cbd_expert_plan_s& plan, int op, bool narrow_strides, 
   l.form = op == CBD_EXPERT_BWD_WEIGHT ? cbd::EXPERT_DW
            : (op == CBD_EXPERT_FORWARD) == (p.w_layout == CBD_EXPERT_EKC) ? cbd::EXPERT_AK
                                                                           : cbd::EXPERT_AM;
-  l.threads = 256;
+  l.threads = kThreads;
   // The contiguous side of the output and, for bwd_weight, its other side.
   const bool wide_k = op == CBD_EXPERT_FORWARD || (op == CBD_EXPERT_BWD_WEIGHT && p.w_layout == CBD_EXPERT_ECK);
   const int64_t m = wide_k ? p.k : p.c;
@@ -74,7 +79,8 @@ ExpertLaunch choose(const cbd_expert_plan_s& plan, int op, bool narrow_strides, 
   l.kernel = plan.opt.force_kernel;
   // Few rows an expert: 64 experts of 2048 x 1408, stream / mfma in us at 16
   // rows an expert 92 / 97 (AK) and 68 / 77 (AM), at 32 rows 125 / 98 and 83 / 79.
-  const bool stream_ok = op != CBD_EXPERT_BWD_WEIGHT && narrow_strides;
+  const int stream_bm = l.form == cbd::EXPERT_AK ? 32 : 128;
+  const bool stream_ok = op != CBD_EXPERT_BWD_WEIGHT && narrow_strides && grid(stream_bm, 32) <= kMaxGrid;
   if (l.kernel == CBD_EXPERT_KERNEL_AUTO)
     l.kernel = p.dtype != CBD_BF16 ? CBD_EXPERT_KERNEL_GENERIC
                : stream_ok && p.tokens <= (l.form == cbd::EXPERT_AK ? 16 : 24) * p.experts
@@ -83,7 +89,7 @@ ExpertLaunch choose(const cbd_expert_plan_s& plan, int op, bool narrow_strides, 
   if (l.kernel == CBD_EXPERT_KERNEL_STREAM && !stream_ok) l.kernel = CBD_EXPERT_KERNEL_MFMA;
   l.dma = 0;
   if (l.kernel == CBD_EXPERT_KERNEL_STREAM) {
-    l.bm = l.form == cbd::EXPERT_AK ? 32 : 128;
+    l.bm = stream_bm;
     l.bn = 32;
     l.grid = grid(l.bm, l.bn);
     return l;
@@ -107,7 +113,8 @@ ExpertLaunch choose(const cbd_expert_plan_s& plan, int op, bool narrow_strides, 
     auto covered = [&](int64_t b) {
       return (m + b - 1) / b * b * (op == CBD_EXPERT_BWD_WEIGHT ? (n + b - 1) / b * b : 1);
     };
-    l.bm = l.bn = grid(128, 128) < 512 || covered(128) * 10 > covered(64) * 11 ? 64 : 128;
+    const bool small = grid(128, 128) < 512 || covered(128) * 10 > covered(64) * 11;
+    l.bm = l.bn = small && grid(64, 64) <= kMaxGrid ? 64 : 128;
   }
   l.grid = grid(l.bm, l.bn);
   // Workgroups that stay: one (256 x 256: its LDS) or two a compute unit.
@@ -185,7 +192,7 @@ cbd_status run(const cbd_expert_plan_t* plan, int op, const void* row_in, const 
     }
   dma = dma && narrow_strides;
   const ExpertLaunch l = choose(*plan, op, narrow_strides, dma, whole_out);
-  if (l.grid > INT32_MAX) return fail(CBD_ERR_UNSUPPORTED, "too many tiles for one launch");
+  if (l.grid > kMaxGrid) return fail(CBD_ERR_UNSUPPORTED, "too many tiles for one launch");
 
   ExpertArgs a = {};
   a.ends = ends;

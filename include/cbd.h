@@ -428,8 +428,9 @@ cbd_status cbd_expert_plan_info(const cbd_expert_plan_t* plan, int32_t op, cbd_e
  * other alignment or stride only selects a kernel.  Errors: INVALID_ARG for
  * NULL pointers (row tensors may be NULL when T = 0), strides below the
  * width and an output that overlaps an operand or ends; UNSUPPORTED for
- * pointers off their element's alignment and strides whose tiles pass 32-bit
- * offsets; HIP for a launch error.  Nothing is launched on an error. */
+ * pointers off their element's alignment, strides whose tiles pass 32-bit
+ * offsets and calls of 2^24 workgroups or more; HIP for a launch error.
+ * Nothing is launched on an error. */
 cbd_status cbd_expert_forward(const cbd_expert_plan_t* plan, const void* x, const void* w,
                               const void* ends, void* y, const cbd_expert_strides* strides,
                               void* stream);
