@@ -12,12 +12,18 @@ come out as zeros; an expert without rows gets a zero gradient.  W is
 strided views with a contiguous last dimension.  include/cbd.h states the
 operation in full.
 
+Autograd records the three calls where an operand requires gradients; each is
+linear in both operands, so their gradients are these calls again, to any
+order.  Into a given output nothing can be recorded: such a call is refused,
+like torch's with out=.  Forward-mode derivatives are not there and raise.
+
 `expert_linear` and `expert_linear_bwd` build and cache the plan themselves.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 
 from . import BF16, F32, _check, _dtype, _lib, _torch_dtype
 
@@ -207,24 +213,9 @@ def _product(p, op, rows, w, ends, out, stream):
     return out
 
 
-def expert_forward(p: ExpertPlan, x, w, ends, y=None, stream=None):
-    """y[t] = W_e x[t] on `stream` (default: torch's current one); y is
-    allocated unless given, and returned."""
-    return _product(p, FORWARD, x, w, ends, y, stream)
-
-
-def expert_bwd_data(p: ExpertPlan, dy, w, ends, dx=None, stream=None):
-    """dx[t] = W_e^T dy[t]."""
-    return _product(p, BWD_DATA, dy, w, ends, dx, stream)
-
-
-def expert_bwd_weight(p: ExpertPlan, dy, x, ends, dw=None, accumulate=False, stream=None):
-    """dW_e = sum over the rows of e of dy[t] x[t]^T, in the layout of W;
-    accumulate: added to the given dw."""
+def _weight(p, dy, x, ends, dw, accumulate, stream):
     import torch
 
-    if accumulate and dw is None:
-        raise ValueError("accumulate needs dw")
     s_y = _strided(dy, (p.tokens, p.k), p._tdtype, None, "dy")
     dev = dy.device
     s_x = _strided(x, (p.tokens, p.c), p._tdtype, dev, "x")
@@ -237,6 +228,88 @@ def expert_bwd_weight(p: ExpertPlan, dy, x, ends, dw=None, accumulate=False, str
                                           dw.data_ptr(), 1 if accumulate else 0, _strides(s_x, s_y, s_w),
                                           _handle(stream, dev)), "cbd_expert_bwd_weight")
     return dw
+
+
+def _records(a, b):
+    """Whether autograd would record a product of a and b, or carry their
+    tangents through it."""
+    import torch
+
+    if torch.is_grad_enabled() and (getattr(a, "requires_grad", False) or getattr(b, "requires_grad", False)):
+        return True
+    forward = torch.autograd.forward_ad
+    return forward._current_level >= 0 and any(
+        isinstance(t, torch.Tensor) and forward.unpack_dual(t).tangent is not None for t in (a, b))
+
+
+@functools.lru_cache(None)
+def _recorder():
+    import torch
+
+    class ExpertProduct(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, p, op, a, b, ends):
+            ctx.plan, ctx.op = p, op
+            need_a, need_b = ctx.needs_input_grad[2:4]
+            ctx.save_for_backward(a if need_b else None, b if need_a else None, ends)
+            if op == BWD_WEIGHT:
+                return _weight(p, a, b, ends, None, False, None)
+            return _product(p, op, a, b, ends, None, None)
+
+        @staticmethod
+        def backward(ctx, g):
+            p, op = ctx.plan, ctx.op
+            a, b, ends = ctx.saved_tensors
+            need_a, need_b = ctx.needs_input_grad[2:4]
+            # An f32 weight gradient's gradient becomes an operand of the next products.
+            g = g.to(p._tdtype).contiguous()
+            ga = gb = None
+            if op == FORWARD:       # x, w
+                ga = expert_bwd_data(p, g, b, ends) if need_a else None
+                gb = expert_bwd_weight(p, g, a, ends).to(p._tdtype) if need_b else None
+            elif op == BWD_DATA:    # dy, w
+                ga = expert_forward(p, g, b, ends) if need_a else None
+                gb = expert_bwd_weight(p, a, g, ends).to(p._tdtype) if need_b else None
+            else:                   # dy, x
+                ga = expert_forward(p, b, g, ends) if need_a else None
+                gb = expert_bwd_data(p, a, g, ends) if need_b else None
+            return None, None, ga, gb, None
+
+    return ExpertProduct
+
+
+def _recorded(p, op, a, b, ends, out, stream):
+    if out is not None:
+        raise ValueError("autograd cannot record a call into a given output: an operand requires gradients "
+                         "(or has a tangent); leave the output out or call under torch.no_grad()")
+    # The node belongs to the call's stream, so that its backward runs there.
+    with _on(a.device, stream) if a.is_cuda else _HERE:
+        return _recorder().apply(p, op, a, b, ends)
+
+
+def expert_forward(p: ExpertPlan, x, w, ends, y=None, stream=None):
+    """y[t] = W_e x[t] on `stream` (default: torch's current one); y is
+    allocated unless given, and returned."""
+    if _records(x, w):
+        return _recorded(p, FORWARD, x, w, ends, y, stream)
+    return _product(p, FORWARD, x, w, ends, y, stream)
+
+
+def expert_bwd_data(p: ExpertPlan, dy, w, ends, dx=None, stream=None):
+    """dx[t] = W_e^T dy[t]."""
+    if _records(dy, w):
+        return _recorded(p, BWD_DATA, dy, w, ends, dx, stream)
+    return _product(p, BWD_DATA, dy, w, ends, dx, stream)
+
+
+def expert_bwd_weight(p: ExpertPlan, dy, x, ends, dw=None, accumulate=False, stream=None):
+    """dW_e = sum over the rows of e of dy[t] x[t]^T, in the layout of W;
+    accumulate: added to the given dw."""
+    if accumulate and dw is None:
+        raise ValueError("accumulate needs dw")
+    if _records(dy, x):
+        return _recorded(p, BWD_WEIGHT, dy, x, ends, dw, stream)
+    return _weight(p, dy, x, ends, dw, accumulate, stream)
 
 
 _plans = {}
@@ -261,7 +334,7 @@ def _cached(tokens, w_shape, w_layout, tdtype, dw_dtype):
 
 
 def expert_linear(x, w, ends, w_layout="ekc"):
-    """y[t] = W_e x[t] for x [T, C], w [E, K, C] or [E, C, K]."""
+    """y[t] = W_e x[t] for x [T, C], w [E, K, C] or [E, C, K]; differentiable."""
     p = _cached(x.shape[0], tuple(w.shape), w_layout, w.dtype, None)
     return expert_forward(p, x, w, ends)
 
