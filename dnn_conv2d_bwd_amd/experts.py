@@ -174,6 +174,14 @@ def _on(device, stream):
     return torch.cuda.stream(stream)
 
 
+def _written(tensors):
+    """Tells autograd that the library writes into tensors of the caller's, so
+    that a backward pass that saved one of them refuses the new contents."""
+    import torch
+
+    torch.autograd.graph.increment_version(tensors)
+
+
 def _ends(p, ends, device):
     import torch
 
@@ -204,8 +212,10 @@ def _product(p, op, rows, w, ends, out, stream):
     bits = _ends(p, ends, dev)
     with _on(dev, stream):
         if out is None:
-            out = torch.empty((p.tokens, wide_out), dtype=p._tdtype, device=dev)
-        s_out = _strided(out, (p.tokens, wide_out), p._tdtype, dev, out_name)
+            out, s_out = torch.empty((p.tokens, wide_out), dtype=p._tdtype, device=dev), _DENSE[2]
+        else:
+            s_out = _strided(out, (p.tokens, wide_out), p._tdtype, dev, out_name)
+            _written(out)
         st = _strides(s_in, s_out, s_w) if fwd else _strides(s_out, s_in, s_w)
         f = _lib.cbd_expert_forward if fwd else _lib.cbd_expert_bwd_data
         _check(f(p._h[bits], rows.data_ptr(), w.data_ptr(), ends.data_ptr(), out.data_ptr(), st,
@@ -222,8 +232,10 @@ def _weight(p, dy, x, ends, dw, accumulate, stream):
     bits = _ends(p, ends, dev)
     with _on(dev, stream):
         if dw is None:
-            dw = torch.empty(p.w_shape, dtype=p._tdw, device=dev)
-        s_w = _strided(dw, p.w_shape, p._tdw, dev, "dw")
+            dw, s_w = torch.empty(p.w_shape, dtype=p._tdw, device=dev), _DENSE[3]
+        else:
+            s_w = _strided(dw, p.w_shape, p._tdw, dev, "dw")
+            _written(dw)
         _check(_lib.cbd_expert_bwd_weight(p._h[bits], dy.data_ptr(), x.data_ptr(), ends.data_ptr(),
                                           dw.data_ptr(), 1 if accumulate else 0, _strides(s_x, s_y, s_w),
                                           _handle(stream, dev)), "cbd_expert_bwd_weight")

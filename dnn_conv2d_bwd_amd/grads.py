@@ -7,7 +7,8 @@
 
 `clip_grad_norm(grads, max_norm)` makes the plan itself.  f32 and bf16
 tensors may be mixed; each must be dense (any order of its dimensions).  The
-norm stays on the GPU: nothing here waits for it.  include/cbd.h states the
+norm stays on the GPU: nothing here waits for it.  Nothing is recorded by
+autograd; tensors that are written to count as changed in place.  include/cbd.h states the
 operation in full.
 """
 from __future__ import annotations
@@ -15,7 +16,7 @@ from __future__ import annotations
 import ctypes
 
 from . import BF16, F32, _check, _lib
-from .experts import _handle, _on
+from .experts import _handle, _on, _written
 
 
 def _bind():
@@ -129,10 +130,14 @@ def _scratch(p, norm, workspace, device):
         norm = torch.empty((), dtype=torch.float32, device=device)
     elif norm.dtype != torch.float32 or norm.numel() != 1 or norm.device != device:
         raise ValueError(f"norm must be one float32 on {device}")
+    else:
+        _written(norm)
     if workspace is None:
         workspace = torch.empty(p._ws, dtype=torch.uint8, device=device)
     elif not workspace.is_contiguous() or workspace.device != device:
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    else:
+        _written(workspace)
     return norm, workspace
 
 
@@ -167,6 +172,9 @@ def clip_grads(p: GradPlan, grads, max_norm, out=None, norm=None, workspace=None
             for i, (g, o) in enumerate(zip(grads, out)):
                 if g.shape != o.shape or (g.stride() != o.stride() and not (g.is_contiguous() and o.is_contiguous())):
                     raise ValueError(f"output {i} is laid out unlike its gradient")
+            _written(out)
+        else:
+            _written(grads)
         _check(_lib.cbd_grad_clip(p._h, ptrs, optrs, float(max_norm), norm.data_ptr(), ws.data_ptr(),
                                   ws.numel() * ws.element_size(), _handle(stream, dev)), "cbd_grad_clip")
     return norm if out is None else (norm, out)
