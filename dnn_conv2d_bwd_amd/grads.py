@@ -79,7 +79,7 @@ class GradPlan:
 
 def grad_plan(grads) -> GradPlan:
     """Plan for tensors of these sizes and types (their addresses are not kept)."""
-    types = _types()
+    grads, types = list(grads), _types()
     for i, g in enumerate(grads):
         if g.dtype not in types:
             raise ValueError(f"gradient {i} has dtype {g.dtype}; float32 and bfloat16 are supported")
