@@ -109,9 +109,9 @@ struct RowTiles {
     r.ok = r.begin < r.end;
     if (r.end - r.begin > most) r.end = r.begin + most;
   }
-  // Tile of hardware workgroup b.  g > 0: workgroups take b, b + g, ...; where
-  // the last round's tiles are at most g / 2, each is taken as two halves of
-  // its rows.
+  // Tile of hardware workgroup b.  g > 0: of workgroups that take b, b + g, ...
+  // (g a multiple of 256, or as many as there are tiles); where the last
+  // round's tiles are at most g / 2, each is taken as two halves of its rows.
   CBD_INLINE __device__ ExpertTile at(const ExpertArgs& a, int64_t b, int bn, int g = 0) {
     ExpertTile r;
     int half = -1;
