@@ -78,7 +78,9 @@ ExpertLaunch choose(const cbd_expert_plan_s& plan, int op, bool narrow_strides, 
   };
   l.kernel = plan.opt.force_kernel;
   // Few rows an expert: 64 experts of 2048 x 1408, stream / mfma in us at 16
-  // rows an expert 92 / 97 (AK) and 68 / 77 (AM), at 32 rows 125 / 98 and 83 / 79.
+  // rows an expert 90 / 95 (AK) and 68 / 77 (AM), at 32 rows 125 / 95 and 83 /
+  // 79.  Experts whose weights the caches hold together are faster on mfma from
+  // fewer rows on (2048 x 1024, AK, the same weights again and again: 57 / 40).
   const int stream_bm = l.form == cbd::EXPERT_AK ? 32 : 128;
   const bool stream_ok = op != CBD_EXPERT_BWD_WEIGHT && narrow_strides && grid(stream_bm, 32) <= kMaxGrid;
   if (l.kernel == CBD_EXPERT_KERNEL_AUTO)
@@ -98,10 +100,11 @@ ExpertLaunch choose(const cbd_expert_plan_s& plan, int op, bool narrow_strides, 
     // k runs along the rows of x (dy), and of W in the AK form.
     l.dma = dma && (op == CBD_EXPERT_BWD_WEIGHT || n % 8 == 0);
     // 256 x 256 tiles where they fill the card twice and, with rows an expert
-    // that vary, their last row tiles are few: 2048 -> 2048 wide, 256 rows an
-    // expert, 142 us against 169 with 128 x 128.  A last feature tile that is
-    // at most half used takes more rows to be worth it (1408 wide: 256 rows
-    // 171 / 160, 512 rows 252 / 280).
+    // that vary, their last row tiles are few (256 / 128 in us, 64 experts of
+    // 2048 inputs: 2048 outputs, 128 rows an expert 173 / 143, 192 rows 171 /
+    // 187, 256 rows 182 / 201; 1024 outputs 99 / 76, 103 / 105, 104 / 109).  A
+    // last feature tile that is at most half used takes more rows to be worth
+    // it (1408 outputs: 256 rows 152 / 149, 384 rows 165 / 192).
     const bool half = (m + 127) / 128 % 2 != 0;
     const bool many = op == CBD_EXPERT_BWD_WEIGHT || p.tokens >= (half ? 384 : 192) * p.experts;
     l.bm = l.bn = l.dma && whole_out && many && grid(256, 256) >= 512 ? 256 : 128;

@@ -85,7 +85,7 @@ __device__ inline void store4(uint16_t* p, f32x4 v, int n, bool add) {
   }
 }
 
-// One operand of a tile: R rows (features or tokens) by 16 k, R = 32 * NB.
+// One operand of a tile: R rows (features or tokens) by BK k, R = 32 * NB.
 // KC: k is contiguous in memory.
 template <typename T, bool KC, int NB, int BK>
 struct Operand {
@@ -151,8 +151,8 @@ struct Operand {
       *(f32x4*)(lds + (idx / QUADS) * ROW + 4 * (idx % QUADS)) = x;
     }
   }
-  // Fragments of a wave's 16 * NB rows from row r0: f[block][i].
-  // of k kb .. kb + 15
+  // Fragments of a wave's 16 * NB rows from row r0, k kb .. kb + 15:
+  // f[block][i].
   CBD_INLINE __device__ static void read(const float* lds, int r0, int kb, float (&f)[NB][4]) {
     const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
     if (KC) {
