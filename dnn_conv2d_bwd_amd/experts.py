@@ -247,7 +247,7 @@ def _records(a, b):
     tangents through it."""
     import torch
 
-    if torch.is_grad_enabled() and (getattr(a, "requires_grad", False) or getattr(b, "requires_grad", False)):
+    if (getattr(a, "requires_grad", False) or getattr(b, "requires_grad", False)) and torch.is_grad_enabled():
         return True
     forward = torch.autograd.forward_ad
     return forward._current_level >= 0 and any(
