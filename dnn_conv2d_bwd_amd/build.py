@@ -35,6 +35,11 @@ SOURCES = [
     "kern_expert_generic.hip",
     "kern_expert_mfma.hip",
     "kern_expert_stream.hip",
+    "gated_api.cpp",
+    "kern_gated_generic.hip",
+    "kern_gated_mfma.hip",
+    "kern_gated_mfma_bwd.hip",
+    "kern_gated_stream.hip",
     "grad_api.cpp",
     "kern_grad_norm.hip",
 ]

@@ -6,53 +6,22 @@
 #include <string>
 
 #include "cbd_internal.h"
+#include "expert_common.h"
 #include "expert_internal.h"
 
 namespace {
 
 using cbd::ExpertArgs;
 using cbd::ExpertLaunch;
-
-cbd_status fail(cbd_status s, const char* msg) {
-  cbd::set_error(msg);
-  return s;
-}
-
-int esize(int dtype) { return dtype == CBD_F32 ? 4 : 2; }
-
-// A 2-D (or, with count > 1, 3-D) strided block of memory.
-struct Block {
-  const void* p;
-  int64_t rows, width, ld;   // elements
-  int64_t count, stride;     // slices
-  int es;
-  uint64_t span() const {
-    if (rows <= 0 || count <= 0) return 0;
-    return (uint64_t)((count - 1) * stride + (rows - 1) * ld + width) * es;
-  }
-};
-
-// Whether two blocks share a byte.  Column slices of one buffer (the same row
-// pitch, no slices) are told apart; otherwise the whole spans count.
-bool share(const Block& a, const Block& b) {
-  const uint64_t sa = a.span(), sb = b.span();
-  if (!sa || !sb) return false;
-  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-  if (!(x < y + sb && y < x + sa)) return false;
-  if (a.count == 1 && b.count == 1 && a.ld * a.es == b.ld * b.es) {
-    const uint64_t pitch = (uint64_t)a.ld * a.es, wa = (uint64_t)a.width * a.es, wb = (uint64_t)b.width * b.es;
-    const uint64_t d = x <= y ? (y - x) % pitch : (pitch - (x - y) % pitch) % pitch;
-    if (d >= wa && d + wb <= pitch) return false;
-  }
-  return true;
-}
-
-constexpr int64_t kMaxSlice = int64_t(1) << 31;  // bytes: offsets within a slice or tile are 32-bit
-
-// Threads of a workgroup, and the most workgroups of a launch (a grid has fewer
-// than 2^32 threads).
-constexpr int kThreads = 256;
-constexpr int64_t kMaxGrid = UINT32_MAX / kThreads;
+using cbd::host::Block;
+using cbd::host::esize;
+using cbd::host::fail;
+using cbd::host::guarded;
+using cbd::host::kMaxGrid;
+using cbd::host::kMaxSlice;
+using cbd::host::kThreads;
+using cbd::host::on16;
+using cbd::host::share;
 
 // Launch of an operator.  narrow_strides: 256 rows of either input stay within
 // 32-bit offsets; dma: and both start every row on a 16-byte boundary;
@@ -183,9 +152,6 @@ cbd_status run(const cbd_expert_plan_t* plan, int op, const void* row_in, const 
     return CBD_OK;
   }
 
-  auto on16 = [](const Block& b) {
-    return (((uintptr_t)b.p | (uint64_t)(b.ld * b.es) | (uint64_t)(b.count > 1 ? b.stride * b.es : 0)) & 15u) == 0;
-  };
   const bool whole_out = on16(bo) && bo.width % (16 / bo.es) == 0;
   bool dma = true, narrow_strides = true;
   for (const Block* b : {&bx, &by, &bw})
@@ -238,16 +204,6 @@ cbd_status run(const cbd_expert_plan_t* plan, int op, const void* row_in, const 
   }
   cbd::set_error("");
   return CBD_OK;
-}
-
-// Runs f, turning a C++ exception (the error string's allocation) into a status.
-template <typename F>
-cbd_status guarded(F&& f) {
-  try {
-    return f();
-  } catch (...) {
-    return CBD_ERR_NO_MEMORY;
-  }
 }
 
 cbd_status make_plan(const cbd_expert_problem* q, const cbd_expert_options* opt, cbd_expert_plan_t** out) {

@@ -441,6 +441,57 @@ cbd_status cbd_expert_bwd_weight(const cbd_expert_plan_t* plan, const void* dy, 
                                  const void* ends, void* dw, int32_t accumulate,
                                  const cbd_expert_strides* strides, void* stream);
 
+/* ---- gated experts: both projections, activation and product ----
+ *
+ * The block of an expert e with G_e and U_e (K x C each) before and D_e
+ * (C x K) behind:  y[t] = D_e (act(G_e x[t]) * (U_e x[t])), rows t of e.
+ *
+ *   gated_forward  g = G_e x[t], u = U_e x[t],  h[t] = act(g) * u
+ *                  and, with gu, gu[t] = (g, u): g in the first K columns
+ *   gated_bwd      dh = D_e^T dy[t],
+ *                  dgu[t] = (dh * u * act'(g), dh * act(g)), (g, u) = gu[t]
+ *
+ * y = D_e h is cbd_expert_forward; with dgu, the gradients of x and of the
+ * two projections are cbd_expert_bwd_data and cbd_expert_bwd_weight of the
+ * projections' plan, and D's is cbd_expert_bwd_weight of dy and h.
+ *
+ * The projections are one plan with k = 2 K: W [E][2 K][C] with the gate's
+ * rows first, or [E][C][2 K] with its columns first.  gated_bwd takes the
+ * plan of D: c = K, k = C.  Row ranges, rows past the last expert (+0 in h, gu
+ * and dgu), sums, strides, capture and independence of rows are as for the
+ * expert calls.  act and the products are computed in f32 from the f32 sums
+ * (gated_bwd: from gu as it is stored); h, gu and dgu are rounded once. */
+typedef enum {
+  CBD_ACT_SILU = 0, /* g / (1 + exp(-g)) */
+  CBD_ACT_GELU = 1, /* g / 2 * (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+  CBD_ACT_RELU = 2  /* max(g, 0); its derivative at 0 is 0 */
+} cbd_activation;
+
+/* Row and expert strides in elements; 0 (or a NULL pointer): dense. */
+typedef struct {
+  int64_t in_row;   /* x (forward) or dy (bwd) */
+  int64_t h_row;    /* h (forward) */
+  int64_t gu_row;   /* gu */
+  int64_t dgu_row;  /* dgu (bwd) */
+  int64_t w_row;    /* W: between the rows of one expert */
+  int64_t w_expert; /* W: between experts */
+} cbd_gated_strides;
+
+/* gu of the forward call may be NULL: it is not written then.  Errors as for
+ * the expert calls, plus INVALID_ARG for an unknown act and a forward plan with
+ * odd k, and UNSUPPORTED for a plan with a forced kernel that does not take
+ * the call (gated_bwd has no stream kernel and runs the MFMA one). */
+cbd_status cbd_expert_gated_forward(const cbd_expert_plan_t* plan, const void* x, const void* w,
+                                    const void* ends, void* h, void* gu, int32_t act,
+                                    const cbd_gated_strides* strides, void* stream);
+cbd_status cbd_expert_gated_bwd(const cbd_expert_plan_t* plan, const void* dy, const void* w,
+                                const void* gu, const void* ends, void* dgu, int32_t act,
+                                const cbd_gated_strides* strides, void* stream);
+
+/* What a call on dense, 16-byte aligned tensors launches (tile_m: features of
+ * h); bwd: 0 or 1. */
+cbd_status cbd_expert_gated_info(const cbd_expert_plan_t* plan, int32_t bwd, cbd_expert_info_t* out);
+
 /* ---- global gradient norm and clipping over a list of tensors ----
  *
  *   norm  = sqrt( sum over every element g of every tensor of g^2 )
