@@ -16,7 +16,7 @@ layout)` mirrors torch's convolution_backward with output_mask
 and allocates dX.
 
 Next to it: the expert layer (ragged products grouped by expert and their
-gradients, experts.py), gated experts (gated.py) and the global gradient norm with clipping (grads.py).
+gradients, experts.py), gated experts (gated.py), the norms around a block (blocks.py) and the global gradient norm with clipping (grads.py).
 
 If libcbd.so is missing, importing this module raises ImportError: there is
 no fallback path.
@@ -44,6 +44,8 @@ EXPORTS = ("cbd_plan", "cbd_plan_ex", "cbd_run", "cbd_run_ws", "cbd_run_noalloc"
            "cbd_expert_plan", "cbd_expert_plan_destroy", "cbd_expert_plan_info", "cbd_expert_forward",
            "cbd_expert_bwd_data", "cbd_expert_bwd_weight",
            "cbd_expert_gated_forward", "cbd_expert_gated_bwd", "cbd_expert_gated_info",
+           "cbd_block_plan", "cbd_block_plan_destroy", "cbd_block_workspace_size", "cbd_block_forward",
+           "cbd_block_bwd",
            "cbd_grad_plan", "cbd_grad_plan_destroy", "cbd_grad_workspace_size", "cbd_grad_norm",
            "cbd_grad_clip")
 
@@ -343,6 +345,8 @@ from .experts import (ECK, EKC, EXPERT_KERNEL_AUTO, EXPERT_KERNEL_GENERIC, EXPER
                       EXPERT_KERNEL_NAMES, BWD_DATA, BWD_WEIGHT, FORWARD, ExpertInfo, ExpertOptions,
                       ExpertPlan, ExpertProblem, ExpertStrides, expert_bwd_data, expert_bwd_weight,
                       expert_forward, expert_linear, expert_linear_bwd, expert_plan)
+from .blocks import (GATE_CHANNEL, GATE_NONE, GATE_ROW, BlockGrads, BlockParams, BlockPlan,  # noqa: E402,F401
+                     BlockProblem, BlockStrides, block_bwd, block_forward, block_norm, block_plan)
 from .gated import (ACT_GELU, ACT_RELU, ACT_SILU, GatedStrides, expert_ffn, expert_gated_bwd,  # noqa: E402,F401
                     expert_gated_forward, expert_gated_info)
 from .grads import GradPlan, clip_grad_norm, clip_grads, grad_norm, grad_plan  # noqa: E402,F401

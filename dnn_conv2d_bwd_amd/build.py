@@ -40,6 +40,8 @@ SOURCES = [
     "kern_gated_mfma.hip",
     "kern_gated_mfma_bwd.hip",
     "kern_gated_stream.hip",
+    "block_api.cpp",
+    "kern_block_norm.hip",
     "grad_api.cpp",
     "kern_grad_norm.hip",
 ]

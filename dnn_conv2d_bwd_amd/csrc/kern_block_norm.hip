@@ -1,0 +1,451 @@
+// kern_block_norm.hip -- the norms around a block, with its gate and residual.
+//
+//   yn = y * ry,  ry = 1 / sqrt(mean y^2 + eps)      (y itself where it is not normed)
+//   z  = r + scale * gate * w_post * yn
+//   zn = z * rz,  rz = 1 / sqrt(mean z^2 + eps),     n = w_pre * zn
+//
+// Backward, with v = w_pre * dn and c = scale * gate * w_post:
+//   dz' = dz + rz * (v - zn * S1 / C)                S1 = sum v * zn
+//   dr = dz',  q = c * dz',  dy = ry * (q - yn * S2 / C),  S2 = sum q * yn
+// S2 = sum c * yn * (dz + rz * v) - rz * S1 / C * sum c * yn * zn, so that the
+// three sums of a row come from one round over its threads.  The vectors'
+// gradients need sum dn * zn and sum scale * dz' * yn over the rows: w_post and
+// a gate vector are factors of the second that a column shares.
+//
+// A row stays in registers from its one load to its stores; a workgroup (or,
+// up to 1024 bf16 a row, a wave) takes rows i, i + grid, ..., loads the next one
+// before it joins the sums of this one, and keeps its columns' sums in
+// registers to the end.  z is rounded where it is stored, not where n is made
+// of it.
+//
+// Bound: HBM.
+#include <type_traits>
+
+#include "block_internal.h"
+#include "cbd_device.h"
+
+namespace cbd {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4_2 __attribute__((ext_vector_type(4), aligned(2)));
+
+// A 16-byte chunk of a row, as it lies in memory.
+template <typename T>
+struct Chunk {
+  static constexpr int N = 16 / sizeof(T);
+  using any = std::conditional_t<sizeof(T) == 4, u32x4_4, u32x4_2>;
+  u32x4 v;
+  __device__ inline void zero() { v = u32x4{0u, 0u, 0u, 0u}; }
+  // The first n of its elements (n <= 0: none) from p, zeros after them.
+  __device__ inline void load(const T* p, int n) {
+    if (n >= N) {
+      v = *(const any*)p;
+      return;
+    }
+    zero();
+#pragma unroll
+    for (int j = 0; j < N - 1; j++)
+      if (j < n) {
+        if constexpr (sizeof(T) == 4)
+          v[j] = ((const uint32_t*)p)[j];
+        else
+          v[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+      }
+  }
+  __device__ inline void store(T* p, int n) const {
+    if (n >= N) {
+      *(any*)p = v;
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < N - 1; j++)
+      if (j < n) {
+        if constexpr (sizeof(T) == 4)
+          ((uint32_t*)p)[j] = v[j];
+        else
+          p[j] = (T)(v[j >> 1] >> (16 * (j & 1)));
+      }
+  }
+  __device__ inline float get(int j) const {
+    if constexpr (sizeof(T) == 4)
+      return __uint_as_float(v[j]);
+    else
+      return j & 1 ? __uint_as_float(v[j >> 1] & 0xffff0000u) : __uint_as_float(v[j >> 1] << 16);
+  }
+  __device__ inline void put(const float (&f)[N]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int j = 0; j < 4; j++) v[j] = __float_as_uint(f[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; j++) v[j] = dev::bf16_pack2(f[2 * j], f[2 * j + 1]);
+    }
+  }
+};
+
+// Sum over a wave, for everyone: shifts within rows of 16 lanes, the rows' last
+// lanes into the next ones, and the last lane's value.
+__device__ inline float wave_sum(float v) {
+  auto plus = [&](int moved) { v += __int_as_float(moved); };
+  plus(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x111, 0xf, 0xf, false));  // row_shr:1
+  plus(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x112, 0xf, 0xf, false));
+  plus(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x114, 0xf, 0xf, false));
+  plus(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x118, 0xf, 0xf, false));
+  plus(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x142, 0xa, 0xf, false));  // row_bcast:15
+  plus(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x143, 0xc, 0xf, false));  // row_bcast:31
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+// Sums over a row's threads, in a fixed order, for everyone.  Two buffers, so
+// that one barrier is enough: who writes a buffer again has passed the other's
+// barrier, before which everyone has read it.
+template <int LANES, int S>
+struct RowSum {
+  float (*part)[LANES / 64][S];
+  int at = 0;
+  __device__ inline void operator()(float (&s)[S]) {
+#pragma unroll
+    for (int i = 0; i < S; i++) s[i] = wave_sum(s[i]);
+    if constexpr (LANES > 64) {
+      if ((threadIdx.x & 63) == 0)
+#pragma unroll
+        for (int i = 0; i < S; i++) part[at][threadIdx.x >> 6][i] = s[i];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < S; i++) s[i] = 0.f;
+#pragma unroll
+      for (int w = 0; w < LANES / 64; w++)
+#pragma unroll
+        for (int i = 0; i < S; i++) s[i] += part[at][w][i];
+      at ^= 1;
+    }
+  }
+};
+
+template <int LANES>
+constexpr int kThreads = LANES == 64 ? 256 : LANES;
+// Waves a SIMD: 128 registers (1024 threads have no more) where a thread has
+// one chunk.
+template <int CH>
+constexpr int kWaves = CH == 1 ? 4 : 1;
+// The next row is loaded ahead; with more chunks a thread has no room for it.
+template <int CH>
+constexpr bool kAhead = CH == 1;
+
+// What a thread has of its rows: CH chunks, LANES chunks apart.
+template <typename T, int LANES, int CH>
+struct Rows {
+  static constexpr int N = Chunk<T>::N;
+  int lane, n[CH];  // elements of each chunk that are inside (negative: none)
+  int64_t row, step;
+  __device__ inline explicit Rows(const BlockArgs& a) {
+    lane = LANES == 64 ? threadIdx.x & 63 : threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < CH; i++) n[i] = a.c - N * (lane + LANES * i);
+    const int sub = LANES == 64 ? __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) : 0;
+    constexpr int per = LANES == 64 ? 4 : 1;
+    row = (int64_t)blockIdx.x * per + sub;
+    step = (int64_t)gridDim.x * per;
+  }
+  __device__ inline void load(Chunk<T> (&v)[CH], const void* p, int64_t at) const {
+    const T* q = (const T*)p + at + N * lane;
+#pragma unroll
+    for (int i = 0; i < CH; i++) v[i].load(q + N * LANES * i, n[i]);
+  }
+  __device__ inline void store(const Chunk<T> (&v)[CH], void* p, int64_t at) const {
+    T* q = (T*)p + at + N * lane;
+#pragma unroll
+    for (int i = 0; i < CH; i++) v[i].store(q + N * LANES * i, n[i]);
+  }
+  __device__ inline static void zero(Chunk<T> (&v)[CH]) {
+#pragma unroll
+    for (int i = 0; i < CH; i++) v[i].zero();
+  }
+};
+
+__device__ inline float inverse_rms(float squares, const BlockArgs& a) {
+  return 1.f / __builtin_sqrtf(squares / (float)a.c + a.eps);
+}
+
+template <typename T, int LANES, int CH>
+__global__ __launch_bounds__(kThreads<LANES>, kWaves<CH>) void block_forward_kernel(const BlockArgs a) {
+  constexpr int N = Chunk<T>::N;
+  __shared__ float part[2][LANES / 64][1];
+  RowSum<LANES, 1> sum{part};
+  Rows<T, LANES, CH> rows(a);
+  Chunk<T> wq[CH], gq[CH], wp[CH];  // w_post, gate, w_pre
+  Rows<T, LANES, CH>::zero(gq);
+  if (a.w_post) rows.load(wq, a.w_post, 0);
+  if (a.gate && !a.gate_rows) rows.load(gq, a.gate, 0);
+  if (a.w_pre) rows.load(wp, a.w_pre, 0);
+  Chunk<T> r[CH], y[CH], g[CH];
+  auto fetch = [&](int64_t row) {
+    rows.load(r, a.r, row * a.ldr);
+    if (a.y) rows.load(y, a.y, row * a.ldy);
+    if (a.gate_rows) rows.load(g, a.gate, row * a.ldgate);
+  };
+  if (kAhead<CH> && rows.row < a.rows) fetch(rows.row);
+  for (int64_t row = rows.row; row < a.rows; row += rows.step) {
+    if (!kAhead<CH>) fetch(row);
+    float z[CH][N], v[CH][N];
+#pragma unroll
+    for (int i = 0; i < CH; i++)
+#pragma unroll
+      for (int j = 0; j < N; j++) {
+        z[i][j] = r[i].get(j);
+        v[i][j] = a.y ? y[i].get(j) : 0.f;
+      }
+    float s[1] = {0.f};
+    // What the gate, the weight and the scale make of y.
+    Chunk<T> gr[CH];
+#pragma unroll
+    for (int i = 0; i < CH; i++) gr[i] = a.gate_rows ? g[i] : gq[i];
+    if (kAhead<CH> && row + rows.step < a.rows) fetch(row + rows.step);
+    float ry = 1.f, rz = 1.f;
+    if (a.w_post) {
+#pragma unroll
+      for (int i = 0; i < CH; i++)
+#pragma unroll
+        for (int j = 0; j < N; j++) s[0] = __builtin_fmaf(v[i][j], v[i][j], s[0]);
+      sum(s);
+      ry = inverse_rms(s[0], a);
+    }
+    s[0] = 0.f;
+#pragma unroll
+    for (int i = 0; i < CH; i++)
+#pragma unroll
+      for (int j = 0; j < N; j++) {
+        float t = v[i][j];
+        if (a.w_post) t = t * ry * wq[i].get(j);
+        if (a.gate) t *= gr[i].get(j);
+        if (a.y) z[i][j] = __builtin_fmaf(a.scale, t, z[i][j]);
+        s[0] = __builtin_fmaf(z[i][j], z[i][j], s[0]);
+      }
+    if (a.z) {
+      Chunk<T> o[CH];
+#pragma unroll
+      for (int i = 0; i < CH; i++) o[i].put(z[i]);
+      rows.store(o, a.z, row * a.ldz);
+    }
+    if (a.w_pre) {
+      sum(s);
+      rz = inverse_rms(s[0], a);
+      Chunk<T> o[CH];
+#pragma unroll
+      for (int i = 0; i < CH; i++) {
+        float f[N];
+#pragma unroll
+        for (int j = 0; j < N; j++) f[j] = z[i][j] * rz * wp[i].get(j);
+        o[i].put(f);
+      }
+      rows.store(o, a.n, row * a.ldn);
+    }
+    if (a.stats && rows.lane == 0) {
+      a.stats[2 * row] = ry;
+      a.stats[2 * row + 1] = rz;
+    }
+  }
+}
+
+template <typename T, int LANES, int CH>
+__global__ __launch_bounds__(kThreads<LANES>, kWaves<CH>) void block_bwd_kernel(const BlockArgs a) {
+  constexpr int N = Chunk<T>::N;
+  __shared__ float part[2][LANES / 64][3];
+  RowSum<LANES, 3> sum{part};
+  Rows<T, LANES, CH> rows(a);
+  Chunk<T> wq[CH], gq[CH], wp[CH];
+  Rows<T, LANES, CH>::zero(gq);
+  if (a.w_post) rows.load(wq, a.w_post, 0);
+  if (a.gate && !a.gate_rows) rows.load(gq, a.gate, 0);
+  if (a.w_pre) rows.load(wp, a.w_pre, 0);
+  float pre[CH][N], post[CH][N];  // the columns' sums
+#pragma unroll
+  for (int i = 0; i < CH; i++)
+#pragma unroll
+    for (int j = 0; j < N; j++) pre[i][j] = post[i][j] = 0.f;
+  Chunk<T> r[CH], y[CH], g[CH], dz[CH], dn[CH];
+  float ry1 = 1.f, rz1 = 1.f;
+  Rows<T, LANES, CH>::zero(y);
+  Rows<T, LANES, CH>::zero(dz);
+  Rows<T, LANES, CH>::zero(dn);
+  auto fetch = [&](int64_t row) {
+    rows.load(r, a.r, row * a.ldr);
+    if (a.y) rows.load(y, a.y, row * a.ldy);
+    if (a.dz) rows.load(dz, a.dz, row * a.lddz);
+    if (a.dn) rows.load(dn, a.dn, row * a.lddn);
+    if (a.gate_rows) rows.load(g, a.gate, row * a.ldgate);
+    if (a.w_post) ry1 = a.stats[2 * row];
+    if (a.w_pre) rz1 = a.stats[2 * row + 1];
+  };
+  if (kAhead<CH> && rows.row < a.rows) fetch(rows.row);
+  const float inv_c = 1.f / (float)a.c;
+  for (int64_t row = rows.row; row < a.rows; row += rows.step) {
+    if (!kAhead<CH>) fetch(row);
+    const float ry = ry1, rz = rz1;
+    float zn[CH][N], yn[CH][N], e[CH][N];
+    float s[3] = {0.f, 0.f, 0.f};
+    Chunk<T> gr[CH];
+#pragma unroll
+    for (int i = 0; i < CH; i++) gr[i] = a.gate_rows ? g[i] : gq[i];
+#pragma unroll
+    for (int i = 0; i < CH; i++)
+#pragma unroll
+      for (int j = 0; j < N; j++) {
+        const float d = dn[i].get(j);
+        yn[i][j] = y[i].get(j) * ry;
+        float c = a.scale;
+        if (a.w_post) c *= wq[i].get(j);
+        if (a.gate) c *= gr[i].get(j);
+        const float cy = c * yn[i][j];
+        zn[i][j] = (r[i].get(j) + cy) * rz;
+        const float v = a.w_pre ? d * wp[i].get(j) : 0.f;
+        e[i][j] = __builtin_fmaf(rz, v, dz[i].get(j));
+        pre[i][j] = __builtin_fmaf(d, zn[i][j], pre[i][j]);
+        s[0] = __builtin_fmaf(v, zn[i][j], s[0]);
+        s[1] = __builtin_fmaf(cy, e[i][j], s[1]);
+        s[2] = __builtin_fmaf(cy, zn[i][j], s[2]);
+      }
+    if (kAhead<CH> && row + rows.step < a.rows) fetch(row + rows.step);
+    sum(s);
+    const float along = rz * s[0] * inv_c;           // of zn in dz'
+    const float back = (s[1] - along * s[2]) * inv_c;  // of yn in dy
+    Chunk<T> o_r[CH], o_y[CH], o_g[CH];
+#pragma unroll
+    for (int i = 0; i < CH; i++) {
+      float fr[N], fy[N], fg[N];
+#pragma unroll
+      for (int j = 0; j < N; j++) {
+        fr[j] = __builtin_fmaf(-along, zn[i][j], e[i][j]);
+        const float da = a.scale * fr[j];
+        const float gate = a.gate ? gr[i].get(j) : 1.f;
+        const float w = a.w_post ? wq[i].get(j) : 1.f;
+        fg[j] = da * yn[i][j] * w;
+        const float dg = da * gate;
+        post[i][j] = __builtin_fmaf(a.gate_rows ? dg : da, yn[i][j], post[i][j]);
+        fy[j] = a.w_post ? ry * __builtin_fmaf(-back, yn[i][j], dg * w) : dg;
+      }
+      o_r[i].put(fr);
+      o_y[i].put(fy);
+      o_g[i].put(fg);
+    }
+    if (a.dr) rows.store(o_r, a.dr, row * a.lddr);
+    if (a.dy) rows.store(o_y, a.dy, row * a.lddy);
+    if (a.dgate) rows.store(o_g, a.dgate, row * a.lddgate);
+  }
+  if (!a.partial) return;
+  float* const out = a.partial + (int64_t)blockIdx.x * 2 * a.c;
+  if constexpr (LANES == 64) {
+    // The four waves' sums, joined in their order.
+    __shared__ float join[2][3][CH * N][64];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    if (wave > 0) {
+#pragma unroll
+      for (int i = 0; i < CH; i++)
+#pragma unroll
+        for (int j = 0; j < N; j++) {
+          join[0][wave - 1][i * N + j][lane] = pre[i][j];
+          join[1][wave - 1][i * N + j][lane] = post[i][j];
+        }
+    }
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int w = 0; w < 3; w++)
+#pragma unroll
+      for (int i = 0; i < CH; i++)
+#pragma unroll
+        for (int j = 0; j < N; j++) {
+          pre[i][j] += join[0][w][i * N + j][lane];
+          post[i][j] += join[1][w][i * N + j][lane];
+        }
+  }
+#pragma unroll
+  for (int i = 0; i < CH; i++) {
+    const int at = N * (rows.lane + LANES * i);
+#pragma unroll
+    for (int j = 0; j < N; j++)
+      if (at + j < a.c) {
+        out[at + j] = pre[i][j];
+        out[a.c + at + j] = post[i][j];
+      }
+  }
+}
+
+// 64 columns by 16 slices of the workgroups' sums, which are joined in 64 bits.
+constexpr int FINISH = 1024;
+__global__ __launch_bounds__(FINISH) void block_finish_kernel(const BlockFinish a) {
+  __shared__ double part[FINISH / 64][64];
+  const int lane = threadIdx.x & 63, slice = threadIdx.x >> 6;
+  const int col = blockIdx.x * 64 + lane, which = blockIdx.y;
+  double s = 0.0;
+  if (col < a.c) {
+    const float* p = a.partial + (int64_t)which * a.c + col;
+#pragma unroll 8
+    for (int i = slice; i < a.n; i += FINISH / 64) s += (double)p[(int64_t)i * 2 * a.c];
+  }
+  part[slice][lane] = s;
+  __syncthreads();
+  if (slice > 0 || col >= a.c) return;
+#pragma unroll
+  for (int i = 1; i < FINISH / 64; i++) s += part[i][lane];
+  auto vector = [&](const void* v) {
+    return !v ? 1.0 : (double)(a.dtype == CBD_F32 ? ((const float*)v)[col] : dev::bf16_to_f32(((const uint16_t*)v)[col]));
+  };
+  auto put = [&](void* o, double v) {
+    if (!o) return;
+    if (a.dw_dtype == CBD_F32)
+      ((float*)o)[col] = (float)v;
+    else
+      ((uint16_t*)o)[col] = (uint16_t)dev::bf16_rne((float)v);
+  };
+  if (which == 0) {
+    put(a.dw_pre, s);
+  } else {
+    put(a.dw_post, s * vector(a.gate));
+    put(a.dgate, s * vector(a.w_post));
+  }
+}
+
+template <typename T, bool BWD>
+const void* pick(BlockShape s) {
+  constexpr int F = sizeof(T) / 2;
+#define CBD_BLOCK(L, C) \
+  if (s.lanes == L && s.chunks == C) return BWD ? (const void*)&block_bwd_kernel<T, L, C> : (const void*)&block_forward_kernel<T, L, C>;
+  CBD_BLOCK(64, 1)
+  CBD_BLOCK(128, 1)
+  CBD_BLOCK(256, 1)
+  CBD_BLOCK(512, 1)
+  CBD_BLOCK(1024, 1)
+  CBD_BLOCK(1024, 2)
+  if constexpr (F == 2) {
+    CBD_BLOCK(1024, 4)
+  }
+#undef CBD_BLOCK
+  return nullptr;
+}
+
+template <bool BWD>
+int launch(const BlockArgs& a, BlockShape s, int dtype, int64_t grid, void* stream) {
+  const void* k = dtype == CBD_F32 ? pick<float, BWD>(s) : pick<uint16_t, BWD>(s);
+  void* args[] = {const_cast<BlockArgs*>(&a)};
+  return (int)hipLaunchKernel(k, dim3((unsigned)grid), dim3(s.lanes == 64 ? 256 : s.lanes), args, 0,
+                              (hipStream_t)stream);
+}
+
+}  // namespace
+
+int launch_block_forward(const BlockArgs& a, BlockShape s, int dtype, int64_t grid, void* stream) {
+  return launch<false>(a, s, dtype, grid, stream);
+}
+int launch_block_bwd(const BlockArgs& a, BlockShape s, int dtype, int64_t grid, void* stream) {
+  return launch<true>(a, s, dtype, grid, stream);
+}
+int launch_block_finish(const BlockFinish& a, void* stream) {
+  void* args[] = {const_cast<BlockFinish*>(&a)};
+  return (int)hipLaunchKernel((const void*)&block_finish_kernel, dim3((unsigned)((a.c + 63) / 64), 2), dim3(FINISH),
+                              args, 0, (hipStream_t)stream);
+}
+
+}  // namespace cbd

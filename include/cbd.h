@@ -492,6 +492,84 @@ cbd_status cbd_expert_gated_bwd(const cbd_expert_plan_t* plan, const void* dy, c
  * h); bwd: 0 or 1. */
 cbd_status cbd_expert_gated_info(const cbd_expert_plan_t* plan, int32_t bwd, cbd_expert_info_t* out);
 
+/* ---- the norms around a block, with its gate and residual ----
+ *
+ * Between two blocks of a network, for rows of C elements:
+ *
+ *   z = r + scale * gate * (w_post * norm(y))    the residual stream r, and y,
+ *   n = w_pre * norm(z)                          what the last block made of it
+ *   norm(v) = v / sqrt(mean(v^2) + eps)
+ *
+ * Parts may be left out: w_post NULL: y is not normed; gate NULL: no gate; y
+ * NULL (then w_post, gate and z are NULL too): z is r and is not written; w_pre
+ * NULL (then n is NULL): no n.  The gate is one vector for all rows or has a
+ * row for each.  stats receives 1 / sqrt(mean + eps) of y and of z, 1 where
+ * there is no norm.  Backward, from the gradients of z and n (NULL: zeros):
+ * dr, dy, dw_post, dgate and dw_pre, each NULL where it is not wanted.
+ *
+ * Everything is computed in f32 from the inputs, sums included (a row whose
+ * squares pass f32's range has norm(v) = 0), and each result is rounded once;
+ * n is made of the unrounded z.  A row's results do not depend on other rows.
+ * The vectors' gradients add up f32 sums of rows in a fixed order: the same
+ * inputs give the same bits.  No rows: they are 0.  z may be r itself, n y
+ * itself, dr dz itself and dy dn itself (the same address and row stride). */
+typedef enum { CBD_GATE_NONE = 0, CBD_GATE_CHANNEL = 1, CBD_GATE_ROW = 2 } cbd_gate_kind;
+
+typedef struct {
+  int64_t rows;     /* 0 .. 2^40 */
+  int64_t c;        /* 1 .. 16384 */
+  int32_t dtype;    /* cbd_dtype of the rows, w_post, gate, w_pre, dr, dy and a row gate's dgate */
+  int32_t dw_dtype; /* cbd_dtype of the vectors' gradients: CBD_F32, or CBD_BF16 with bf16 rows */
+  double eps;       /* finite, >= 0 */
+  double scale;     /* finite */
+} cbd_block_problem;
+
+typedef struct {
+  const void* w_post;
+  const void* gate;
+  const void* w_pre;
+  int32_t gate_kind; /* cbd_gate_kind of gate; CBD_GATE_NONE where it is NULL */
+  int32_t reserved;  /* must be zero */
+} cbd_block_params;
+
+/* Row strides in elements; 0 (or a NULL pointer): dense. */
+typedef struct {
+  int64_t r, y, gate, z, n;            /* gate: of a row gate */
+  int64_t dz, dn, dr, dy, dgate;
+} cbd_block_strides;
+
+typedef struct {
+  void* dr;
+  void* dy;
+  void* dw_post;
+  void* dgate;
+  void* dw_pre;
+} cbd_block_grads;
+
+typedef struct cbd_block_plan_s cbd_block_plan_t; /* opaque; immutable */
+
+/* Host-only.  INVALID_ARG: NULL, sizes, types, eps or scale out of the ranges
+ * above; UNSUPPORTED: rows or c above them. */
+cbd_status cbd_block_plan(const cbd_block_problem* problem, cbd_block_plan_t** out_plan);
+void cbd_block_plan_destroy(cbd_block_plan_t* plan); /* NULL is allowed */
+
+/* Device workspace of the backward call (256-byte aligned; no initialisation,
+ * nothing kept; one per stream in use). */
+cbd_status cbd_block_workspace_size(const cbd_block_plan_t* plan, uint64_t* bytes);
+
+/* stats: [rows][2] f32; NULL where they are not wanted (forward).  The backward
+ * call may go without a workspace (NULL) where no vector's gradient is wanted.
+ * Stream-ordered, nothing is allocated, calls can be captured.  Errors as for
+ * the expert calls, plus INVALID_ARG for parts that do not go together and a
+ * short workspace, and UNSUPPORTED for a workspace off its alignment. */
+cbd_status cbd_block_forward(const cbd_block_plan_t* plan, const void* r, const void* y,
+                             const cbd_block_params* params, void* z, void* n, float* stats,
+                             const cbd_block_strides* strides, void* stream);
+cbd_status cbd_block_bwd(const cbd_block_plan_t* plan, const void* dz, const void* dn, const void* r,
+                         const void* y, const float* stats, const cbd_block_params* params,
+                         const cbd_block_grads* grads, const cbd_block_strides* strides,
+                         void* workspace, uint64_t workspace_bytes, void* stream);
+
 /* ---- global gradient norm and clipping over a list of tensors ----
  *
  *   norm  = sqrt( sum over every element g of every tensor of g^2 )
