@@ -42,6 +42,8 @@ SOURCES = [
     "kern_gated_stream.hip",
     "block_api.cpp",
     "kern_block_norm.hip",
+    "ortho_api.cpp",
+    "kern_ortho.hip",
     "grad_api.cpp",
     "kern_grad_norm.hip",
 ]

@@ -1,0 +1,378 @@
+// kern_ortho.hip -- orthogonalised updates: Newton-Schulz steps
+//
+//   A = X X^T,  B = a I + b A + c A A,  X <- B X
+//
+// on matrices held as two halves a value (ortho_internal.h).  A product of two
+// such values is hi hi + hi lo + lo hi, three matrix instructions on halves with
+// f32 sums; lo lo is below 2^-22 of it.  A value keeps 22 bits: each step's
+// rounding is some 2^-24 of it, next to sums of f32 products, whose own are
+// larger; and halves go at 16 times the rate of the f32 instructions, so that
+// three of them are 5 times as fast.  One exponent a matrix, chosen by the plan
+// from the bounds of the singular values, keeps the largest value at 2^14 at
+// most and the smallest ones' lo out of the subnormals.
+//
+// A and B are symmetric: only tiles on and above the diagonal are computed, and
+// each is stored twice.
+//
+// A workgroup of 4 waves (2 x 2) computes a tile of 64 MB x 64 MB in runs of 32
+// k: 128 bytes of a row, hi and lo, go straight to one of two LDS stages
+// (buffer_load ... lds), in chunks of 16 bytes, chunk c of row r at c ^ (r / 2 %
+// 8), so that reads of 32 rows spread over the banks.
+#include <type_traits>
+
+#include "cbd_device.h"
+#include "ortho_internal.h"
+
+namespace cbd {
+namespace {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((__vector_size__(16 * sizeof(float))));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) char lds_char;
+#define INLINE __attribute__((always_inline))
+
+constexpr int THREADS = 256;
+
+__device__ inline uint16_t half_bits(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
+__device__ inline float half_value(uint32_t b) { return (float)__builtin_bit_cast(_Float16, (uint16_t)b); }
+// The two halves of a value: hi in bits 0-15, lo in bits 16-31.
+__device__ inline uint32_t split(float v) {
+  const uint16_t hi = half_bits(v);
+  return hi | (uint32_t)half_bits(v - half_value(hi)) << 16;
+}
+
+// s_waitcnt: every load and LDS access is done.
+__device__ inline void wait_all() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0 | (7 << 4));  // vmcnt 0, expcnt 7, lgkmcnt 0
+  asm volatile("" ::: "memory");
+}
+__device__ inline void barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <int MB, int STAGE>
+__global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void ortho_product_kernel(const OrthoArgs a) {
+  constexpr int T = 64 * MB;
+  constexpr int BYTES = T * 128;      // of an operand's stage
+  constexpr int N = BYTES / 4096;     // 1 KiB blocks of it that a wave fills
+  constexpr bool SYM = STAGE == ORTHO_SQUARE || STAGE == ORTHO_POLY;
+  __shared__ __attribute__((aligned(1024))) char smem[4 * BYTES];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave & 1, wn = wave >> 1;
+
+  // The matrix and the tile.
+  const int per = SYM ? a.tiles_m * (a.tiles_m + 1) / 2 : a.tiles_m * a.tiles_n;
+  const int t = dev::logical_tile((int)blockIdx.x, (int)gridDim.x, 1);
+  const int mat = __builtin_amdgcn_readfirstlane(t / per);
+  int local = __builtin_amdgcn_readfirstlane(t - mat * per), mt, nt;
+  if (SYM) {
+    for (nt = 0; local > nt; nt++) local -= nt + 1;  // column nt has nt + 1 tiles
+    mt = local;
+  } else {
+    // Groups of 8 rows of tiles by all columns.
+    const int g = local / (8 * a.tiles_n), in = local - g * 8 * a.tiles_n;
+    const int gm = a.tiles_m - 8 * g < 8 ? a.tiles_m - 8 * g : 8;
+    nt = in / gm;
+    mt = 8 * g + in - nt * gm;
+  }
+  mt = __builtin_amdgcn_readfirstlane(mt);
+  nt = __builtin_amdgcn_readfirstlane(nt);
+
+  // Loads: row lane / 8 of every 8, chunk lane % 8 in LDS.
+  uint64_t bp = (uint64_t)(a.p + mat * a.p_mat + (int64_t)mt * T * a.ldp);
+  uint64_t bq = (uint64_t)(a.q + mat * a.q_mat + (int64_t)nt * T * a.ldq);
+  uint32_t vp[N], vq[N];
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    const int row = 8 * (N * wave + i) + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
+    vp[i] = (uint32_t)row * (uint32_t)a.ldp * 2u + (uint32_t)c * 16u;
+    vq[i] = (uint32_t)row * (uint32_t)a.ldq * 2u + (uint32_t)c * 16u;
+  }
+  const uint32_t rec_p = (uint32_t)T * (uint32_t)a.ldp * 2u, rec_q = (uint32_t)T * (uint32_t)a.ldq * 2u;
+  const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_char*)smem + (uint32_t)(wave * N * 1024));
+  auto issue = [&](uint64_t b, uint32_t rec, uint32_t voff, uint32_t soff, uint32_t m0v) INLINE {
+    const i32x4 d = {(int)(uint32_t)b, (int)((uint32_t)(b >> 32) & 0xffffu), (int)rec, 0x00020000};
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds\n\ts_nop 0"
+                 ::"s"(m0v), "v"(voff), "s"(d), "s"(soff) : "memory", "m0");
+#pragma clang diagnostic pop
+  };
+  // Run k of an operand into stage s; past the last there is nothing to load
+  // (a record count of 0 gives zeros), but the count of loads stays.
+  auto load_p = [&](int k, int s, int i) INLINE {
+    issue(bp, k < a.runs ? rec_p : 0u, vp[i], (uint32_t)k * 128u, base + (uint32_t)(2 * s * BYTES + i * 1024));
+  };
+  auto load_q = [&](int k, int s, int i) INLINE {
+    issue(bq, k < a.runs ? rec_q : 0u, vq[i], (uint32_t)k * 128u, base + (uint32_t)((2 * s + 1) * BYTES + i * 1024));
+  };
+
+  // Fragments: 32 rows by 16 k; half h (0: hi, 1: lo) of k 16 ks ...
+  int at_p[4], at_q[4];
+  {
+    const int rp = 32 * MB * wm + (lane & 31), rq = 32 * MB * wn + (lane & 31);
+#pragma unroll
+    for (int c = 0; c < 4; c++) {
+      at_p[c] = rp * 128 + (((2 * c + (lane >> 5)) ^ ((rp >> 1) & 7)) << 4);
+      at_q[c] = rq * 128 + (((2 * c + (lane >> 5)) ^ ((rq >> 1) & 7)) << 4);
+    }
+  }
+  auto read_p = [&](int s, int ks, int h, int b) INLINE {
+    return *(const f16x8*)(smem + 2 * s * BYTES + at_p[2 * h + ks] + b * 4096);
+  };
+  auto read_q = [&](int s, int ks, int h, int b) INLINE {
+    return *(const f16x8*)(smem + (2 * s + 1) * BYTES + at_q[2 * h + ks] + b * 4096);
+  };
+
+  f32x16 acc[MB][MB];
+#pragma unroll
+  for (int i = 0; i < MB; i++)
+#pragma unroll
+    for (int j = 0; j < MB; j++) acc[i][j] = f32x16{};
+
+  // MFMAs on (x, y), with R reads and L loads spread between them.
+  auto part = [&](const f16x8 (&x)[MB], const f16x8 (&y)[MB], auto rc, auto&& rd, auto lc, auto&& ld) INLINE {
+    constexpr int Q = MB * MB, R = decltype(rc)::value, L = decltype(lc)::value;
+#pragma unroll
+    for (int i = 0; i < Q; i++) {
+      const int n = i / MB, m = (n & 1) ? MB - 1 - i % MB : i % MB;
+      acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[m], y[n], acc[m][n], 0, 0, 0);
+#pragma unroll
+      for (int r = i * R / Q; r < (i + 1) * R / Q; r++) rd(r);
+#pragma unroll
+      for (int r = i * L / Q; r < (i + 1) * L / Q; r++) ld(r);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  constexpr std::integral_constant<int, 0> none{};
+  constexpr std::integral_constant<int, MB> one{};
+  constexpr std::integral_constant<int, 2 * MB> two{};
+  constexpr std::integral_constant<int, N> all{};
+  auto nothing = [](int) {};
+
+  f16x8 ph0[MB], ph1[MB], pl[MB], qh0[MB], qh1[MB], ql[MB];
+  // Run 0 and the first operand's run 1.
+#pragma unroll
+  for (int i = 0; i < N; i++) load_p(0, 0, i);
+#pragma unroll
+  for (int i = 0; i < N; i++) load_q(0, 0, i);
+  wait_all();
+  barrier();
+#pragma unroll
+  for (int i = 0; i < N; i++) load_p(1, 1, i);
+#pragma unroll
+  for (int b = 0; b < MB; b++) {
+    ph0[b] = read_p(0, 0, 0, b);
+    qh0[b] = read_q(0, 0, 0, b);
+  }
+  // Run k in stage S, whose first hi fragments are in registers.  The other
+  // stage gets the second operand's run k + 1 here, and this one, once every
+  // wave has read it, the first operand's run k + 2.
+  auto run = [&](int k, auto sc) INLINE {
+    constexpr int S = decltype(sc)::value;
+    part(ph0, qh0, two,
+         [&](int r) { r < MB ? (void)(ql[r] = read_q(S, 0, 1, r)) : (void)(pl[r - MB] = read_p(S, 0, 1, r - MB)); }, all,
+         [&](int i) { load_q(k + 1, 1 - S, i); });
+    part(ph0, ql, one, [&](int r) { ph1[r] = read_p(S, 1, 0, r); }, none, nothing);
+    part(pl, qh0, one, [&](int r) { qh1[r] = read_q(S, 1, 0, r); }, none, nothing);
+    part(ph1, qh1, two,
+         [&](int r) { r < MB ? (void)(ql[r] = read_q(S, 1, 1, r)) : (void)(pl[r - MB] = read_p(S, 1, 1, r - MB)); }, none,
+         nothing);
+    wait_all();
+    barrier();
+    part(ph1, ql, one, [&](int r) { ph0[r] = read_p(1 - S, 0, 0, r); }, all, [&](int i) { load_p(k + 2, S, i); });
+    part(pl, qh1, one, [&](int r) { qh0[r] = read_q(1 - S, 0, 0, r); }, none, nothing);
+  };
+#pragma unroll 1
+  for (int k = 0; k < a.runs; k += 2) {
+    run(k, std::integral_constant<int, 0>());
+    if (k + 1 < a.runs) run(k + 1, std::integral_constant<int, 1>());
+  }
+  // The last loads (zeros) have landed, and everyone has read the stages.
+  wait_all();
+  barrier();
+
+  // A lane of block (m, n): C column lane % 32, rows 8 q + 4 (lane / 32) + 0..3.
+  char* const st = smem + wave * 4096;
+  const int r = lane & 31, hi = lane >> 5;
+  const int m0 = T * mt + 32 * MB * wm, n0 = T * nt + 32 * MB * wn;
+#pragma unroll
+  for (int n = 0; n < MB; n++)
+#pragma unroll
+    for (int m = 0; m < MB; m++) {
+      if constexpr (MB == 4) asm volatile("" : "+a"(acc[m][n]));
+      const int row0 = m0 + 32 * m, col = n0 + 32 * n + r;
+      float v[16];
+#pragma unroll
+      for (int j = 0; j < 16; j++) v[j] = acc[m][n][j] * a.mul;
+      if constexpr (STAGE == ORTHO_POLY) {
+        // A is symmetric: row `col` has the four neighbouring elements.
+        const uint16_t* d = a.p + mat * a.p_mat + (int64_t)col * a.ldp + (row0 >> 5) * 64 + 4 * hi;
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+          const u32x2 x = *(const u32x2*)(d + 8 * q), y = *(const u32x2*)(d + 8 * q + 32);
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            const float w = half_value(x[j >> 1] >> (16 * (j & 1))) + half_value(y[j >> 1] >> (16 * (j & 1)));
+            v[4 * q + j] = __builtin_fmaf(a.p_mul, w, v[4 * q + j]);
+            if (row0 + 8 * q + 4 * hi + j == col) v[4 * q + j] += a.diag;
+          }
+        }
+      }
+      if constexpr (STAGE == ORTHO_LAST) {
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            const int row = row0 + 8 * q + 4 * hi + j;
+            if (row < a.rows && col < a.cols) {
+              const int64_t o = mat * a.out_mat + (a.flip ? col * a.out_row + row : row * a.out_row + col);
+              if (a.out_dtype == CBD_F32)
+                ((float*)a.out)[o] = v[4 * q + j];
+              else
+                ((uint16_t*)a.out)[o] = (uint16_t)dev::bf16_rne(v[4 * q + j]);
+            }
+          }
+      } else {
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 16; j++) {
+          const int row = row0 + 8 * (j >> 2) + 4 * hi + (j & 3);
+          w[j] = row < a.rows && col < a.cols ? split(v[j]) : 0u;
+        }
+        // 128 bytes of a row at a time: 8 lanes.
+        auto leave = [&](uint16_t* o, int ld) INLINE {
+          asm volatile("" ::: "memory");  // a wave's LDS accesses run in order
+#pragma unroll
+          for (int it = 0; it < 4; it++) {
+            const int row = 8 * it + (lane >> 3), c = lane & 7;
+            *(u32x4*)(o + (int64_t)row * ld + 8 * c) = *(const u32x4*)(st + row * 128 + ((c ^ (row & 7)) << 4));
+          }
+          asm volatile("" ::: "memory");
+        };
+        // C^T: row `col`, four neighbouring elements of a lane.
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+          char* const s = st + r * 128 + (hi << 3);
+          *(u32x2*)(s + ((q ^ (r & 7)) << 4)) =
+              u32x2{(w[4 * q] & 0xffffu) | w[4 * q + 1] << 16, (w[4 * q + 2] & 0xffffu) | w[4 * q + 3] << 16};
+          *(u32x2*)(s + (((4 + q) ^ (r & 7)) << 4)) =
+              u32x2{w[4 * q] >> 16 | (w[4 * q + 1] & 0xffff0000u), w[4 * q + 2] >> 16 | (w[4 * q + 3] & 0xffff0000u)};
+        }
+        leave(a.ct + mat * a.ct_mat + (int64_t)(n0 + 32 * n) * a.ldct + (row0 >> 5) * 64, a.ldct);
+        // C: by elements.  A diagonal tile of a symmetric matrix has both already.
+        if (!SYM || mt != nt) {
+#pragma unroll
+          for (int j = 0; j < 16; j++) {
+            const int row = 8 * (j >> 2) + 4 * hi + (j & 3);
+            char* const s = st + row * 128 + 2 * (r & 7);
+            *(uint16_t*)(s + (((r >> 3) ^ (row & 7)) << 4)) = (uint16_t)w[j];
+            *(uint16_t*)(s + (((4 + (r >> 3)) ^ (row & 7)) << 4)) = (uint16_t)(w[j] >> 16);
+          }
+          leave(a.c + mat * a.c_mat + (int64_t)row0 * a.ldc + ((n0 + 32 * n) >> 5) * 64, a.ldc);
+        }
+      }
+    }
+}
+
+// ---- the input: norm, then both directions as two halves a value
+
+template <typename T>
+__device__ inline float value(const void* p, int64_t i) {
+  if constexpr (sizeof(T) == 4)
+    return ((const float*)p)[i];
+  else
+    return dev::bf16_to_f32(((const uint16_t*)p)[i]);
+}
+
+// Sums of squares in 64 bits: workgroup i of a matrix takes rows i, i + 64, ...
+template <typename T>
+__global__ __launch_bounds__(THREADS) void ortho_norm_kernel(const OrthoSplit a) {
+  __shared__ double part[THREADS / 64];
+  const int64_t mat = blockIdx.y;
+  double s = 0.0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += kOrthoParts)
+    for (int col = threadIdx.x; col < a.cols; col += THREADS) {
+      const double v = value<T>(a.in, mat * a.in_mat + row * a.in_row + col);
+      s = __builtin_fma(v, v, s);
+    }
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) s += __shfl_xor(s, m, 64);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) a.partial[mat * kOrthoParts + blockIdx.x] = (part[0] + part[1]) + (part[2] + part[3]);
+}
+
+// 64 x 64 elements of a matrix.
+template <typename T>
+__global__ __launch_bounds__(THREADS) void ortho_split_kernel(const OrthoSplit a) {
+  __shared__ uint32_t tile[64][65];
+  const int64_t mat = blockIdx.z;
+  const int row0 = blockIdx.y * 64, col0 = blockIdx.x * 64, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  // Every wave adds the parts in the same order.
+  double s = a.partial[mat * kOrthoParts + lane];
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) s += __shfl_xor(s, m, 64);
+  const double f = a.up / (__builtin_sqrt(s) + a.eps);
+#pragma unroll 4
+  for (int i = 0; i < 16; i++) {
+    const int row = 4 * i + wave;
+    float v = 0.f;
+    if (row0 + row < a.rows && col0 + lane < a.cols)
+      v = (float)((double)value<T>(a.in, mat * a.in_mat + (int64_t)(row0 + row) * a.in_row + col0 + lane) * f);
+    tile[row][lane] = split(v);
+  }
+  __syncthreads();
+  // Rows of two runs: lane j takes halves 2 j and 2 j + 1 of a row's 128.
+  const int run = lane >> 5, e = 2 * (lane & 15), lo = (lane >> 4) & 1;
+#pragma unroll 4
+  for (int i = 0; i < 16; i++) {
+    const int row = 4 * i + wave;
+    const uint32_t x = tile[row][32 * run + e], y = tile[row][32 * run + e + 1];
+    const uint32_t u = tile[32 * run + e][row], v = tile[32 * run + e + 1][row];
+    uint16_t* const o = a.x + mat * a.x_mat + (int64_t)(row0 + row) * a.ldx + col0 * 2;
+    uint16_t* const p = a.xt + mat * a.xt_mat + (int64_t)(col0 + row) * a.ldxt + row0 * 2;
+    ((uint32_t*)o)[lane] = lo ? x >> 16 | (y & 0xffff0000u) : (x & 0xffffu) | y << 16;
+    ((uint32_t*)p)[lane] = lo ? u >> 16 | (v & 0xffff0000u) : (u & 0xffffu) | v << 16;
+  }
+}
+
+template <int STAGE>
+const void* pick(int tile) {
+  return tile == 256   ? (const void*)&ortho_product_kernel<4, STAGE>
+         : tile == 128 ? (const void*)&ortho_product_kernel<2, STAGE>
+                       : (const void*)&ortho_product_kernel<1, STAGE>;
+}
+
+}  // namespace
+
+int launch_ortho_norm(const OrthoSplit& a, int64_t matrices, void* stream) {
+  void* args[] = {const_cast<OrthoSplit*>(&a)};
+  const void* k = a.dtype == CBD_F32 ? (const void*)&ortho_norm_kernel<float> : (const void*)&ortho_norm_kernel<uint16_t>;
+  return (int)hipLaunchKernel(k, dim3(kOrthoParts, (unsigned)matrices), dim3(THREADS), args, 0, (hipStream_t)stream);
+}
+int launch_ortho_split(const OrthoSplit& a, int64_t matrices, void* stream) {
+  void* args[] = {const_cast<OrthoSplit*>(&a)};
+  const void* k =
+      a.dtype == CBD_F32 ? (const void*)&ortho_split_kernel<float> : (const void*)&ortho_split_kernel<uint16_t>;
+  return (int)hipLaunchKernel(k, dim3((unsigned)((a.cols + 63) / 64), (unsigned)((a.rows + 63) / 64), (unsigned)matrices),
+                              dim3(THREADS), args, 0, (hipStream_t)stream);
+}
+int launch_ortho_product(const OrthoArgs& a, int stage, int tile, int64_t matrices, void* stream) {
+  void* args[] = {const_cast<OrthoArgs*>(&a)};
+  const bool sym = stage == ORTHO_SQUARE || stage == ORTHO_POLY;
+  const int64_t per = sym ? (int64_t)a.tiles_m * (a.tiles_m + 1) / 2 : (int64_t)a.tiles_m * a.tiles_n;
+  const void* k = stage == ORTHO_SQUARE ? pick<ORTHO_SQUARE>(tile)
+                  : stage == ORTHO_POLY ? pick<ORTHO_POLY>(tile)
+                  : stage == ORTHO_STEP ? pick<ORTHO_STEP>(tile)
+                                        : pick<ORTHO_LAST>(tile);
+  return (int)hipLaunchKernel(k, dim3((unsigned)(per * matrices)), dim3(THREADS), args, 0, (hipStream_t)stream);
+}
+
+}  // namespace cbd

@@ -1,0 +1,274 @@
+// ortho_api.cpp -- plans, argument checks and launches of the orthogonalised updates.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <memory>
+#include <string>
+
+#include "cbd_internal.h"
+#include "expert_common.h"
+#include "ortho_internal.h"
+
+namespace {
+
+using cbd::host::Block;
+using cbd::host::esize;
+using cbd::host::fail;
+using cbd::host::guarded;
+using cbd::host::share;
+
+constexpr int kTop = 14;  // stored values stay below 2^14 times what rounding adds (halves end at 2^16)
+
+int64_t up_to(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+
+// The exponent that brings a bound to at most 2^kTop; false if there is none.
+bool exponent(double bound, int& e) {
+  if (!(bound >= std::ldexp(1.0, -20) && bound <= std::ldexp(1.0, 20))) return false;
+  e = kTop - (int)std::ceil(std::log2(bound));
+  return true;
+}
+
+// Tile of a product with `count(t)` tiles of t x t: the one whose rounds over
+// the card take the least matrix time.
+template <typename F>
+int pick_tile(F&& count) {
+  struct {
+    int t, at_once;
+    double slower;
+  } const all[] = {{256, 256, 1.0}, {128, 512, 1.2}, {64, 1024, 1.6}};
+  int best = 256;
+  double least = 0.0;
+  for (const auto& c : all) {
+    const double rounds = std::ceil((double)count(c.t) / c.at_once);
+    const double time = rounds * (c.at_once / 256) * c.t * c.t * c.slower;
+    if (c.t == 256 || time < least) {
+      best = c.t;
+      least = time;
+    }
+  }
+  return best;
+}
+
+cbd_status make_plan(const cbd_ortho_problem* q, cbd_ortho_plan_t** out) {
+  if (!q || !out) return fail(CBD_ERR_INVALID_ARG, "NULL problem or output");
+  *out = nullptr;
+  if (q->matrices < 0 || q->rows < 1 || q->cols < 1)
+    return fail(CBD_ERR_INVALID_ARG, "matrices must be >= 0, rows and cols >= 1");
+  if (q->dtype != CBD_F32 && q->dtype != CBD_BF16) return fail(CBD_ERR_INVALID_ARG, "unknown dtype");
+  if (q->steps < 1 || q->steps > 64) return fail(CBD_ERR_INVALID_ARG, "steps must be 1 to 64");
+  if (!(q->eps > 0.0) || !std::isfinite(q->eps) || !std::isfinite((float)q->scale))
+    return fail(CBD_ERR_INVALID_ARG, "eps must be finite and > 0, scale finite");
+  if (q->matrices > 65535 || q->rows > 65536 || q->cols > 65536)
+    return fail(CBD_ERR_UNSUPPORTED, "more than 65535 matrices, or sides above 65536");
+  std::unique_ptr<cbd_ortho_plan_s> p(new cbd_ortho_plan_s);
+  p->prob = *q;
+  p->prob.coefficients = nullptr;
+  // Bounds of the singular values, of A and of B in each step.
+  double top = 1.0;
+  for (int k = 0; k <= q->steps; k++) {
+    int e = 0;
+    if (!exponent(top, e)) return fail(CBD_ERR_UNSUPPORTED, "the steps let singular values grow or shrink too far");
+    p->ex.push_back(e);
+    if (k == q->steps) break;
+    const double usual[3] = {3.4445, -4.7750, 2.0315};
+    const double* c = q->coefficients ? q->coefficients + 3 * k : usual;
+    for (int i = 0; i < 3; i++) {
+      if (!std::isfinite(c[i])) return fail(CBD_ERR_INVALID_ARG, "a coefficient is not finite");
+      p->coefficients.push_back(c[i]);
+    }
+    double most_b = 0.0, most_x = 0.0;
+    for (int i = 0; i <= 4096; i++) {
+      const double x = top * i / 4096, b = std::fabs(c[0] + x * x * (c[1] + x * x * c[2]));
+      most_b = std::max(most_b, b);
+      most_x = std::max(most_x, b * x);
+    }
+    int ea = 0, eb = 0;
+    if (!exponent(top * top, ea) || !exponent(most_b, eb))
+      return fail(CBD_ERR_UNSUPPORTED, "the steps let singular values grow or shrink too far");
+    p->ea.push_back(ea);
+    p->eb.push_back(eb);
+    top = most_x;
+  }
+  p->s = std::min(q->rows, q->cols);
+  p->l = std::max(q->rows, q->cols);
+  const int64_t n = std::max<int64_t>(q->matrices, 1);
+  p->tile_sym = pick_tile([&](int64_t t) {
+    const int64_t m = (p->s + t - 1) / t;
+    return n * m * (m + 1) / 2;
+  });
+  p->tile_step = pick_tile([&](int64_t t) { return n * ((p->s + t - 1) / t) * ((p->l + t - 1) / t); });
+  const int64_t pad = std::max(p->tile_sym, p->tile_step);
+  p->sp = up_to(p->s, pad);
+  p->lp = up_to(p->l, pad);
+  *out = p.release();
+  cbd::set_error("");
+  return CBD_OK;
+}
+
+// Halves of a matrix in each of the workspace's arrays, and the whole.
+struct Layout {
+  int64_t x, a;               // halves of X (either direction) and of A or B
+  uint64_t parts, bytes;
+  explicit Layout(const cbd_ortho_plan_s& p) {
+    const uint64_t n = (uint64_t)p.prob.matrices;
+    x = 2 * p.sp * p.lp;
+    a = 2 * p.sp * p.sp;
+    parts = (n * cbd::kOrthoParts * sizeof(double) + 255) / 256 * 256;
+    bytes = parts + n * 2 * (3 * (uint64_t)x + 2 * (uint64_t)a) + 256;
+  }
+};
+
+cbd_status run(const cbd_ortho_plan_t* plan, const void* in, void* out, const cbd_ortho_strides* st, void* ws,
+               uint64_t ws_bytes, void* stream) {
+  if (!plan) return fail(CBD_ERR_INVALID_ARG, "NULL plan");
+  const cbd_ortho_problem& q = plan->prob;
+  if (!q.matrices) {
+    cbd::set_error("");
+    return CBD_OK;
+  }
+  if (!in || !out || !ws) return fail(CBD_ERR_INVALID_ARG, "NULL tensor or workspace");
+  cbd_ortho_strides s = {0, 0, 0, 0};
+  if (st) s = *st;
+  if (!s.in_row) s.in_row = q.cols;
+  if (!s.out_row) s.out_row = q.cols;
+  if (s.in_row < q.cols || s.out_row < q.cols) return fail(CBD_ERR_INVALID_ARG, "a row stride is smaller than the row");
+  if (s.in_row > (int64_t(1) << 31) || s.out_row > (int64_t(1) << 31))
+    return fail(CBD_ERR_UNSUPPORTED, "a stride is too large");
+  const int64_t in_span = (q.rows - 1) * s.in_row + q.cols, out_span = (q.rows - 1) * s.out_row + q.cols;
+  if (!s.in_matrix) s.in_matrix = in_span;
+  if (!s.out_matrix) s.out_matrix = out_span;
+  if (s.in_matrix < in_span || s.out_matrix < out_span)
+    return fail(CBD_ERR_INVALID_ARG, "a matrix stride is smaller than the matrix");
+  if (s.in_matrix > (int64_t(1) << 40) || s.out_matrix > (int64_t(1) << 40))
+    return fail(CBD_ERR_UNSUPPORTED, "a stride is too large");
+  const Layout lay(*plan);
+  if (ws_bytes < lay.bytes) return fail(CBD_ERR_INVALID_ARG, "workspace smaller than cbd_ortho_workspace_size");
+  if ((uintptr_t)ws & 255u) return fail(CBD_ERR_UNSUPPORTED, "workspace must be 256-byte aligned");
+  const int es = esize(q.dtype);
+  if (((uintptr_t)in | (uintptr_t)out) & (uintptr_t)(es - 1))
+    return fail(CBD_ERR_UNSUPPORTED, "a pointer is not aligned to its element size");
+  const Block bi = {in, q.rows, q.cols, s.in_row, q.matrices, s.in_matrix, es};
+  const Block bo = {out, q.rows, q.cols, s.out_row, q.matrices, s.out_matrix, es};
+  const Block bw = {ws, 1, (int64_t)lay.bytes, (int64_t)lay.bytes, 1, 0, 1};
+  const bool itself = in == out && s.in_row == s.out_row && s.in_matrix == s.out_matrix;
+  if ((!itself && share(bi, bo)) || share(bi, bw) || share(bo, bw))
+    return fail(CBD_ERR_INVALID_ARG, "the output or the workspace overlaps another tensor");
+
+  const bool tall = q.rows > q.cols;
+  const int64_t n = q.matrices;
+  double* const partial = (double*)ws;
+  uint16_t* const x = (uint16_t*)((char*)ws + lay.parts);  // rows: the smaller side
+  uint16_t* xt = x + n * lay.x;                            // rows: the larger one
+  uint16_t* xt_next = xt + n * lay.x;
+  uint16_t* const sq = xt_next + n * lay.x;                // A
+  uint16_t* const poly = sq + n * lay.a;                   // B
+  const int32_t ldx = (int32_t)(2 * plan->lp), ldxt = (int32_t)(2 * plan->sp);
+
+  cbd::OrthoSplit f = {};
+  f.in = in;
+  f.in_row = s.in_row;
+  f.in_mat = s.in_matrix;
+  f.rows = (int32_t)q.rows;
+  f.cols = (int32_t)q.cols;
+  f.dtype = q.dtype;
+  f.partial = partial;
+  f.eps = q.eps;
+  f.up = std::ldexp(1.0, plan->ex[0]);
+  f.x = tall ? xt : x;
+  f.ldx = tall ? ldxt : ldx;
+  f.xt = tall ? x : xt;
+  f.ldxt = tall ? ldx : ldxt;
+  f.x_mat = f.xt_mat = lay.x;
+  int err = cbd::launch_ortho_norm(f, n, stream);
+  if (!err) err = cbd::launch_ortho_split(f, n, stream);
+
+  auto tiles = [](int64_t v, int t) { return (int32_t)((v + t - 1) / t); };
+  for (int k = 0; k < q.steps && !err; k++) {
+    const double* c = &plan->coefficients[3 * k];
+    const int ex = plan->ex[k], ea = plan->ea[k], eb = plan->eb[k];
+    cbd::OrthoArgs a = {};
+    a.p = a.q = x;
+    a.p_mat = a.q_mat = lay.x;
+    a.ldp = a.ldq = ldx;
+    a.runs = tiles(plan->l, 32);
+    a.tiles_m = a.tiles_n = tiles(plan->s, plan->tile_sym);
+    a.rows = a.cols = (int32_t)plan->s;
+    a.c = a.ct = sq;
+    a.c_mat = a.ct_mat = lay.a;
+    a.ldc = a.ldct = ldxt;
+    a.mul = (float)std::ldexp(1.0, ea - 2 * ex);
+    err = cbd::launch_ortho_product(a, cbd::ORTHO_SQUARE, plan->tile_sym, n, stream);
+    if (err) break;
+
+    a.p = a.q = sq;
+    a.p_mat = a.q_mat = lay.a;
+    a.ldp = a.ldq = ldxt;
+    a.runs = tiles(plan->s, 32);
+    a.c = a.ct = poly;
+    a.mul = (float)std::ldexp(c[2], eb - 2 * ea);
+    a.p_mul = (float)std::ldexp(c[1], eb - ea);
+    a.diag = (float)std::ldexp(c[0], eb);
+    err = cbd::launch_ortho_product(a, cbd::ORTHO_POLY, plan->tile_sym, n, stream);
+    if (err) break;
+
+    const bool last = k == q.steps - 1;
+    a = {};
+    a.p = poly;
+    a.p_mat = lay.a;
+    a.ldp = ldxt;
+    a.q = xt;
+    a.q_mat = lay.x;
+    a.ldq = ldxt;
+    a.runs = tiles(plan->s, 32);
+    a.tiles_m = tiles(plan->s, plan->tile_step);
+    a.tiles_n = tiles(plan->l, plan->tile_step);
+    a.rows = (int32_t)plan->s;
+    a.cols = (int32_t)plan->l;
+    if (last) {
+      a.mul = (float)(std::ldexp(1.0, -eb - ex) * q.scale);
+      a.out = out;
+      a.out_row = s.out_row;
+      a.out_mat = s.out_matrix;
+      a.out_dtype = q.dtype;
+      a.flip = tall;
+    } else {
+      a.mul = (float)std::ldexp(1.0, plan->ex[k + 1] - eb - ex);
+      a.c = x;
+      a.c_mat = lay.x;
+      a.ldc = ldx;
+      a.ct = xt_next;
+      a.ct_mat = lay.x;
+      a.ldct = ldxt;
+    }
+    err = cbd::launch_ortho_product(a, last ? cbd::ORTHO_LAST : cbd::ORTHO_STEP, plan->tile_step, n, stream);
+    std::swap(xt, xt_next);
+  }
+  if (err) {
+    cbd::set_error(std::string("orthogonalising kernel launch failed: ") + cbd::hip_error_name(err));
+    return CBD_ERR_HIP;
+  }
+  cbd::set_error("");
+  return CBD_OK;
+}
+
+}  // namespace
+
+extern "C" cbd_status cbd_ortho_plan(const cbd_ortho_problem* problem, cbd_ortho_plan_t** out_plan) {
+  return guarded([&] { return make_plan(problem, out_plan); });
+}
+
+extern "C" void cbd_ortho_plan_destroy(cbd_ortho_plan_t* plan) { delete plan; }
+
+extern "C" cbd_status cbd_ortho_workspace_size(const cbd_ortho_plan_t* plan, uint64_t* bytes) {
+  return guarded([&]() -> cbd_status {
+    if (!plan || !bytes) return fail(CBD_ERR_INVALID_ARG, "NULL plan or output");
+    *bytes = Layout(*plan).bytes;
+    return CBD_OK;
+  });
+}
+
+extern "C" cbd_status cbd_orthogonalize(const cbd_ortho_plan_t* plan, const void* in, void* out,
+                                        const cbd_ortho_strides* strides, void* workspace, uint64_t workspace_bytes,
+                                        void* stream) {
+  return guarded([&] { return run(plan, in, out, strides, workspace, workspace_bytes, stream); });
+}

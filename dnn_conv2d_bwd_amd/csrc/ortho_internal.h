@@ -1,0 +1,70 @@
+// ortho_internal.h -- plan, kernel arguments and launchers of the orthogonalised updates.
+#pragma once
+#include <stdint.h>
+
+#include <vector>
+
+#include "../../include/cbd.h"
+
+namespace cbd {
+
+// Split matrices: a value v is held as two halves, hi = half(v 2^e) and lo =
+// half(v 2^e - hi), with one exponent e for the matrix.  Rows are runs of 64
+// halves: hi of 32 neighbouring elements, then their lo.
+//
+// X is the matrix with its smaller side as rows (S of them, L columns); it is
+// kept in both directions, since each product contracts along rows of both its
+// operands.
+
+// What a product C = P Q^T is for.
+enum OrthoStage {
+  ORTHO_SQUARE = 0,  // A = X X^T
+  ORTHO_POLY = 1,    // B = a I + b A + c A A
+  ORTHO_STEP = 2,    // X = B X, in both directions
+  ORTHO_LAST = 3     // the same, to the output
+};
+
+struct OrthoArgs {
+  const uint16_t *p, *q;     // operands: rows of ldp / ldq halves
+  int64_t p_mat, q_mat;      // halves between matrices
+  int32_t ldp, ldq;
+  int32_t runs;              // of 32 elements along the contracted side
+  int32_t tiles_m, tiles_n;  // (symmetric: n >= m of them)
+  int32_t rows, cols;        // of C; past them zeros are stored
+  uint16_t *c, *ct;          // C and C^T (symmetric: the same matrix)
+  int64_t c_mat, ct_mat;
+  int32_t ldc, ldct;
+  float mul;                 // C is the products' sum times this
+  float p_mul, diag;         // ORTHO_POLY: and P times p_mul, and diag on the diagonal
+  void* out;                 // ORTHO_LAST
+  int64_t out_row, out_mat;
+  int32_t out_dtype, flip;   // flip: the output is C^T
+};
+
+struct OrthoSplit {
+  const void* in;
+  int64_t in_row, in_mat;
+  int32_t rows, cols, dtype;
+  double* partial;           // [matrices][kOrthoParts] sums of squares
+  double eps, up;            // up = 2^e
+  uint16_t *x, *xt;          // rows x cols in the input's direction, and the other
+  int64_t x_mat, xt_mat;
+  int32_t ldx, ldxt;
+};
+
+constexpr int kOrthoParts = 64;
+
+int launch_ortho_norm(const OrthoSplit& a, int64_t matrices, void* stream);
+int launch_ortho_split(const OrthoSplit& a, int64_t matrices, void* stream);
+int launch_ortho_product(const OrthoArgs& a, int stage, int tile, int64_t matrices, void* stream);
+
+}  // namespace cbd
+
+struct cbd_ortho_plan_s {
+  cbd_ortho_problem prob;
+  std::vector<double> coefficients;   // steps x 3
+  int64_t s, l, sp, lp;               // sides, and their padded lengths
+  int tile_sym, tile_step;
+  // Exponents of X before each step, of A and of B.
+  std::vector<int> ex, ea, eb;
+};

@@ -607,6 +607,55 @@ cbd_status cbd_grad_clip(const cbd_grad_plan_t* plan, const void* const* grads, 
                          double max_norm, float* norm, void* workspace, uint64_t workspace_bytes,
                          void* stream);
 
+/* ---- orthogonalised updates: Newton-Schulz steps on a stack of matrices ----
+ *
+ *   X = M / (|M| + eps)                       |M|: the Frobenius norm
+ *   A = X X^T,  X <- a X + (b A + c A A) X    `steps` times
+ *   out = scale * X
+ *
+ * for each of the `matrices` M (rows x cols) by itself; with more rows than
+ * columns the same polynomial is taken from the other side (A = X^T X).  The
+ * norm is in 64 bits; products are of values of 22 bits with f32 sums, and the
+ * result is rounded once to its type.  A zero matrix gives zeros; a NaN or
+ * infinity anywhere in a matrix gives NaN in all of it.  The same inputs give
+ * the same bits. */
+typedef struct {
+  int64_t matrices;           /* 0 .. 65535 */
+  int64_t rows, cols;         /* 1 .. 65536 each */
+  int32_t dtype;              /* cbd_dtype of M and out */
+  int32_t steps;              /* 1 .. 64 */
+  double eps;                 /* finite, > 0 */
+  double scale;               /* finite */
+  const double* coefficients; /* steps times (a, b, c), read by cbd_ortho_plan only;
+                                 NULL: 3.4445, -4.7750, 2.0315 in every step */
+} cbd_ortho_problem;
+
+/* In elements; 0 (or a NULL pointer): dense. */
+typedef struct {
+  int64_t in_row, in_matrix;
+  int64_t out_row, out_matrix;
+} cbd_ortho_strides;
+
+typedef struct cbd_ortho_plan_s cbd_ortho_plan_t; /* opaque; immutable */
+
+/* Host-only.  INVALID_ARG: NULL, sizes, types, steps, eps or scale out of the
+ * ranges above, coefficients that are not finite; UNSUPPORTED: matrices, rows or
+ * cols above them, and coefficients whose steps let singular values of [0, 1]
+ * grow past 2^20 or shrink below 2^-20. */
+cbd_status cbd_ortho_plan(const cbd_ortho_problem* problem, cbd_ortho_plan_t** out_plan);
+void cbd_ortho_plan_destroy(cbd_ortho_plan_t* plan); /* NULL is allowed */
+
+/* Device workspace (256-byte aligned; no initialisation, nothing kept; one per
+ * stream in use). */
+cbd_status cbd_ortho_workspace_size(const cbd_ortho_plan_t* plan, uint64_t* bytes);
+
+/* out may be in itself (the same address and strides).  Stream-ordered, nothing
+ * is allocated, calls can be captured.  Errors as for the expert calls, plus
+ * INVALID_ARG for a short workspace. */
+cbd_status cbd_orthogonalize(const cbd_ortho_plan_t* plan, const void* in, void* out,
+                             const cbd_ortho_strides* strides, void* workspace,
+                             uint64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,287 @@
+"""Orthogonalised updates against their definition in 64 bits, and their
+refusals.
+
+Bounds.  The kernel's values have 22 bits where f32 has 24, its products are
+summed in f32: each of its roundings is at most 4 times one of the f32 form of
+the same formula.  How far roundings are amplified depends on the matrix, and is
+measured on it: the f32 form, computed on the CPU, is off by some error from 64
+bits, and the kernel may be off by 4 times that, and by 2^-22 of the result for
+its last product; in the largest element by 4 times the f32 form's and 2^-20 of
+the result's largest (a largest error of fewer roundings is less even).
+Results add half a step (bf16 2^-8, f32 2^-24)."""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import pytest
+import torch
+
+import dnn_conv2d_bwd_amd as cbd
+
+TORCH = {"bf16": torch.bfloat16, "f32": torch.float32}
+USUAL = (3.4445, -4.7750, 2.0315)
+
+
+def define(m, steps=5, coefficients=None, eps=1e-7, scale=1.0, dtype=torch.float64):
+    norm = m.double().square().sum((1, 2), keepdim=True).sqrt() + eps
+    x = (m.double() / norm).to(dtype)
+    flip = m.shape[1] > m.shape[2]
+    x = x.transpose(1, 2) if flip else x
+    for k in range(steps):
+        a, b, c = USUAL if coefficients is None else coefficients[k]
+        q = x @ x.transpose(1, 2)
+        x = a * x + (b * q + c * (q @ q)) @ x
+    return (scale * x).transpose(1, 2) if flip else scale * x
+
+
+def draw(n, rows, cols, dtype="f32", seed=0, rank=None, scale=1e-3):
+    gen = torch.Generator().manual_seed(4000 + seed)
+    m = torch.randn(n, rows, cols, generator=gen)
+    if rank:
+        m = 0.3 * m + torch.randn(n, rows, rank, generator=gen) @ torch.randn(n, rank, cols, generator=gen) / rank ** 0.5
+    return (scale * m).to(TORCH[dtype])
+
+
+def near(got, m, dtype, name="", **kw):
+    want, plain = define(m, **kw), define(m, dtype=torch.float32, **kw).double()
+    got, half = got.double().cpu(), torch.finfo(TORCH[dtype]).eps / 2
+    for i in range(m.shape[0]):
+        w, err, err32 = want[i], (got[i] - want[i]).abs(), (plain[i] - want[i]).abs()
+        ok = 4 * err32.norm() + (2.0 ** -22 + half) * w.norm()
+        assert err.norm() <= ok, f"{name} matrix {i}: {float(err.norm() / w.norm())} off, {float(ok / w.norm())} allowed"
+        top = w.abs().max()
+        assert (err <= 4 * err32.max() + 2.0 ** -20 * top + half * w.abs()).all(), f"{name} matrix {i}: an element is off"
+
+
+class Stack:
+    """Matrices in a buffer with `gap` extra elements a row, `space` more rows
+    between matrices and `off` elements before, NaN in all of them."""
+
+    def __init__(self, m, gap=0, space=0, off=0):
+        self.shape = n, r, c = m.shape
+        pitch, mat = c + gap, (r + space) * (c + gap)
+        self.buf = torch.full((off + n * mat + 64,), float("nan"), dtype=m.dtype, device="cuda")
+        self.t = self.buf[off:off + n * mat].view(n, r + space, pitch)[:, :r, :c]
+        self.t.copy_(m)
+
+    def take(self):
+        res = self.t.clone()
+        self.t.fill_(float("nan"))
+        assert bool(torch.isnan(self.buf).all()), "a store outside the output"
+        return res
+
+
+def call(m, gap=0, space=0, off=0, stream=None, **kw):
+    p = cbd.ortho_plan(*m.shape, dtype="f32" if m.dtype == torch.float32 else "bf16", **kw)
+    a, o = Stack(m, gap, space, off), Stack(torch.full(m.shape, float("nan"), dtype=m.dtype), gap, space, off)
+    ws = torch.full((p.workspace_size() + 256,), 0xff, dtype=torch.uint8, device="cuda")  # NaN, and a guard
+    if stream is not None:
+        stream.wait_stream(torch.cuda.current_stream())
+    assert cbd.orthogonalize(p, a.t, o.t, ws[:p.workspace_size()], stream=stream) is o.t
+    torch.cuda.synchronize()
+    assert bool((ws[p.workspace_size():] == 0xff).all())
+    return o.take()
+
+
+# One element; vectors; sides around the runs of 32 and the tiles of 64 and 128; tall, wide, square; many.
+SIZES = [(1, 1, 1), (3, 1, 40), (2, 40, 1), (5, 16, 16), (2, 31, 33), (3, 64, 64), (2, 65, 200), (2, 200, 65), (1, 128, 129),
+         (70, 17, 24), (2, 96, 515), (1, 515, 389), (1, 300, 1030)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("size", SIZES, ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_against_definition(dtype, size):
+    print("[ortho]", dtype, size, flush=True)
+    m = draw(*size, dtype=dtype, seed=sum(size))
+    near(call(m), m, dtype, str(size))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("size", [(9, 512, 768), (12, 700, 520), (30, 256, 256), (2, 1100, 2300), (300, 64, 96)], ids=str)
+def test_every_tile(size):
+    """Enough tiles that the larger ones are chosen, with edges inside them."""
+    print("[ortho] tiles", size, flush=True)
+    m = draw(*size, seed=size[1], rank=max(1, size[1] // 8))
+    got = call(m)
+    some = [0, size[0] // 2, size[0] - 1]
+    near(got[some], m[some], "f32", str(size))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gap,space,off", [(8, 0, 0), (1, 0, 1), (0, 3, 0), (5, 2, 3)])
+def test_strides_and_alignment(gap, space, off):
+    for dtype in ("bf16", "f32"):
+        for size in ((3, 40, 72), (2, 101, 67)):
+            m = draw(*size, dtype=dtype)
+            got = call(m, gap, space, off)
+            near(got, m, dtype)
+            assert torch.equal(got, call(m))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("steps,coefficients", [
+    (1, None), (3, None), (8, None), (2, [(1.5, -0.5, 0.0)]), (7, [(1.875, -1.25, 0.375)]),
+    (3, [(8.2872, -23.5959, 17.3004), (4.1071, -2.9478, 0.5448), (3.9487, -2.9089, 0.5518)])])
+def test_steps_and_coefficients(steps, coefficients):
+    m = draw(2, 90, 140, rank=12)
+    co = None if coefficients is None else coefficients * (steps if len(coefficients) == 1 else 1)
+    near(call(m, steps=steps, coefficients=coefficients), m, "f32", steps=steps, coefficients=co)
+
+
+@pytest.mark.gpu
+def test_scale_and_eps():
+    m = draw(2, 50, 70)
+    near(call(m, scale=-0.2), m, "f32", scale=-0.2)
+    near(call(m, eps=0.5), m, "f32", eps=0.5)
+    for by in (1e-30, 1e-4, 1e30):  # the norm's squares are in 64 bits
+        near(call(m * by, eps=1e-38), m * by, "f32", eps=1e-38)
+
+
+@pytest.mark.gpu
+def test_known_results():
+    """Matrices whose singular values are all alike come out as multiples of
+    themselves: signed permutations, and a Hadamard matrix."""
+    n = 64
+    h = torch.ones(1, 1)
+    while h.shape[0] < n:
+        h = torch.cat([torch.cat([h, h], 1), torch.cat([h, -h], 1)])
+    perm = torch.eye(n)[torch.randperm(n, generator=torch.Generator().manual_seed(1))]
+    m = torch.stack([h, 3.0 * perm, -0.01 * perm])
+    x = 1.0 / (1.0 + 1e-7 / m.double().square().sum((1, 2)).sqrt()) / math.sqrt(n)
+    for _ in range(5):
+        x = USUAL[0] * x + USUAL[1] * x ** 3 + USUAL[2] * x ** 5
+    want = torch.stack([h / 8, perm, -perm]).double() * x.view(3, 1, 1)
+    # Each step's derivative is at most 3.95 in size, and each is off by at most
+    # 16 roundings of 2^-22 of values up to 14.5: 14.5 * 16 * (1 + ... + 3.95^4) roundings.
+    assert (call(m).double().cpu() - want).abs().max() <= 14.5 * 16 * 325 * 2.0 ** -22 * float(x.max()) / 8
+
+
+@pytest.mark.gpu
+def test_extremes():
+    m = draw(5, 40, 56)
+    m[1] = 0.0
+    m[2, 3, 4] = float("nan")
+    m[3, 0, 0] = float("inf")
+    got = call(m)
+    assert not got[1].any() and torch.isnan(got[2]).all() and torch.isnan(got[3]).all()
+    keep = [0, 4]
+    near(got[keep], m[keep], "f32")
+    assert torch.equal(got[keep], call(m[keep]))
+    one = torch.zeros(1, 33, 65)
+    one[0, 32, 64] = 5.0  # a single element: its singular value is 1
+    near(call(one), one, "f32")
+
+
+@pytest.mark.gpu
+def test_in_place_streams_repeats_and_graph_replays():
+    m = draw(4, 100, 180, dtype="bf16")
+    want = call(m)
+    s = torch.cuda.Stream()
+    for stream in (None, s, s):
+        assert torch.equal(call(m, stream=stream), want)
+    p = cbd.ortho_plan(4, 100, 180, "bf16")
+    x = m.cuda()
+    assert cbd.orthogonalize(p, x, out=x) is x and torch.equal(x, want)
+    with pytest.raises(cbd.CbdError, match="overlaps"):
+        wide = torch.zeros(4, 100, 190, dtype=torch.bfloat16, device="cuda")
+        cbd.orthogonalize(p, wide[:, :, :180], out=wide[:, :, 10:])
+    x = m.cuda()
+    out, ws = torch.empty_like(x), torch.empty(p.workspace_size(), dtype=torch.uint8, device="cuda")
+    cbd.orthogonalize(p, x, out, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cbd.orthogonalize(p, x, out, ws)
+    for i in range(4):
+        x.copy_(draw(4, 100, 180, dtype="bf16", seed=i + 1))
+        ws.fill_(0xff)
+        graph.replay()
+        torch.cuda.synchronize()
+        mine = out.clone()
+        torch.cuda.synchronize()
+        assert torch.equal(mine, cbd.orthogonalize(p, x)), i
+
+
+@pytest.mark.gpu
+def test_convenience_and_written():
+    m = draw(6, 40, 24).cuda()
+    want = cbd.orthogonalize(cbd.ortho_plan(6, 40, 24), m)
+    assert torch.equal(cbd.orthogonalized(m), want)
+    assert torch.equal(cbd.orthogonalized(m.view(2, 3, 40, 24)), want.view(2, 3, 40, 24))
+    assert torch.equal(cbd.orthogonalized(m[1]), want[1])
+    assert torch.equal(cbd.orthogonalized(m[::2]), want[::2])
+    assert cbd.orthogonalized(m[:0]).shape == (0, 40, 24)
+    t = torch.zeros_like(m)
+    loss = (torch.ones_like(t, requires_grad=True) * t).sum()
+    cbd.orthogonalize(cbd.ortho_plan(6, 40, 24), m, out=t)
+    with pytest.raises(RuntimeError, match="inplace"):
+        loss.backward()
+
+
+# ------------------------------------------------------------ refusals (CPU)
+
+@pytest.mark.parametrize("over,status", [
+    (dict(matrices=-1), 1), (dict(rows=0), 1), (dict(cols=-2), 1), (dict(dtype=2), 1), (dict(steps=0), 1),
+    (dict(steps=65), 1), (dict(eps=0.0), 1), (dict(eps=float("nan")), 1), (dict(scale=float("inf")), 1),
+    (dict(matrices=65536), 2), (dict(rows=65537), 2), (dict(cols=65537), 2), (dict(matrices=0), 0), (dict(), 0),
+    (dict(co=(3.0, float("nan"), 1.0)), 1), (dict(co=(0.0, 0.0, 0.0)), 2), (dict(co=(9.0, 9.0, 9.0)), 2),
+    (dict(co=(1e-30, 0.0, 0.0)), 2), (dict(co=(1.5, -0.5, 0.0)), 0)])
+def test_plan_refusals(over, status):
+    kw = dict(matrices=2, rows=16, cols=24, dtype=cbd.F32, steps=5, eps=1e-7, scale=1.0)
+    co = over.pop("co", None)
+    kw.update(over)
+    if co:
+        kw["coefficients"] = (ctypes.c_double * 15)(*(co * 5))
+    h = ctypes.c_void_p()
+    assert cbd._lib.cbd_ortho_plan(ctypes.byref(cbd.OrthoProblem(**kw)), ctypes.byref(h)) == status
+    assert bool(h.value) == (status == 0)
+    if status:
+        assert cbd._lib.cbd_last_error()
+    cbd._lib.cbd_ortho_plan_destroy(h)
+
+
+def test_run_refusals():
+    """Argument checks come before any launch, so made-up addresses do."""
+    S = cbd.OrthoStrides
+    p = cbd.ortho_plan(3, 16, 24)
+    i, o, ws, size = 0x10000, 0x20000, 0x1000000, p.workspace_size()
+
+    def run(i=i, o=o, ws=ws, size=size, s=None, plan=p._h):
+        return cbd._lib.cbd_orthogonalize(plan, i, o, ctypes.byref(s) if s else None, ws, size, None)
+
+    assert run(plan=None) == 1 and run(i=None) == 1 and run(o=None) == 1 and run(ws=None) == 1
+    assert run(size=size - 1) == 1 and run(ws=ws + 128) == 2
+    assert run(i=i + 2) == 2 and run(o=o + 1) == 2
+    assert run(s=S(23, 0, 0, 0)) == 1 and run(s=S(0, 0, 23, 0)) == 1 and run(s=S(0, 383, 0, 0)) == 1
+    assert run(s=S(0, 0, 0, -1)) == 1 and run(s=S(2 ** 31 + 1, 0, 0, 0)) == 2 and run(s=S(0, 2 ** 40 + 1, 0, 0)) == 2
+    assert run(o=i + 4) == 1 and run(o=i, s=S(24, 384, 32, 512)) == 1 and run(o=ws) == 1 and run(i=ws + 64) == 1
+    none = cbd.ortho_plan(0, 16, 24)
+    assert run(plan=none._h, i=None, o=None, ws=None, size=0) == 0
+
+
+def test_python_refusals_without_a_gpu():
+    with pytest.raises(ValueError, match="GPU"):
+        cbd.orthogonalize(cbd.ortho_plan(1, 4, 4), torch.zeros(1, 4, 4))
+    with pytest.raises(ValueError, match="triples"):
+        cbd.ortho_plan(1, 4, 4, coefficients=[(1.0, 2.0)])
+    with pytest.raises(ValueError, match="triples"):
+        cbd.ortho_plan(1, 4, 4, coefficients=[(1.5, -0.5, 0.0)] * 4)
+    with pytest.raises(ValueError, match="matrices"):
+        cbd.orthogonalized(torch.zeros(4))
+    with pytest.raises(ValueError, match="bfloat16"):
+        cbd.orthogonalized(torch.zeros(4, 4, dtype=torch.float64))
+
+
+@pytest.mark.gpu
+def test_python_refusals():
+    p = cbd.ortho_plan(2, 4, 8)
+    m = torch.zeros(2, 4, 8, device="cuda")
+    for bad in (m.bfloat16(), m[:1], m[:, :, :7], m.transpose(1, 2), m[:1].expand(2, 4, 8)):
+        with pytest.raises(ValueError):
+            cbd.orthogonalize(p, bad)
+    with pytest.raises(ValueError):
+        cbd.orthogonalize(p, m, out=torch.zeros(2, 4, 8))
+    with pytest.raises(cbd.CbdError, match="workspace"):
+        cbd.orthogonalize(p, m, workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"))
