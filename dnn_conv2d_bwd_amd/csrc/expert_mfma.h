@@ -536,16 +536,58 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void expert_mfma_kernel(
   // Gated results.  Forward: a wave's blocks m are of the gate for m < MB / 2,
   // the others of the same features of the other projection; h and, saved, the
   // two leave one after another through the wave's buffer, HM blocks wide.
-  // Backward: 32 features of dh at a time in f32, four a lane, which meet the
-  // same four of g and u there.
-  [[maybe_unused]] auto finish_gated = [&](const Tile& c, auto lc, f32x16 (&acc)[MB][decltype(lc)::value]) CBD_INLINE {
+  // Backward: 16 rows by 64 features of dh at a time in f32, eight a lane, which
+  // meet the same eight of g and u there.
+  struct Gates {
+    u32x4 g[4], u[4];  // of 32 rows by 64 features
+  };
+  [[maybe_unused]] auto fetch = [&](const Tile& c, int n, int h, Gates& x) CBD_INLINE {
+    if constexpr (GATE == GATE_BWD) {
+      const int tid = fresh_tid(), lane = tid & 63;
+      const int wm = (tid >> 6) & 1, wn = tid >> 7;
+      const uint16_t* const gs = (const uint16_t*)a.gu + c.n0 * a.ldgu + c.m0;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const int row = 64 * n + 32 * wn + 8 * i + (lane >> 3), f = 32 * MB * wm + 64 * h + 8 * (lane & 7);
+        if constexpr (OUT != ANY) {
+          const uint32_t off = row < c.nrows && f < c.mrows ? ((uint32_t)row * (uint32_t)a.ldgu + (uint32_t)f) * 2u
+                                                            : dev::kOOB;
+          x.g[i] = __builtin_amdgcn_raw_buffer_load_b128(dev::rsrc(gs, 0x7ffffffcu), off, 0, kStoreAux);
+          x.u[i] = __builtin_amdgcn_raw_buffer_load_b128(dev::rsrc(gs + a.M, 0x7ffffffcu), off, 0, kStoreAux);
+        } else {
+          x.g[i] = x.u[i] = u32x4{0u, 0u, 0u, 0u};
+          if (row < c.nrows) {
+            const uint16_t* const q = gs + row * a.ldgu + f;
+            if (c.mrows - f >= 8) {
+              x.g[i] = *(const u32x4u*)q;
+              x.u[i] = *(const u32x4u*)(q + a.M);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 7; j++)
+                if (f + j < c.mrows) {
+                  x.g[i][j >> 1] |= (uint32_t)q[j] << (16 * (j & 1));
+                  x.u[i][j >> 1] |= (uint32_t)q[a.M + j] << (16 * (j & 1));
+                }
+            }
+          }
+        }
+      }
+    }
+  };
+  // Units of 32 rows by 64 features, and how many of them have their gates
+  // fetched ahead: all at the start of the main loop, or (256 x 256, and without
+  // DMA: registers) one before the next tile's first loads, the others each a
+  // unit before.
+  constexpr int UNITS = MB / 2;
+  [[maybe_unused]] constexpr bool EARLY = GATE == GATE_BWD && MB == 2 && DMA;
+  [[maybe_unused]] auto finish_gated = [&](const Tile& c, auto lc, f32x16 (&acc)[MB][decltype(lc)::value],
+                                           Gates (&ahead)[EARLY ? UNITS * decltype(lc)::value : 1]) CBD_INLINE {
     if constexpr (GATE != GATE_NONE) {
       constexpr int L = decltype(lc)::value;
       const int tid = fresh_tid(), lane = tid & 63;
       const int wm = (tid >> 6) & 1, wn = tid >> 7;
       char* const st0 = smem + STAGES + (tid >> 6) * (SBUF * 4096);
       const int r = lane & 31, hi = lane >> 5;
-      const dev::Gate gate(a.act);
       if constexpr (PAIR) {
         constexpr int GM = MB / 2, CH = 4 * GM;   // blocks, and chunks of a row
         constexpr int OUTS = GATE == GATE_FWD ? 1 : 3;
@@ -568,19 +610,24 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void expert_mfma_kernel(
 #pragma unroll
               for (int m = 0; m < MB; m++) asm volatile("" : "+a"(acc[m][n]));
             }
+            auto stage = [&](auto&& value) CBD_INLINE {
 #pragma unroll
-            for (int m = 0; m < GM; m++)
+              for (int m = 0; m < GM; m++)
 #pragma unroll
-              for (int q = 0; q < 4; q++) {
-                float v[4];
+                for (int q = 0; q < 4; q++) {
+                  float v[4];
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                  const float g = acc[m][n][4 * q + j], u = acc[m + GM][n][4 * q + j];
-                  v[j] = o == 0 ? gate.act<false>(g) * u : o == 1 ? g : u;
+                  for (int j = 0; j < 4; j++) v[j] = value(acc[m][n][4 * q + j], acc[m + GM][n][4 * q + j]);
+                  *(u32x2*)(st + r * 128 + (((4 * m + q) ^ (r & 7)) << 4) + (hi << 3)) =
+                      u32x2{dev::bf16_pack2(v[0], v[1]), dev::bf16_pack2(v[2], v[3])};
                 }
-                *(u32x2*)(st + r * 128 + (((4 * m + q) ^ (r & 7)) << 4) + (hi << 3)) =
-                    u32x2{dev::bf16_pack2(v[0], v[1]), dev::bf16_pack2(v[2], v[3])};
-              }
+            };
+            if (o == 1)
+              stage([](float g, float) { return g; });
+            else if (o == 2)
+              stage([](float, float u) { return u; });
+            else
+              dev::with_gate(a.act, [&](auto kind) CBD_INLINE { stage([&](float g, float u) { return kind.act(g) * u; }); });
             asm volatile("" ::: "memory");  // a wave's LDS accesses run in order
 #pragma unroll
             for (int it = 0; it < 2 * GM; it++) {
@@ -593,65 +640,60 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void expert_mfma_kernel(
           }
         }
       } else {
-        const uint16_t* const gs = (const uint16_t*)a.gu + c.n0 * a.ldgu + c.m0;
 #pragma unroll
-        for (int i = 0; i < L * MB; i++) {
-          const int n = i / MB, m = i % MB;
-          const int fm = 32 * MB * wm + 32 * m, rn = 64 * n + 32 * wn;
-          char* const st = st0 + (i % SBUF) * 4096;
-          if constexpr (MB == 4) asm volatile("" : "+a"(acc[m][n]));
-          u32x2 gv[4], uv[4];
+        for (int i = 0; i < L * UNITS; i++) {
+          const int n = i / UNITS, h = i % UNITS;
+          if constexpr (MB == 4) {
 #pragma unroll
-          for (int it = 0; it < 4; it++) {
-            const int row = rn + 8 * it + (lane >> 3), f = fm + 4 * (lane & 7);
-            if constexpr (OUT != ANY) {
-              const uint32_t off = row < c.nrows && f < c.mrows
-                                       ? ((uint32_t)row * (uint32_t)a.ldgu + (uint32_t)f) * 2u
-                                       : dev::kOOB;
-              gv[it] = __builtin_amdgcn_raw_buffer_load_b64(dev::rsrc(gs, 0x7ffffffcu), off, 0, 0);
-              uv[it] = __builtin_amdgcn_raw_buffer_load_b64(dev::rsrc(gs + a.M, 0x7ffffffcu), off, 0, 0);
-            } else {
-              gv[it] = uv[it] = u32x2{0u, 0u};
-              if (row < c.nrows) {
-                const uint16_t* const q = gs + row * a.ldgu + f;
-                typedef uint32_t words __attribute__((ext_vector_type(2), aligned(2)));
-                if (c.mrows - f >= 4) {
-                  gv[it] = *(const words*)q;
-                  uv[it] = *(const words*)(q + a.M);
-                } else {
+            for (int m = 0; m < 2; m++) asm volatile("" : "+a"(acc[2 * h + m][n]));
+          }
+          const Gates x = ahead[EARLY ? i : 0];
+          if (!EARLY && i + 1 < L * UNITS) fetch(c, (i + 1) / UNITS, (i + 1) % UNITS, ahead[0]);
 #pragma unroll
-                  for (int j = 0; j < 3; j++)
-                    if (f + j < c.mrows) {
-                      gv[it][j >> 1] |= (uint32_t)q[j] << (16 * (j & 1));
-                      uv[it][j >> 1] |= (uint32_t)q[a.M + j] << (16 * (j & 1));
-                    }
+          for (int half = 0; half < 2; half++) {
+            char* const st = st0 + (SBUF == 2 && half ? 4096 : 0);
+            // 16 rows of 64 features, chunk k (4 of them) of row r at k ^ r.
+            if ((r >> 4) == half) {
+#pragma unroll
+              for (int m = 0; m < 2; m++)
+#pragma unroll
+                for (int q = 0; q < 4; q++)
+                  *(f32x4*)(st + (r & 15) * 256 + (((8 * m + 2 * q + hi) ^ (r & 15)) << 4)) =
+                      f32x4{acc[2 * h + m][n][4 * q], acc[2 * h + m][n][4 * q + 1], acc[2 * h + m][n][4 * q + 2],
+                            acc[2 * h + m][n][4 * q + 3]};
+            }
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int it = 0; it < 2; it++) {
+              const int row = 8 * it + (lane >> 3), ch = lane & 7;
+              u32x4 dg, du;
+              dev::with_gate(a.act, [&](auto kind) CBD_INLINE {
+#pragma unroll
+                for (int p = 0; p < 2; p++) {
+                  const f32x4 dh = *(const f32x4*)(st + row * 256 + (((2 * ch + p) ^ row) << 4));
+                  float vg[4], vu[4];
+#pragma unroll
+                  for (int j = 0; j < 4; j++) {
+                    const uint32_t wg = x.g[2 * half + it][2 * p + (j >> 1)], wu = x.u[2 * half + it][2 * p + (j >> 1)];
+                    const float g = __uint_as_float(j & 1 ? wg & 0xffff0000u : wg << 16);
+                    const float u = __uint_as_float(j & 1 ? wu & 0xffff0000u : wu << 16);
+                    float slope;
+                    vu[j] = dh[j] * kind.act(g, &slope);
+                    vg[j] = dh[j] * u * slope;
+                  }
+#pragma unroll
+                  for (int j = 0; j < 2; j++) {
+                    dg[2 * p + j] = dev::bf16_pack2(vg[2 * j], vg[2 * j + 1]);
+                    du[2 * p + j] = dev::bf16_pack2(vu[2 * j], vu[2 * j + 1]);
+                  }
                 }
-              }
+              });
+              const int at = 64 * n + 32 * wn + 16 * half + row, f = 32 * MB * wm + 64 * h + 8 * ch;
+              put(c, c.out, a.ldo, at, f, dg);
+              put(c, c.out + a.M, a.ldo, at, f, du);
             }
+            asm volatile("" ::: "memory");
           }
-#pragma unroll
-          for (int q = 0; q < 4; q++)
-            *(f32x4*)(st + r * 128 + (((2 * q + hi) ^ (r & 7)) << 4)) =
-                f32x4{acc[m][n][4 * q], acc[m][n][4 * q + 1], acc[m][n][4 * q + 2], acc[m][n][4 * q + 3]};
-          asm volatile("" ::: "memory");
-#pragma unroll
-          for (int it = 0; it < 4; it++) {
-            const int row = 8 * it + (lane >> 3), ch = lane & 7;
-            const f32x4 dh = *(const f32x4*)(st + row * 128 + ((ch ^ (row & 7)) << 4));
-            float dg[4], du[4];
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-              const float g = dev::bf16_to_f32(j & 1 ? gv[it][j >> 1] >> 16 : gv[it][j >> 1] & 0xffffu);
-              const float u = dev::bf16_to_f32(j & 1 ? uv[it][j >> 1] >> 16 : uv[it][j >> 1] & 0xffffu);
-              float slope;
-              du[j] = dh[j] * gate.act<false>(g, slope);
-              dg[j] = dh[j] * u * slope;
-            }
-            put(c, c.out, a.ldo, rn + row, fm + 4 * ch, u32x2{dev::bf16_pack2(dg[0], dg[1]), dev::bf16_pack2(dg[2], dg[3])});
-            put(c, c.out + a.M, a.ldo, rn + row, fm + 4 * ch,
-                u32x2{dev::bf16_pack2(du[0], du[1]), dev::bf16_pack2(du[2], du[3])});
-          }
-          asm volatile("" ::: "memory");
           __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -681,6 +723,14 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void expert_mfma_kernel(
     constexpr int RQ = Q >= 8 ? Q - 4 : Q > 1 ? Q - 1 : 1;
     bf16x8 a0[MB], a1[MB], b0[L], b1[L];
     const f32x16 zero = {};
+    [[maybe_unused]] Gates ahead[EARLY ? UNITS * L : 1];
+    // Between the tile's first loads and the main loop's.
+    auto fetch_early = [&]() CBD_INLINE {
+      if constexpr (EARLY) {
+#pragma unroll
+        for (int i = 0; i < UNITS * L; i++) fetch(c, i / UNITS, i % UNITS, ahead[i]);
+      }
+    };
     auto read_one = [&](int stage, int ks, int r, bf16x8 (&ra)[MB], bf16x8 (&rb)[L]) CBD_INLINE {
       // In the order of use: A block 0, B block 0, the other A, the other B.
       if (r < RA || (r >= RA + RB && r < MB * RA + RB)) {
@@ -721,6 +771,7 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void expert_mfma_kernel(
       else
         __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(AHEAD));
       __builtin_amdgcn_s_barrier();
+      fetch_early();
 #pragma unroll
       for (int r = 0; r < R; r++) read_one(0, 0, r, a0, b0);
       // Loads past the last step fetch zeros (a record count of 0); the next
@@ -811,11 +862,12 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void expert_mfma_kernel(
       }
     }
     const Tile done = c;
+    if constexpr (GATE == GATE_BWD && !EARLY) fetch(done, 0, 0, ahead[0]);
     if (t.ok) c = begin(t);
     if constexpr (GATE == GATE_NONE)
       finish(done, lc, acc);
     else
-      finish_gated(done, lc, acc);
+      finish_gated(done, lc, acc, ahead);
   };
   // Zeros, where nothing is contracted (added: nothing to do).
   auto blank = [&]() CBD_INLINE {

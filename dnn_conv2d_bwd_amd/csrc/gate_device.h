@@ -50,6 +50,39 @@ struct Gate {
   }
 };
 
+// For bf16 results, one activation at a time: half the instructions of the
+// general form, by the hardware's exp2 and reciprocal.  f(kind) is called with
+// one of these.
+template <int ACT>
+struct GateOf {
+  static constexpr float A = ACT == CBD_ACT_GELU ? 1.5957691216057308f : 1.f, B = A * 0.044715f, LOG2E = 1.4426950408889634f;
+  __device__ static inline float act(float g, float* slope = nullptr) {
+    if constexpr (ACT == CBD_ACT_RELU) {
+      if (slope) *slope = g > 0.f ? 1.f : 0.f;
+      return g <= 0.f ? 0.f : g;
+    } else {
+      float t = -LOG2E * g, bend = 1.f;  // -t log2(e), and t'(g)
+      if constexpr (ACT == CBD_ACT_GELU) {
+        const float q = Gate::square(g);
+        t = g * __builtin_fmaf(-B * LOG2E, q, -A * LOG2E);
+        bend = __builtin_fmaf(3.f * B, q, A);
+      }
+      const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(t)), v = g * s;
+      if (slope) *slope = __builtin_fmaf(v * (1.f - s), bend, s);
+      return v;
+    }
+  }
+};
+template <typename F>
+CBD_INLINE __device__ inline void with_gate(int act, F&& f) {
+  if (act == CBD_ACT_SILU)
+    f(GateOf<CBD_ACT_SILU>());
+  else if (act == CBD_ACT_GELU)
+    f(GateOf<CBD_ACT_GELU>());
+  else
+    f(GateOf<CBD_ACT_RELU>());
+}
+
 // Row r of an operand tile of F rows that holds two projections, for W waves
 // side by side: every wave has F / W rows, first those of the gate, then the
 // same features of the other projection.

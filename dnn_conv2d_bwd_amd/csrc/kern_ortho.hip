@@ -131,18 +131,15 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void ortho_product_kernel
   };
 
   f32x16 acc[MB][MB];
-#pragma unroll
-  for (int i = 0; i < MB; i++)
-#pragma unroll
-    for (int j = 0; j < MB; j++) acc[i][j] = f32x16{};
 
   // MFMAs on (x, y), with R reads and L loads spread between them.
-  auto part = [&](const f16x8 (&x)[MB], const f16x8 (&y)[MB], auto rc, auto&& rd, auto lc, auto&& ld) INLINE {
+  const f32x16 zero = {};
+  auto part = [&](auto firstc, const f16x8 (&x)[MB], const f16x8 (&y)[MB], auto rc, auto&& rd, auto lc, auto&& ld) INLINE {
     constexpr int Q = MB * MB, R = decltype(rc)::value, L = decltype(lc)::value;
 #pragma unroll
     for (int i = 0; i < Q; i++) {
       const int n = i / MB, m = (n & 1) ? MB - 1 - i % MB : i % MB;
-      acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[m], y[n], acc[m][n], 0, 0, 0);
+      acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[m], y[n], firstc.value ? zero : acc[m][n], 0, 0, 0);
 #pragma unroll
       for (int r = i * R / Q; r < (i + 1) * R / Q; r++) rd(r);
 #pragma unroll
@@ -174,25 +171,26 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void ortho_product_kernel
   // Run k in stage S, whose first hi fragments are in registers.  The other
   // stage gets the second operand's run k + 1 here, and this one, once every
   // wave has read it, the first operand's run k + 2.
-  auto run = [&](int k, auto sc) INLINE {
+  auto run = [&](int k, auto sc, auto firstc) INLINE {
     constexpr int S = decltype(sc)::value;
-    part(ph0, qh0, two,
+    part(firstc, ph0, qh0, two,
          [&](int r) { r < MB ? (void)(ql[r] = read_q(S, 0, 1, r)) : (void)(pl[r - MB] = read_p(S, 0, 1, r - MB)); }, all,
          [&](int i) { load_q(k + 1, 1 - S, i); });
-    part(ph0, ql, one, [&](int r) { ph1[r] = read_p(S, 1, 0, r); }, none, nothing);
-    part(pl, qh0, one, [&](int r) { qh1[r] = read_q(S, 1, 0, r); }, none, nothing);
-    part(ph1, qh1, two,
+    part(std::false_type(), ph0, ql, one, [&](int r) { ph1[r] = read_p(S, 1, 0, r); }, none, nothing);
+    part(std::false_type(), pl, qh0, one, [&](int r) { qh1[r] = read_q(S, 1, 0, r); }, none, nothing);
+    part(std::false_type(), ph1, qh1, two,
          [&](int r) { r < MB ? (void)(ql[r] = read_q(S, 1, 1, r)) : (void)(pl[r - MB] = read_p(S, 1, 1, r - MB)); }, none,
          nothing);
     wait_all();
     barrier();
-    part(ph1, ql, one, [&](int r) { ph0[r] = read_p(1 - S, 0, 0, r); }, all, [&](int i) { load_p(k + 2, S, i); });
-    part(pl, qh1, one, [&](int r) { qh0[r] = read_q(1 - S, 0, 0, r); }, none, nothing);
+    part(std::false_type(), ph1, ql, one, [&](int r) { ph0[r] = read_p(1 - S, 0, 0, r); }, all, [&](int i) { load_p(k + 2, S, i); });
+    part(std::false_type(), pl, qh1, one, [&](int r) { qh0[r] = read_q(1 - S, 0, 0, r); }, none, nothing);
   };
+  run(0, std::integral_constant<int, 0>(), std::true_type());
 #pragma unroll 1
-  for (int k = 0; k < a.runs; k += 2) {
-    run(k, std::integral_constant<int, 0>());
-    if (k + 1 < a.runs) run(k + 1, std::integral_constant<int, 1>());
+  for (int k = 1; k < a.runs; k += 2) {
+    run(k, std::integral_constant<int, 1>(), std::false_type());
+    if (k + 1 < a.runs) run(k + 1, std::integral_constant<int, 0>(), std::false_type());
   }
   // The last loads (zeros) have landed, and everyone has read the stages.
   wait_all();
@@ -278,6 +276,7 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void ortho_product_kernel
           leave(a.c + mat * a.c_mat + (int64_t)row0 * a.ldc + ((n0 + 32 * n) >> 5) * 64, a.ldc);
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
 }
 
@@ -291,20 +290,41 @@ __device__ inline float value(const void* p, int64_t i) {
     return dev::bf16_to_f32(((const uint16_t*)p)[i]);
 }
 
-// Sums of squares in 64 bits: workgroup i of a matrix takes rows i, i + 64, ...
+// Sums of squares in 64 bits: wave i of a matrix's takes rows i, i + all, ...,
+// 16 bytes a lane at any alignment.
 template <typename T>
 __global__ __launch_bounds__(THREADS) void ortho_norm_kernel(const OrthoSplit a) {
-  __shared__ double part[THREADS / 64];
+  constexpr int V = 16 / sizeof(T), WAVES = THREADS / 64;
+  typedef uint32_t u32x4_4 __attribute__((ext_vector_type(4), aligned(4)));
+  typedef uint32_t u32x4_2 __attribute__((ext_vector_type(4), aligned(2)));
+  using any = std::conditional_t<sizeof(T) == 4, u32x4_4, u32x4_2>;
+  __shared__ double part[WAVES];
   const int64_t mat = blockIdx.y;
-  double s = 0.0;
-  for (int64_t row = blockIdx.x; row < a.rows; row += kOrthoParts)
-    for (int col = threadIdx.x; col < a.cols; col += THREADS) {
-      const double v = value<T>(a.in, mat * a.in_mat + row * a.in_row + col);
-      s = __builtin_fma(v, v, s);
-    }
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  double s[2] = {0.0, 0.0};
+  auto add = [&](int j, float f) INLINE { s[j & 1] = __builtin_fma((double)f, (double)f, s[j & 1]); };
+  for (int64_t row = blockIdx.x * WAVES + wave; row < a.rows; row += kOrthoParts * WAVES) {
+    const T* const p = (const T*)a.in + mat * a.in_mat + row * a.in_row;
+    int col = V * lane;
+#pragma unroll 4
+    for (; col + V <= a.cols; col += 64 * V) {
+      const u32x4 v = *(const any*)(p + col);
 #pragma unroll
-  for (int m = 32; m > 0; m >>= 1) s += __shfl_xor(s, m, 64);
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+      for (int j = 0; j < 4; j++) {
+        if constexpr (sizeof(T) == 4) {
+          add(j, __uint_as_float(v[j]));
+        } else {
+          add(0, __uint_as_float(v[j] << 16));
+          add(1, __uint_as_float(v[j] & 0xffff0000u));
+        }
+      }
+    }
+    for (int j = 0; j < V && col + j < a.cols; j++) add(j, value<T>(p, col + j));
+  }
+  double sum = s[0] + s[1];
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) sum += __shfl_xor(sum, m, 64);
+  if (lane == 0) part[wave] = sum;
   __syncthreads();
   if (threadIdx.x == 0) a.partial[mat * kOrthoParts + blockIdx.x] = (part[0] + part[1]) + (part[2] + part[3]);
 }
@@ -316,7 +336,9 @@ __global__ __launch_bounds__(THREADS) void ortho_split_kernel(const OrthoSplit a
   const int64_t mat = blockIdx.z;
   const int row0 = blockIdx.y * 64, col0 = blockIdx.x * 64, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   // Every wave adds the parts in the same order.
-  double s = a.partial[mat * kOrthoParts + lane];
+  double s = 0.0;
+#pragma unroll
+  for (int i = 0; i < kOrthoParts / 64; i++) s += a.partial[mat * kOrthoParts + 64 * i + lane];
 #pragma unroll
   for (int m = 32; m > 0; m >>= 1) s += __shfl_xor(s, m, 64);
   const double f = a.up / (__builtin_sqrt(s) + a.eps);

@@ -52,7 +52,7 @@ struct OrthoSplit {
   int32_t ldx, ldxt;
 };
 
-constexpr int kOrthoParts = 64;
+constexpr int kOrthoParts = 256;
 
 int launch_ortho_norm(const OrthoSplit& a, int64_t matrices, void* stream);
 int launch_ortho_split(const OrthoSplit& a, int64_t matrices, void* stream);
