@@ -23,7 +23,7 @@ import ctypes
 import functools
 
 from . import BF16, F32, _check, _dtype, _lib, _torch_dtype
-from .experts import _handle, _on, _records, _strided, _written
+from .experts import _DENSE, _any_records, _handle, _on, _strided, _written
 
 GATE_NONE, GATE_CHANNEL, GATE_ROW = 0, 1, 2
 
@@ -79,6 +79,7 @@ class BlockPlan:
         _check(_lib.cbd_block_workspace_size(h, ctypes.byref(out)), "cbd_block_workspace_size")
         self._ws = int(out.value)
         self._tdtype, self._tdw = _torch_dtype(self.dtype), _torch_dtype(self.dw_dtype)
+        self._shape, self._vshape = (self.rows, self.c), (self.c,)
 
     def workspace_size(self) -> int:
         """Bytes of device workspace the backward call needs."""
@@ -97,62 +98,72 @@ def block_plan(rows, c, dtype="bf16", dw_dtype=None, eps=1e-6, scale=1.0) -> Blo
     return BlockPlan(rows, c, dtype, dw_dtype, eps, scale)
 
 
-def _vector(t, p, device, name, dtype=None):
-    dtype = p._tdtype if dtype is None else dtype
-    if (not hasattr(t, "data_ptr") or not t.is_cuda or t.dtype != dtype or t.shape != (p.c,)
-            or t.device != device or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape ({p.c},) on {device}")
+def _vector(t, p, device, name):
+    if (not hasattr(t, "data_ptr") or t.dtype is not p._tdtype or t.shape != p._vshape or t.get_device() != device.index
+            or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {p._tdtype} tensor of shape ({p.c},) on {device}")
+    return t.data_ptr()
 
 
 def _params(p, r, y, w_post, gate, w_pre, strides):
-    """Checks the operands; the struct of the parameters, and the device."""
-    shape = (p.rows, p.c)
-    strides.r = _strided(r, shape, p._tdtype, None, "r")[0]
+    """Checks the operands; the struct of the parameters, and the device.
+    strides: the row strides that are not dense, by name."""
+    s = _strided(r, p._shape, p._tdtype, None, "r")
     dev = r.device
+    if s is not _DENSE[2]:
+        strides["r"] = s[0]
     if y is not None:
-        strides.y = _strided(y, shape, p._tdtype, dev, "y")[0]
+        s = _strided(y, p._shape, p._tdtype, dev, "y")
+        if s is not _DENSE[2]:
+            strides["y"] = s[0]
     elif w_post is not None or gate is not None:
         raise ValueError("w_post and gate need y")
-    kind = GATE_NONE
+    kind, at = GATE_NONE, None
     if gate is not None:
-        kind = GATE_CHANNEL if gate.dim() == 1 else GATE_ROW
-        if kind == GATE_CHANNEL:
-            _vector(gate, p, dev, "gate")
+        if gate.dim() == 1:
+            kind, at = GATE_CHANNEL, _vector(gate, p, dev, "gate")
         else:
-            strides.gate = _strided(gate, shape, p._tdtype, dev, "gate")[0]
-    for name, w in (("w_post", w_post), ("w_pre", w_pre)):
-        if w is not None:
-            _vector(w, p, dev, name)
-    return BlockParams(_ptr(w_post), _ptr(gate), _ptr(w_pre), kind, 0), dev
+            kind, at = GATE_ROW, gate.data_ptr()
+            s = _strided(gate, p._shape, p._tdtype, dev, "gate")
+            if s is not _DENSE[2]:
+                strides["gate"] = s[0]
+    return BlockParams(None if w_post is None else _vector(w_post, p, dev, "w_post"), at,
+                       None if w_pre is None else _vector(w_pre, p, dev, "w_pre"), kind, 0), dev
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _rows(p, t, name, device):
-    """An output of rows and its stride: allocated, or the caller's."""
+def _rows(p, t, name, device, strides):
+    """An output of rows: allocated, or the caller's."""
     import torch
 
     if t is None:
-        return torch.empty((p.rows, p.c), dtype=p._tdtype, device=device), 0
-    s = _strided(t, (p.rows, p.c), p._tdtype, device, name)[0]
+        return torch.empty(p._shape, dtype=p._tdtype, device=device)
+    s = _strided(t, p._shape, p._tdtype, device, name)
+    if s is not _DENSE[2]:
+        strides[name] = s[0]
     _written(t)
-    return t, s
+    return t
+
+
+def _struct(strides):
+    return ctypes.byref(BlockStrides(**strides)) if strides else None
 
 
 def _forward(p, r, y, w_post, gate, w_pre, save, z, n, stats, stream):
     import torch
 
-    st = BlockStrides()
+    st = {}
     params, dev = _params(p, r, y, w_post, gate, w_pre, st)
     if (z is not None and y is None) or (n is not None and w_pre is None):
         raise ValueError("z goes with y, and n with w_pre")
     with _on(dev, stream):
         if y is not None:
-            z, st.z = _rows(p, z, "z", dev)
+            z = _rows(p, z, "z", dev, st)
         if w_pre is not None:
-            n, st.n = _rows(p, n, "n", dev)
+            n = _rows(p, n, "n", dev, st)
         if stats is not None:
             if stats.dtype != torch.float32 or stats.shape != (p.rows, 2) or stats.device != dev or not stats.is_contiguous():
                 raise ValueError(f"stats must be a contiguous float32 tensor of shape ({p.rows}, 2) on {dev}")
@@ -160,7 +171,7 @@ def _forward(p, r, y, w_post, gate, w_pre, save, z, n, stats, stream):
         elif save:
             stats = torch.empty((p.rows, 2), dtype=torch.float32, device=dev)
         _check(_lib.cbd_block_forward(p._h, r.data_ptr(), _ptr(y), ctypes.byref(params), _ptr(z), _ptr(n),
-                                      _ptr(stats), ctypes.byref(st), _handle(stream, dev)), "cbd_block_forward")
+                                      _ptr(stats), _struct(st), _handle(stream, dev)), "cbd_block_forward")
     return z, n, stats
 
 
@@ -169,7 +180,7 @@ def block_forward(p: BlockPlan, r, y=None, w_post=None, gate=None, w_pre=None, s
     """(z, n) on `stream` (default: torch's current one), and with save, or given
     stats, (z, n, stats); outputs are allocated unless given.  z may be r, and n
     y, for a step in place.  stats [T, 2] (f32) is what block_bwd reads."""
-    if any(_records(t, None) for t in (r, y, w_post, gate, w_pre)):
+    if _any_records((r, y, w_post, gate, w_pre)):
         if z is not None or n is not None or stats is not None:
             raise ValueError("autograd cannot record a call into a given output: an operand requires gradients "
                              "(or has a tangent); leave the outputs out or call under torch.no_grad()")
@@ -185,13 +196,13 @@ def _bwd(p, dz, dn, r, y, stats, w_post, gate, w_pre, want, given, workspace, st
     """want: which of dr, dy, dw_post, dgate, dw_pre; given: row outputs."""
     import torch
 
-    st = BlockStrides()
+    st = {}
     params, dev = _params(p, r, y, w_post, gate, w_pre, st)
-    shape = (p.rows, p.c)
-    if dz is not None:
-        st.dz = _strided(dz, shape, p._tdtype, dev, "dz")[0]
-    if dn is not None:
-        st.dn = _strided(dn, shape, p._tdtype, dev, "dn")[0]
+    for name, t in (("dz", dz), ("dn", dn)):
+        if t is not None:
+            s = _strided(t, p._shape, p._tdtype, dev, name)
+            if s is not _DENSE[2]:
+                st[name] = s[0]
     if (w_post is not None or w_pre is not None) and (
             stats is None or stats.dtype != torch.float32 or stats.shape != (p.rows, 2) or stats.device != dev
             or not stats.is_contiguous()):
@@ -203,11 +214,11 @@ def _bwd(p, dz, dn, r, y, stats, w_post, gate, w_pre, want, given, workspace, st
         def vector(wanted):
             return torch.empty(p.c, dtype=p._tdw, device=dev) if wanted else None
 
-        dr, st.dr = _rows(p, given.get("dr"), "dr", dev) if want_r else (None, 0)
-        dy, st.dy = _rows(p, given.get("dy"), "dy", dev) if want_y else (None, 0)
+        dr = _rows(p, given.get("dr"), "dr", dev, st) if want_r else None
+        dy = _rows(p, given.get("dy"), "dy", dev, st) if want_y else None
         dgate = None
         if want_gate and row_gate:
-            dgate, st.dgate = _rows(p, given.get("dgate"), "dgate", dev)
+            dgate = _rows(p, given.get("dgate"), "dgate", dev, st)
         elif want_gate:
             dgate = vector(True)
         dw_post, dw_pre = vector(want_post), vector(want_pre)
@@ -222,7 +233,7 @@ def _bwd(p, dz, dn, r, y, stats, w_post, gate, w_pre, want, given, workspace, st
             ws_bytes = workspace.numel() * workspace.element_size()
         grads = BlockGrads(_ptr(dr), _ptr(dy), _ptr(dw_post), _ptr(dgate), _ptr(dw_pre))
         _check(_lib.cbd_block_bwd(p._h, _ptr(dz), _ptr(dn), r.data_ptr(), _ptr(y), _ptr(stats), ctypes.byref(params),
-                                  ctypes.byref(grads), ctypes.byref(st), _ptr(workspace), ws_bytes,
+                                  ctypes.byref(grads), _struct(st), _ptr(workspace), ws_bytes,
                                   _handle(stream, dev)), "cbd_block_bwd")
     return dr, dy, dw_post, dgate, dw_pre
 
@@ -233,7 +244,7 @@ def block_bwd(p: BlockPlan, dz, dn, r, y=None, stats=None, w_post=None, gate=Non
     zeros); None for parts that are not there or that output_mask leaves out.
     dr, dy and a row gate's dgate are allocated unless given; dr may be dz, and
     dy dn.  The vectors' gradients have the plan's dw_dtype."""
-    if any(_records(t, None) for t in (dz, dn, r, y, w_post, gate, w_pre)):
+    if _any_records((dz, dn, r, y, w_post, gate, w_pre)):
         raise ValueError("block_bwd is not recorded by autograd and an operand requires gradients (or has a "
                          "tangent); call under torch.no_grad()")
     if dgate is not None and (gate is None or gate.dim() == 1):

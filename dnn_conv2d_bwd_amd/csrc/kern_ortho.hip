@@ -50,6 +50,13 @@ __device__ inline void wait_all() {
   __builtin_amdgcn_s_waitcnt(0 | (7 << 4));  // vmcnt 0, expcnt 7, lgkmcnt 0
   asm volatile("" ::: "memory");
 }
+// And one where up to n loads may be on their way.
+template <int n>
+__device__ inline void wait_loads() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14));
+  asm volatile("" ::: "memory");
+}
 __device__ inline void barrier() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
@@ -62,7 +69,10 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void ortho_product_kernel
   constexpr int BYTES = T * 128;      // of an operand's stage
   constexpr int N = BYTES / 4096;     // 1 KiB blocks of it that a wave fills
   constexpr bool SYM = STAGE == ORTHO_SQUARE || STAGE == ORTHO_POLY;
-  __shared__ __attribute__((aligned(1024))) char smem[4 * BYTES];
+  // Stages.  Tiles of 64 are for small products, where a run's 6 matrix
+  // instructions a wave take a fraction of a load's way: four runs are in flight.
+  constexpr int NS = MB == 1 ? 5 : 2;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * NS * BYTES];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave & 1, wn = wave >> 1;
 
@@ -153,44 +163,80 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void ortho_product_kernel
   constexpr std::integral_constant<int, N> all{};
   auto nothing = [](int) {};
 
-  f16x8 ph0[MB], ph1[MB], pl[MB], qh0[MB], qh1[MB], ql[MB];
-  // Run 0 and the first operand's run 1.
+  if constexpr (NS > 2) {
+    acc[0][0] = f32x16{};
+    auto load = [&](int k, int s) INLINE {
 #pragma unroll
-  for (int i = 0; i < N; i++) load_p(0, 0, i);
+      for (int i = 0; i < N; i++) {
+        load_p(k, s, i);
+        load_q(k, s, i);
+      }
+    };
 #pragma unroll
-  for (int i = 0; i < N; i++) load_q(0, 0, i);
-  wait_all();
-  barrier();
+    for (int k = 0; k < NS - 1; k++) load(k, k);
+    int s = 0;
+#pragma unroll 1
+    for (int k = 0; k < a.runs; k++) {
+      // Run k has landed, those after it are on their way; and everyone is done
+      // with the stage of run k - 1, which run k + NS - 1 goes to.
+      wait_loads<(NS - 2) * 2 * N>();
+      barrier();
+      load(k + NS - 1, s == 0 ? NS - 1 : s - 1);
+      const char* const st = smem + 2 * s * BYTES;
+      f16x8 p[4], q[4];
 #pragma unroll
-  for (int i = 0; i < N; i++) load_p(1, 1, i);
+      for (int c = 0; c < 4; c++) {
+        p[c] = *(const f16x8*)(st + at_p[c]);
+        q[c] = *(const f16x8*)(st + BYTES + at_q[c]);
+      }
 #pragma unroll
-  for (int b = 0; b < MB; b++) {
-    ph0[b] = read_p(0, 0, 0, b);
-    qh0[b] = read_q(0, 0, 0, b);
-  }
-  // Run k in stage S, whose first hi fragments are in registers.  The other
-  // stage gets the second operand's run k + 1 here, and this one, once every
-  // wave has read it, the first operand's run k + 2.
-  auto run = [&](int k, auto sc, auto firstc) INLINE {
-    constexpr int S = decltype(sc)::value;
-    part(firstc, ph0, qh0, two,
-         [&](int r) { r < MB ? (void)(ql[r] = read_q(S, 0, 1, r)) : (void)(pl[r - MB] = read_p(S, 0, 1, r - MB)); }, all,
-         [&](int i) { load_q(k + 1, 1 - S, i); });
-    part(std::false_type(), ph0, ql, one, [&](int r) { ph1[r] = read_p(S, 1, 0, r); }, none, nothing);
-    part(std::false_type(), pl, qh0, one, [&](int r) { qh1[r] = read_q(S, 1, 0, r); }, none, nothing);
-    part(std::false_type(), ph1, qh1, two,
-         [&](int r) { r < MB ? (void)(ql[r] = read_q(S, 1, 1, r)) : (void)(pl[r - MB] = read_p(S, 1, 1, r - MB)); }, none,
-         nothing);
+      for (int ks = 0; ks < 2; ks++) {
+        acc[0][0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(p[ks], q[ks], acc[0][0], 0, 0, 0);
+        acc[0][0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(p[ks], q[2 + ks], acc[0][0], 0, 0, 0);
+        acc[0][0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(p[2 + ks], q[ks], acc[0][0], 0, 0, 0);
+      }
+      s = s == NS - 1 ? 0 : s + 1;
+    }
+  } else {
+    f16x8 ph0[MB], ph1[MB], pl[MB], qh0[MB], qh1[MB], ql[MB];
+    // Run 0 and the first operand's run 1.
+#pragma unroll
+    for (int i = 0; i < N; i++) load_p(0, 0, i);
+#pragma unroll
+    for (int i = 0; i < N; i++) load_q(0, 0, i);
     wait_all();
     barrier();
-    part(std::false_type(), ph1, ql, one, [&](int r) { ph0[r] = read_p(1 - S, 0, 0, r); }, all, [&](int i) { load_p(k + 2, S, i); });
-    part(std::false_type(), pl, qh1, one, [&](int r) { qh0[r] = read_q(1 - S, 0, 0, r); }, none, nothing);
-  };
-  run(0, std::integral_constant<int, 0>(), std::true_type());
+#pragma unroll
+    for (int i = 0; i < N; i++) load_p(1, 1, i);
+#pragma unroll
+    for (int b = 0; b < MB; b++) {
+      ph0[b] = read_p(0, 0, 0, b);
+      qh0[b] = read_q(0, 0, 0, b);
+    }
+    // Run k in stage S, whose first hi fragments are in registers.  The other
+    // stage gets the second operand's run k + 1 here, and this one, once every
+    // wave has read it, the first operand's run k + 2.
+    auto run = [&](int k, auto sc, auto firstc) INLINE {
+      constexpr int S = decltype(sc)::value;
+      part(firstc, ph0, qh0, two,
+           [&](int r) { r < MB ? (void)(ql[r] = read_q(S, 0, 1, r)) : (void)(pl[r - MB] = read_p(S, 0, 1, r - MB)); }, all,
+           [&](int i) { load_q(k + 1, 1 - S, i); });
+      part(std::false_type(), ph0, ql, one, [&](int r) { ph1[r] = read_p(S, 1, 0, r); }, none, nothing);
+      part(std::false_type(), pl, qh0, one, [&](int r) { qh1[r] = read_q(S, 1, 0, r); }, none, nothing);
+      part(std::false_type(), ph1, qh1, two,
+           [&](int r) { r < MB ? (void)(ql[r] = read_q(S, 1, 1, r)) : (void)(pl[r - MB] = read_p(S, 1, 1, r - MB)); }, none,
+           nothing);
+      wait_all();
+      barrier();
+      part(std::false_type(), ph1, ql, one, [&](int r) { ph0[r] = read_p(1 - S, 0, 0, r); }, all, [&](int i) { load_p(k + 2, S, i); });
+      part(std::false_type(), pl, qh1, one, [&](int r) { qh0[r] = read_q(1 - S, 0, 0, r); }, none, nothing);
+    };
+    run(0, std::integral_constant<int, 0>(), std::true_type());
 #pragma unroll 1
-  for (int k = 1; k < a.runs; k += 2) {
-    run(k, std::integral_constant<int, 1>(), std::false_type());
-    if (k + 1 < a.runs) run(k + 1, std::integral_constant<int, 0>(), std::false_type());
+    for (int k = 1; k < a.runs; k += 2) {
+      run(k, std::integral_constant<int, 1>(), std::false_type());
+      if (k + 1 < a.runs) run(k + 1, std::integral_constant<int, 0>(), std::false_type());
+    }
   }
   // The last loads (zeros) have landed, and everyone has read the stages.
   wait_all();
@@ -335,6 +381,14 @@ __global__ __launch_bounds__(THREADS) void ortho_split_kernel(const OrthoSplit a
   __shared__ uint32_t tile[64][65];
   const int64_t mat = blockIdx.z;
   const int row0 = blockIdx.y * 64, col0 = blockIdx.x * 64, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 16; i++) {
+    const int row = 4 * i + wave;
+    v[i] = row0 + row < a.rows && col0 + lane < a.cols
+               ? value<T>(a.in, mat * a.in_mat + (int64_t)(row0 + row) * a.in_row + col0 + lane)
+               : 0.f;
+  }
   // Every wave adds the parts in the same order.
   double s = 0.0;
 #pragma unroll
@@ -342,18 +396,12 @@ __global__ __launch_bounds__(THREADS) void ortho_split_kernel(const OrthoSplit a
 #pragma unroll
   for (int m = 32; m > 0; m >>= 1) s += __shfl_xor(s, m, 64);
   const double f = a.up / (__builtin_sqrt(s) + a.eps);
-#pragma unroll 4
-  for (int i = 0; i < 16; i++) {
-    const int row = 4 * i + wave;
-    float v = 0.f;
-    if (row0 + row < a.rows && col0 + lane < a.cols)
-      v = (float)((double)value<T>(a.in, mat * a.in_mat + (int64_t)(row0 + row) * a.in_row + col0 + lane) * f);
-    tile[row][lane] = split(v);
-  }
+#pragma unroll
+  for (int i = 0; i < 16; i++) tile[4 * i + wave][lane] = split((float)((double)v[i] * f));
   __syncthreads();
   // Rows of two runs: lane j takes halves 2 j and 2 j + 1 of a row's 128.
   const int run = lane >> 5, e = 2 * (lane & 15), lo = (lane >> 4) & 1;
-#pragma unroll 4
+#pragma unroll
   for (int i = 0; i < 16; i++) {
     const int row = 4 * i + wave;
     const uint32_t x = tile[row][32 * run + e], y = tile[row][32 * run + e + 1];

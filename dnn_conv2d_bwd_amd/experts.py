@@ -254,6 +254,17 @@ def _records(a, b):
         isinstance(t, torch.Tensor) and forward.unpack_dual(t).tangent is not None for t in (a, b))
 
 
+def _any_records(operands):
+    """_records of any number of operands (None: left out)."""
+    import torch
+
+    if torch.is_grad_enabled():
+        for t in operands:
+            if t is not None and getattr(t, "requires_grad", False):
+                return True
+    return torch.autograd.forward_ad._current_level >= 0 and any(_records(t, None) for t in operands)
+
+
 @functools.lru_cache(None)
 def _recorder():
     import torch

@@ -22,7 +22,7 @@ import ctypes
 import functools
 
 from . import _check, _lib
-from .experts import (_DENSE, ExpertInfo, ExpertPlan, _cached, _ends, _handle, _on, _records, _strided, _w_layout,
+from .experts import (_DENSE, ExpertInfo, ExpertPlan, _any_records, _cached, _ends, _handle, _on, _strided, _w_layout,
                       _written, expert_bwd_data, expert_bwd_weight, expert_forward)
 
 ACT_SILU, ACT_GELU, ACT_RELU = 0, 1, 2
@@ -62,7 +62,7 @@ def _hidden(p):
 
 
 def _refuse(name, *operands):
-    if any(_records(t, None) for t in operands):
+    if _any_records(operands):
         raise ValueError(f"{name} is not recorded by autograd and an operand requires gradients (or has a "
                          "tangent); use expert_ffn or call under torch.no_grad()")
 
