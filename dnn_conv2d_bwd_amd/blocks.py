@@ -211,19 +211,19 @@ def _bwd(p, dz, dn, r, y, stats, w_post, gate, w_pre, want, given, workspace, st
         bool(w) and t is not None for w, t in zip(want, (r, y, w_post, gate, w_pre)))
     row_gate = params.gate_kind == GATE_ROW
     with _on(dev, stream):
-        def vector(wanted):
-            return torch.empty(p.c, dtype=p._tdw, device=dev) if wanted else None
-
         dr = _rows(p, given.get("dr"), "dr", dev, st) if want_r else None
         dy = _rows(p, given.get("dy"), "dy", dev, st) if want_y else None
-        dgate = None
+        dgate = dw_post = dw_pre = None
         if want_gate and row_gate:
-            dgate = _rows(p, given.get("dgate"), "dgate", dev, st)
-        elif want_gate:
-            dgate = vector(True)
-        dw_post, dw_pre = vector(want_post), vector(want_pre)
+            dgate, want_gate = _rows(p, given.get("dgate"), "dgate", dev, st), False
+        vectors = want_post + want_gate + want_pre
+        if vectors:
+            new = iter(torch.empty((vectors, p.c), dtype=p._tdw, device=dev).unbind(0))
+            dw_post = next(new) if want_post else None
+            dgate = next(new) if want_gate else dgate
+            dw_pre = next(new) if want_pre else None
         ws_bytes = 0
-        if dw_post is not None or dw_pre is not None or (dgate is not None and not row_gate):
+        if vectors:
             if workspace is None:
                 workspace = torch.empty(p._ws, dtype=torch.uint8, device=dev)
             elif not workspace.is_contiguous() or workspace.device != dev:

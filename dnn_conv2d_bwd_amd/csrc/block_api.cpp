@@ -32,11 +32,14 @@ cbd_status make_plan(const cbd_block_problem* q, cbd_block_plan_t** out) {
   if (!p) return fail(CBD_ERR_NO_MEMORY, "out of host memory");
   p->prob = *q;
   p->shape = cbd::block_shape(q->c, esize(q->dtype));
-  const int threads = p->shape.lanes == 64 ? 256 : p->shape.lanes, per = cbd::block_rows(p->shape);
+  const int threads = cbd::block_threads(p->shape), per = threads / p->shape.lanes;
   const int64_t groups = (q->rows + per - 1) / per;
   // Workgroups that stay: as many as the compute units hold at once.
   p->grid_fwd = std::min<int64_t>(groups, 256 * (2048 / threads));
   p->grid_bwd = std::min<int64_t>(groups, 256 * (1024 / threads));
+  // A few rows (groups of them) by one workgroup, which then needs no second
+  // launch to join its sums with others'.
+  if (groups <= 4) p->grid_bwd = 1;
   *out = p;
   cbd::set_error("");
   return CBD_OK;
@@ -204,6 +207,17 @@ cbd_status bwd(const cbd_block_plan_t* plan, const void* dz, const void* dn, con
   const cbd_status over = check(t, 15);
   if (over != CBD_OK) return over;
   if (!vectors && (!q.rows || (!g.dr && !g.dy && !dgate_row))) return done(0);
+  cbd::BlockFinish f = {};
+  f.partial = (const float*)ws;
+  f.gate = row_gate ? nullptr : o.p.gate;
+  f.w_post = o.p.w_post;
+  f.dw_post = g.dw_post;
+  f.dgate = row_gate ? nullptr : g.dgate;
+  f.dw_pre = g.dw_pre;
+  f.n = q.rows ? (int32_t)plan->grid_bwd : 0;
+  f.c = (int32_t)q.c;
+  f.dtype = q.dtype;
+  f.dw_dtype = q.dw_dtype;
   int err = 0;
   if (q.rows) {
     cbd::BlockArgs a = arguments(q, o, r, y);
@@ -214,22 +228,10 @@ cbd_status bwd(const cbd_block_plan_t* plan, const void* dz, const void* dn, con
     a.dgate = dgate_row;
     a.stats = const_cast<float*>(stats);
     a.partial = vectors ? (float*)ws : nullptr;
+    a.finish = f;
     err = cbd::launch_block_bwd(a, plan->shape, q.dtype, plan->grid_bwd, stream);
   }
-  if (!err && vectors) {
-    cbd::BlockFinish f = {};
-    f.partial = (const float*)ws;
-    f.gate = row_gate ? nullptr : o.p.gate;
-    f.w_post = o.p.w_post;
-    f.dw_post = g.dw_post;
-    f.dgate = row_gate ? nullptr : g.dgate;
-    f.dw_pre = g.dw_pre;
-    f.n = q.rows ? (int32_t)plan->grid_bwd : 0;
-    f.c = (int32_t)q.c;
-    f.dtype = q.dtype;
-    f.dw_dtype = q.dw_dtype;
-    err = cbd::launch_block_finish(f, stream);
-  }
+  if (!err && vectors && f.n != 1) err = cbd::launch_block_finish(f, stream);
   return done(err);
 }
 

@@ -7,10 +7,18 @@
 namespace cbd {
 
 // How a row of c elements is dealt out: `lanes` threads of up to `chunks`
-// 16-byte chunks each.  64 lanes: a wave a row, 4 rows a workgroup; otherwise
-// a workgroup a row.
+// 16-byte chunks each.  Up to 64 lanes: several rows in a workgroup of 256
+// threads; otherwise a workgroup a row.
 struct BlockShape {
   int32_t lanes, chunks;
+};
+
+// Joins bwd's partial sums: sums[0] = sum dn * zn, sums[1] = sum scale * dz' * yn (* gate, of rows).
+struct BlockFinish {
+  const float* partial;
+  const void *gate, *w_post;         // vectors
+  void *dw_post, *dgate, *dw_pre;    // NULL: not wanted
+  int32_t n, c, dtype, dw_dtype;     // n: workgroups
 };
 
 struct BlockArgs {
@@ -25,14 +33,7 @@ struct BlockArgs {
   int32_t c;
   int32_t gate_rows;  // the gate has rows
   float eps, scale;
-};
-
-// Joins bwd's partial sums: sums[0] = sum dn * zn, sums[1] = sum scale * dz' * yn (* gate, of rows).
-struct BlockFinish {
-  const float* partial;
-  const void *gate, *w_post;         // vectors
-  void *dw_post, *dgate, *dw_pre;    // NULL: not wanted
-  int32_t n, c, dtype, dw_dtype;
+  BlockFinish finish;  // bwd by one workgroup: what it does itself in the end
 };
 
 int launch_block_forward(const BlockArgs& a, BlockShape s, int dtype, int64_t grid, void* stream);
@@ -43,11 +44,11 @@ int launch_block_finish(const BlockFinish& a, void* stream);
 constexpr int kBlockMaxC = 16384;
 inline BlockShape block_shape(int64_t c, int es) {
   const int64_t chunks = (c * es + 15) / 16;
-  for (int lanes = 64; lanes <= 1024; lanes *= 2)
+  for (int lanes = 8; lanes <= 1024; lanes *= 2)
     if (chunks <= lanes) return {lanes, 1};
   return {1024, chunks <= 2048 ? 2 : 4};
 }
-inline int block_rows(BlockShape s) { return s.lanes == 64 ? 4 : 1; }
+inline int block_threads(BlockShape s) { return s.lanes <= 64 ? 256 : s.lanes; }
 
 }  // namespace cbd
 

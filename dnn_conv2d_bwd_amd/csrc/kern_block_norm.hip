@@ -12,10 +12,10 @@
 // gradients need sum dn * zn and sum scale * dz' * yn over the rows: w_post and
 // a gate vector are factors of the second that a column shares.
 //
-// A row stays in registers from its one load to its stores; a workgroup (or,
-// up to 1024 bf16 a row, a wave) takes rows i, i + grid, ..., loads the next one
-// before it joins the sums of this one, and keeps its columns' sums in
-// registers to the end.  z is rounded where it is stored, not where n is made
+// A row stays in registers from its one load to its stores, 16 bytes a thread: a
+// workgroup (or, up to 64 threads a row, a part of one) takes rows i, i + grid,
+// ..., loads the next one before it joins the sums of this one, and keeps its
+// columns' sums in registers to the end.  z is rounded where it is stored, not where n is made
 // of it.
 //
 // Bound: HBM.
@@ -85,17 +85,22 @@ struct Chunk {
   }
 };
 
-// Sum over a wave, for everyone: shifts within rows of 16 lanes, the rows' last
-// lanes into the next ones, and the last lane's value.
-__device__ inline float wave_sum(float v) {
-  auto plus = [&](int moved) { v += __int_as_float(moved); };
-  plus(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x111, 0xf, 0xf, false));  // row_shr:1
-  plus(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x112, 0xf, 0xf, false));
-  plus(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x114, 0xf, 0xf, false));
-  plus(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x118, 0xf, 0xf, false));
-  plus(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x142, 0xa, 0xf, false));  // row_bcast:15
-  plus(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x143, 0xc, 0xf, false));  // row_bcast:31
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+// v and its partner's, LANES / 2 lanes away or mirrored: after all steps every
+// lane of a group of LANES (a power of two up to 64) has the group's sum, each
+// with the same bits, since the two of a step add the same two values.
+template <int CTRL>
+__device__ inline float plus_dpp(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+template <int LANES>
+__device__ inline float group_sum(float v) {
+  if constexpr (LANES >= 2) v = plus_dpp<0xb1>(v);    // quad_perm 1 0 3 2
+  if constexpr (LANES >= 4) v = plus_dpp<0x4e>(v);    // quad_perm 2 3 0 1
+  if constexpr (LANES >= 8) v = plus_dpp<0x141>(v);   // row_half_mirror
+  if constexpr (LANES >= 16) v = plus_dpp<0x140>(v);  // row_mirror
+  if constexpr (LANES >= 32) v += __shfl_xor(v, 16, 64);
+  if constexpr (LANES >= 64) v += __shfl_xor(v, 32, 64);
+  return v;
 }
 
 // Sums over a row's threads, in a fixed order, for everyone.  Two buffers, so
@@ -103,33 +108,44 @@ __device__ inline float wave_sum(float v) {
 // barrier, before which everyone has read it.
 template <int LANES, int S>
 struct RowSum {
-  float (*part)[LANES / 64][S];
+  static constexpr int W = LANES > 64 ? LANES / 64 : 1;
+  float (*part)[S][W];
   int at = 0;
   __device__ inline void operator()(float (&s)[S]) {
 #pragma unroll
-    for (int i = 0; i < S; i++) s[i] = wave_sum(s[i]);
-    if constexpr (LANES > 64) {
+    for (int i = 0; i < S; i++) s[i] = group_sum<LANES < 64 ? LANES : 64>(s[i]);
+    if constexpr (W > 1) {
       if ((threadIdx.x & 63) == 0)
 #pragma unroll
-        for (int i = 0; i < S; i++) part[at][threadIdx.x >> 6][i] = s[i];
+        for (int i = 0; i < S; i++) part[at][i][threadIdx.x >> 6] = s[i];
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < S; i++) s[i] = 0.f;
-#pragma unroll
-      for (int w = 0; w < LANES / 64; w++)
-#pragma unroll
-        for (int i = 0; i < S; i++) s[i] += part[at][w][i];
+      for (int i = 0; i < S; i++) s[i] = group_sum<W>(part[at][i][threadIdx.x & (W - 1)]);
       at ^= 1;
     }
   }
 };
 
+// Opaque to the compiler, which would keep vectors widened to f32 through the
+// loop over rows: twice the registers.
+template <typename T, int CH>
+__device__ inline void as_loaded(Chunk<T> (&v)[CH]) {
+#pragma unroll
+  for (int i = 0; i < CH; i++)
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      uint32_t w = v[i].v[j];
+      asm volatile("" : "+v"(w));
+      v[i].v[j] = w;
+    }
+}
+
 template <int LANES>
-constexpr int kThreads = LANES == 64 ? 256 : LANES;
+constexpr int kThreads = LANES <= 64 ? 256 : LANES;
 // Waves a SIMD: 128 registers (1024 threads have no more) where a thread has
-// one chunk.
-template <int CH>
-constexpr int kWaves = CH == 1 ? 4 : 1;
+// one chunk; with rows inside a wave, whose addresses take registers, 168.
+template <int LANES, int CH>
+constexpr int kWaves = CH > 1 ? 1 : LANES < 64 ? 3 : 4;
 // The next row is loaded ahead; with more chunks a thread has no room for it.
 template <int CH>
 constexpr bool kAhead = CH == 1;
@@ -141,11 +157,12 @@ struct Rows {
   int lane, n[CH];  // elements of each chunk that are inside (negative: none)
   int64_t row, step;
   __device__ inline explicit Rows(const BlockArgs& a) {
-    lane = LANES == 64 ? threadIdx.x & 63 : threadIdx.x;
+    lane = threadIdx.x & (LANES - 1);
 #pragma unroll
     for (int i = 0; i < CH; i++) n[i] = a.c - N * (lane + LANES * i);
-    const int sub = LANES == 64 ? __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) : 0;
-    constexpr int per = LANES == 64 ? 4 : 1;
+    constexpr int per = kThreads<LANES> / LANES;
+    int sub = threadIdx.x / LANES;
+    if (LANES >= 64) sub = __builtin_amdgcn_readfirstlane(sub);
     row = (int64_t)blockIdx.x * per + sub;
     step = (int64_t)gridDim.x * per;
   }
@@ -163,6 +180,16 @@ struct Rows {
 #pragma unroll
     for (int i = 0; i < CH; i++) v[i].zero();
   }
+  // A vector, or ones in its place: factors that change nothing.
+  __device__ inline void vector(Chunk<T> (&v)[CH], const void* p) const {
+    constexpr uint32_t one = sizeof(T) == 4 ? 0x3f800000u : 0x3f803f80u;
+    if (p) {
+      load(v, p, 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < CH; i++) v[i].v = u32x4{one, one, one, one};
+    }
+  }
 };
 
 __device__ inline float inverse_rms(float squares, const BlockArgs& a) {
@@ -170,17 +197,17 @@ __device__ inline float inverse_rms(float squares, const BlockArgs& a) {
 }
 
 template <typename T, int LANES, int CH>
-__global__ __launch_bounds__(kThreads<LANES>, kWaves<CH>) void block_forward_kernel(const BlockArgs a) {
+__global__ __launch_bounds__(kThreads<LANES>, (kWaves<LANES, CH>)) void block_forward_kernel(const BlockArgs a) {
   constexpr int N = Chunk<T>::N;
-  __shared__ float part[2][LANES / 64][1];
+  __shared__ float part[2][1][RowSum<LANES, 1>::W];
   RowSum<LANES, 1> sum{part};
   Rows<T, LANES, CH> rows(a);
   Chunk<T> wq[CH], gq[CH], wp[CH];  // w_post, gate, w_pre
-  Rows<T, LANES, CH>::zero(gq);
-  if (a.w_post) rows.load(wq, a.w_post, 0);
-  if (a.gate && !a.gate_rows) rows.load(gq, a.gate, 0);
-  if (a.w_pre) rows.load(wp, a.w_pre, 0);
+  rows.vector(wq, a.w_post);
+  rows.vector(gq, a.gate_rows ? nullptr : a.gate);
+  rows.vector(wp, a.w_pre);
   Chunk<T> r[CH], y[CH], g[CH];
+  Rows<T, LANES, CH>::zero(y);
   auto fetch = [&](int64_t row) {
     rows.load(r, a.r, row * a.ldr);
     if (a.y) rows.load(y, a.y, row * a.ldy);
@@ -189,13 +216,16 @@ __global__ __launch_bounds__(kThreads<LANES>, kWaves<CH>) void block_forward_ker
   if (kAhead<CH> && rows.row < a.rows) fetch(rows.row);
   for (int64_t row = rows.row; row < a.rows; row += rows.step) {
     if (!kAhead<CH>) fetch(row);
+    as_loaded(wq);
+    as_loaded(gq);
+    as_loaded(wp);
     float z[CH][N], v[CH][N];
 #pragma unroll
     for (int i = 0; i < CH; i++)
 #pragma unroll
       for (int j = 0; j < N; j++) {
         z[i][j] = r[i].get(j);
-        v[i][j] = a.y ? y[i].get(j) : 0.f;
+        v[i][j] = y[i].get(j);
       }
     float s[1] = {0.f};
     // What the gate, the weight and the scale make of y.
@@ -217,10 +247,7 @@ __global__ __launch_bounds__(kThreads<LANES>, kWaves<CH>) void block_forward_ker
     for (int i = 0; i < CH; i++)
 #pragma unroll
       for (int j = 0; j < N; j++) {
-        float t = v[i][j];
-        if (a.w_post) t = t * ry * wq[i].get(j);
-        if (a.gate) t *= gr[i].get(j);
-        if (a.y) z[i][j] = __builtin_fmaf(a.scale, t, z[i][j]);
+        z[i][j] = __builtin_fmaf(a.scale, v[i][j] * ry * wq[i].get(j) * gr[i].get(j), z[i][j]);
         s[0] = __builtin_fmaf(z[i][j], z[i][j], s[0]);
       }
     if (a.z) {
@@ -249,17 +276,36 @@ __global__ __launch_bounds__(kThreads<LANES>, kWaves<CH>) void block_forward_ker
   }
 }
 
+// The gradients that column col's sum (`which` of the two) makes.
+__device__ inline void finish_column(const BlockFinish& a, int which, int col, double s) {
+  auto vector = [&](const void* v) {
+    return !v ? 1.0 : (double)(a.dtype == CBD_F32 ? ((const float*)v)[col] : dev::bf16_to_f32(((const uint16_t*)v)[col]));
+  };
+  auto put = [&](void* o, double v) {
+    if (!o) return;
+    if (a.dw_dtype == CBD_F32)
+      ((float*)o)[col] = (float)v;
+    else
+      ((uint16_t*)o)[col] = (uint16_t)dev::bf16_rne((float)v);
+  };
+  if (which == 0) {
+    put(a.dw_pre, s);
+  } else {
+    put(a.dw_post, s * vector(a.gate));
+    put(a.dgate, s * vector(a.w_post));
+  }
+}
+
 template <typename T, int LANES, int CH>
-__global__ __launch_bounds__(kThreads<LANES>, kWaves<CH>) void block_bwd_kernel(const BlockArgs a) {
+__global__ __launch_bounds__(kThreads<LANES>, (kWaves<LANES, CH>)) void block_bwd_kernel(const BlockArgs a) {
   constexpr int N = Chunk<T>::N;
-  __shared__ float part[2][LANES / 64][3];
+  __shared__ float part[2][3][RowSum<LANES, 3>::W];
   RowSum<LANES, 3> sum{part};
   Rows<T, LANES, CH> rows(a);
   Chunk<T> wq[CH], gq[CH], wp[CH];
-  Rows<T, LANES, CH>::zero(gq);
-  if (a.w_post) rows.load(wq, a.w_post, 0);
-  if (a.gate && !a.gate_rows) rows.load(gq, a.gate, 0);
-  if (a.w_pre) rows.load(wp, a.w_pre, 0);
+  rows.vector(wq, a.w_post);
+  rows.vector(gq, a.gate_rows ? nullptr : a.gate);
+  rows.vector(wp, a.w_pre);
   float pre[CH][N], post[CH][N];  // the columns' sums
 #pragma unroll
   for (int i = 0; i < CH; i++)
@@ -284,6 +330,9 @@ __global__ __launch_bounds__(kThreads<LANES>, kWaves<CH>) void block_bwd_kernel(
   for (int64_t row = rows.row; row < a.rows; row += rows.step) {
     if (!kAhead<CH>) fetch(row);
     const float ry = ry1, rz = rz1;
+    as_loaded(wq);
+    as_loaded(gq);
+    as_loaded(wp);
     float zn[CH][N], yn[CH][N], e[CH][N];
     float s[3] = {0.f, 0.f, 0.f};
     Chunk<T> gr[CH];
@@ -295,12 +344,9 @@ __global__ __launch_bounds__(kThreads<LANES>, kWaves<CH>) void block_bwd_kernel(
       for (int j = 0; j < N; j++) {
         const float d = dn[i].get(j);
         yn[i][j] = y[i].get(j) * ry;
-        float c = a.scale;
-        if (a.w_post) c *= wq[i].get(j);
-        if (a.gate) c *= gr[i].get(j);
-        const float cy = c * yn[i][j];
+        const float cy = a.scale * wq[i].get(j) * gr[i].get(j) * yn[i][j];
         zn[i][j] = (r[i].get(j) + cy) * rz;
-        const float v = a.w_pre ? d * wp[i].get(j) : 0.f;
+        const float v = d * wp[i].get(j);
         e[i][j] = __builtin_fmaf(rz, v, dz[i].get(j));
         pre[i][j] = __builtin_fmaf(d, zn[i][j], pre[i][j]);
         s[0] = __builtin_fmaf(v, zn[i][j], s[0]);
@@ -317,12 +363,10 @@ __global__ __launch_bounds__(kThreads<LANES>, kWaves<CH>) void block_bwd_kernel(
       float fr[N], fy[N], fg[N];
 #pragma unroll
       for (int j = 0; j < N; j++) {
-        fr[j] = __builtin_fmaf(-along, zn[i][j], e[i][j]);
-        const float da = a.scale * fr[j];
-        const float gate = a.gate ? gr[i].get(j) : 1.f;
-        const float w = a.w_post ? wq[i].get(j) : 1.f;
+        // (Where there is no norm, nothing is taken off: not 0 times infinity.)
+        fr[j] = a.w_pre ? __builtin_fmaf(-along, zn[i][j], e[i][j]) : e[i][j];
+        const float da = a.scale * fr[j], dg = da * gr[i].get(j), w = wq[i].get(j);
         fg[j] = da * yn[i][j] * w;
-        const float dg = da * gate;
         post[i][j] = __builtin_fmaf(a.gate_rows ? dg : da, yn[i][j], post[i][j]);
         fy[j] = a.w_post ? ry * __builtin_fmaf(-back, yn[i][j], dg * w) : dg;
       }
@@ -334,32 +378,34 @@ __global__ __launch_bounds__(kThreads<LANES>, kWaves<CH>) void block_bwd_kernel(
     if (a.dy) rows.store(o_y, a.dy, row * a.lddy);
     if (a.dgate) rows.store(o_g, a.dgate, row * a.lddgate);
   }
+  const bool alone = gridDim.x == 1;  // no one to join
   if (!a.partial) return;
   float* const out = a.partial + (int64_t)blockIdx.x * 2 * a.c;
-  if constexpr (LANES == 64) {
-    // The four waves' sums, joined in their order.
-    __shared__ float join[2][3][CH * N][64];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    if (wave > 0) {
+  if constexpr (LANES <= 64) {
+    // The groups' sums, joined in their order.
+    constexpr int G = 256 / LANES, COLS = LANES * CH * N;
+    __shared__ float join[2][CH * N][256];
 #pragma unroll
-      for (int i = 0; i < CH; i++)
+    for (int i = 0; i < CH; i++)
 #pragma unroll
-        for (int j = 0; j < N; j++) {
-          join[0][wave - 1][i * N + j][lane] = pre[i][j];
-          join[1][wave - 1][i * N + j][lane] = post[i][j];
-        }
-    }
+      for (int j = 0; j < N; j++) {
+        join[0][i * N + j][threadIdx.x] = pre[i][j];
+        join[1][i * N + j][threadIdx.x] = post[i][j];
+      }
     __syncthreads();
-    if (wave > 0) return;
-#pragma unroll
-    for (int w = 0; w < 3; w++)
-#pragma unroll
-      for (int i = 0; i < CH; i++)
-#pragma unroll
-        for (int j = 0; j < N; j++) {
-          pre[i][j] += join[0][w][i * N + j][lane];
-          post[i][j] += join[1][w][i * N + j][lane];
-        }
+    for (int k = threadIdx.x; k < 2 * COLS; k += 256) {
+      const int which = k / COLS, col = k % COLS, i = col / (N * LANES), lane = col / N % LANES, j = col % N;
+      float s = 0.f;
+#pragma unroll 8
+      for (int g = 0; g < G; g++) s += join[which][i * N + j][g * LANES + lane];
+      if (col < a.c) {
+        if (alone)
+          finish_column(a.finish, which, col, s);
+        else
+          out[which * a.c + col] = s;
+      }
+    }
+    return;
   }
 #pragma unroll
   for (int i = 0; i < CH; i++) {
@@ -367,8 +413,13 @@ __global__ __launch_bounds__(kThreads<LANES>, kWaves<CH>) void block_bwd_kernel(
 #pragma unroll
     for (int j = 0; j < N; j++)
       if (at + j < a.c) {
-        out[at + j] = pre[i][j];
-        out[a.c + at + j] = post[i][j];
+        if (alone) {
+          finish_column(a.finish, 0, at + j, pre[i][j]);
+          finish_column(a.finish, 1, at + j, post[i][j]);
+        } else {
+          out[at + j] = pre[i][j];
+          out[a.c + at + j] = post[i][j];
+        }
       }
   }
 }
@@ -390,22 +441,7 @@ __global__ __launch_bounds__(FINISH) void block_finish_kernel(const BlockFinish 
   if (slice > 0 || col >= a.c) return;
 #pragma unroll
   for (int i = 1; i < FINISH / 64; i++) s += part[i][lane];
-  auto vector = [&](const void* v) {
-    return !v ? 1.0 : (double)(a.dtype == CBD_F32 ? ((const float*)v)[col] : dev::bf16_to_f32(((const uint16_t*)v)[col]));
-  };
-  auto put = [&](void* o, double v) {
-    if (!o) return;
-    if (a.dw_dtype == CBD_F32)
-      ((float*)o)[col] = (float)v;
-    else
-      ((uint16_t*)o)[col] = (uint16_t)dev::bf16_rne((float)v);
-  };
-  if (which == 0) {
-    put(a.dw_pre, s);
-  } else {
-    put(a.dw_post, s * vector(a.gate));
-    put(a.dgate, s * vector(a.w_post));
-  }
+  finish_column(a, which, col, s);
 }
 
 template <typename T, bool BWD>
@@ -413,6 +449,9 @@ const void* pick(BlockShape s) {
   constexpr int F = sizeof(T) / 2;
 #define CBD_BLOCK(L, C) \
   if (s.lanes == L && s.chunks == C) return BWD ? (const void*)&block_bwd_kernel<T, L, C> : (const void*)&block_forward_kernel<T, L, C>;
+  CBD_BLOCK(8, 1)
+  CBD_BLOCK(16, 1)
+  CBD_BLOCK(32, 1)
   CBD_BLOCK(64, 1)
   CBD_BLOCK(128, 1)
   CBD_BLOCK(256, 1)
@@ -430,7 +469,7 @@ template <bool BWD>
 int launch(const BlockArgs& a, BlockShape s, int dtype, int64_t grid, void* stream) {
   const void* k = dtype == CBD_F32 ? pick<float, BWD>(s) : pick<uint16_t, BWD>(s);
   void* args[] = {const_cast<BlockArgs*>(&a)};
-  return (int)hipLaunchKernel(k, dim3((unsigned)grid), dim3(s.lanes == 64 ? 256 : s.lanes), args, 0,
+  return (int)hipLaunchKernel(k, dim3((unsigned)grid), dim3(block_threads(s)), args, 0,
                               (hipStream_t)stream);
 }
 
