@@ -48,7 +48,7 @@ EXPORTS = ("cbd_plan", "cbd_plan_ex", "cbd_run", "cbd_run_ws", "cbd_run_noalloc"
            "cbd_expert_gated_forward", "cbd_expert_gated_bwd", "cbd_expert_gated_info",
            "cbd_block_plan", "cbd_block_plan_destroy", "cbd_block_workspace_size", "cbd_block_forward",
            "cbd_block_bwd",
-           "cbd_ortho_plan", "cbd_ortho_plan_destroy", "cbd_ortho_workspace_size", "cbd_orthogonalize",
+           "cbd_ortho_plan", "cbd_ortho_plan_destroy", "cbd_ortho_plan_info", "cbd_ortho_workspace_size", "cbd_orthogonalize",
            "cbd_grad_plan", "cbd_grad_plan_destroy", "cbd_grad_workspace_size", "cbd_grad_norm",
            "cbd_grad_clip")
 
@@ -353,4 +353,5 @@ from .blocks import (GATE_CHANNEL, GATE_NONE, GATE_ROW, BlockGrads, BlockParams,
 from .gated import (ACT_GELU, ACT_RELU, ACT_SILU, GatedStrides, expert_ffn, expert_gated_bwd,  # noqa: E402,F401
                     expert_gated_forward, expert_gated_info)
 from .grads import GradPlan, clip_grad_norm, clip_grads, grad_norm, grad_plan  # noqa: E402,F401
-from .updates import OrthoPlan, OrthoProblem, OrthoStrides, orthogonalize, orthogonalized, ortho_plan  # noqa: E402,F401
+from .updates import (OrthoInfo, OrthoPlan, OrthoProblem, OrthoStrides, orthogonalize, orthogonalized,  # noqa: E402,F401
+                      ortho_plan)

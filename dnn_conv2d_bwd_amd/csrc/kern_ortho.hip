@@ -50,11 +50,12 @@ __device__ inline void wait_all() {
   __builtin_amdgcn_s_waitcnt(0 | (7 << 4));  // vmcnt 0, expcnt 7, lgkmcnt 0
   asm volatile("" ::: "memory");
 }
-// And one where up to n loads may be on their way.
-template <int n>
+// And one where up to n loads may be on their way, and (LDS = 15) LDS accesses.
+template <int n, int LDS = 15>
 __device__ inline void wait_loads() {
+  static_assert(n < 64, "vmcnt has six bits");
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt((n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14));
+  __builtin_amdgcn_s_waitcnt((n & 15) | (7 << 4) | (LDS << 8) | ((n >> 4) << 14));
   asm volatile("" ::: "memory");
 }
 __device__ inline void barrier() {
@@ -63,15 +64,12 @@ __device__ inline void barrier() {
   asm volatile("" ::: "memory");
 }
 
-template <int MB, int STAGE>
-__global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void ortho_product_kernel(const OrthoArgs a) {
+template <int MB, int STAGE, int NS>
+__global__ __launch_bounds__(THREADS, MB == 4 || (MB == 2 && NS > 2) ? 1 : 2) void ortho_product_kernel(const OrthoArgs a) {
   constexpr int T = 64 * MB;
   constexpr int BYTES = T * 128;      // of an operand's stage
   constexpr int N = BYTES / 4096;     // 1 KiB blocks of it that a wave fills
   constexpr bool SYM = STAGE == ORTHO_SQUARE || STAGE == ORTHO_POLY;
-  // Stages.  Tiles of 64 are for small products, where a run's 6 matrix
-  // instructions a wave take a fraction of a load's way: four runs are in flight.
-  constexpr int NS = MB == 1 ? 5 : 2;
   __shared__ __attribute__((aligned(1024))) char smem[2 * NS * BYTES];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave & 1, wn = wave >> 1;
@@ -82,8 +80,25 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void ortho_product_kernel
   const int mat = __builtin_amdgcn_readfirstlane(t / per);
   int local = __builtin_amdgcn_readfirstlane(t - mat * per), mt, nt;
   if (SYM) {
-    for (nt = 0; local > nt; nt++) local -= nt + 1;  // column nt has nt + 1 tiles
-    mt = local;
+    // Groups of W columns; in each, row by row: neighbours, which one XCD has,
+    // share both operands.
+    const int W = gridDim.x <= 256 ? 4 : 8;
+    int c0 = 0, w = a.tiles_n < W ? a.tiles_n : W;
+    while (local >= c0 * w + w * (w + 1) / 2) {
+      local -= c0 * w + w * (w + 1) / 2;
+      c0 += w;
+      w = a.tiles_n - c0 < W ? a.tiles_n - c0 : W;
+    }
+    if (local < c0 * w) {
+      mt = local / w;
+      nt = c0 + local - mt * w;
+    } else {
+      local -= c0 * w;
+      int r = 0;
+      for (; local >= w - r; r++) local -= w - r;
+      mt = c0 + r;
+      nt = mt + local;
+    }
   } else {
     // Groups of 8 rows of tiles by all columns.
     const int g = local / (8 * a.tiles_n), in = local - g * 8 * a.tiles_n;
@@ -161,16 +176,27 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void ortho_product_kernel
     return *(const f16x8*)(smem + (2 * s + 1) * BYTES + at_q[2 * h + ks] + b * 4096);
   };
 
-  f32x16 acc[MB][MB];
+  // Sums of hi hi and, apart where registers allow it, of hi lo and lo hi: these
+  // are 2^-11 of the others, and so are their roundings then (3 steps of 9
+  // matrices of 512 x 768 are off by 1.15e-6 together, 0.73e-6 apart; an f32 library
+  // product's form by 0.85e-6).
+  constexpr bool APART = MB < 4;
+  f32x16 acc[MB][MB], low[APART ? MB : 1][APART ? MB : 1];
 
   // MFMAs on (x, y), with R reads and L loads spread between them.
   const f32x16 zero = {};
-  auto part = [&](auto firstc, const f16x8 (&x)[MB], const f16x8 (&y)[MB], auto rc, auto&& rd, auto lc, auto&& ld) INLINE {
+  // first: the sums begin.  hi: these are hi hi.
+  auto multiply = [&](bool first, bool hi, int m, int n, const f16x8& x, const f16x8& y) INLINE {
+    f32x16& sum = APART && !hi ? low[APART ? m : 0][APART ? n : 0] : acc[m][n];
+    sum = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, y, first ? zero : sum, 0, 0, 0);
+  };
+  auto part = [&](auto firstc, auto hic, const f16x8 (&x)[MB], const f16x8 (&y)[MB], auto rc, auto&& rd, auto lc,
+                  auto&& ld) INLINE {
     constexpr int Q = MB * MB, R = decltype(rc)::value, L = decltype(lc)::value;
 #pragma unroll
     for (int i = 0; i < Q; i++) {
       const int n = i / MB, m = (n & 1) ? MB - 1 - i % MB : i % MB;
-      acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[m], y[n], firstc.value ? zero : acc[m][n], 0, 0, 0);
+      multiply(firstc.value, hic.value, m, n, x[m], y[n]);
 #pragma unroll
       for (int r = i * R / Q; r < (i + 1) * R / Q; r++) rd(r);
 #pragma unroll
@@ -178,6 +204,8 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void ortho_product_kernel
       __builtin_amdgcn_sched_barrier(0);
     }
   };
+  constexpr std::true_type hi{};
+  constexpr std::false_type lo{};
   constexpr std::integral_constant<int, 0> none{};
   constexpr std::integral_constant<int, MB> one{};
   constexpr std::integral_constant<int, 2 * MB> two{};
@@ -185,7 +213,8 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void ortho_product_kernel
   auto nothing = [](int) {};
 
   if constexpr (NS > 2) {
-    acc[0][0] = f32x16{};
+    // One workgroup's matrix instructions hide neither a load's nor an LDS
+    // read's way: NS - 1 runs are in flight, and one is read ahead.
     auto load = [&](int k, int s) INLINE {
 #pragma unroll
       for (int i = 0; i < N; i++) {
@@ -195,79 +224,102 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void ortho_product_kernel
     };
 #pragma unroll
     for (int k = 0; k < NS - 1; k++) load(k, k);
-    f16x8 p[2][4], q[2][4];
-    auto read = [&](int s, f16x8 (&x)[4], f16x8 (&y)[4]) INLINE {
+    f16x8 p[2][4][MB], q[2][4][MB];
+    auto read = [&](int s, f16x8 (&x)[4][MB], f16x8 (&y)[4][MB]) INLINE {
       const char* const st = smem + 2 * s * BYTES;
 #pragma unroll
-      for (int c = 0; c < 4; c++) {
-        x[c] = *(const f16x8*)(st + at_p[c]);
-        y[c] = *(const f16x8*)(st + BYTES + at_q[c]);
-      }
+      for (int c = 0; c < 4; c++)
+#pragma unroll
+        for (int b = 0; b < MB; b++) {
+          x[c][b] = *(const f16x8*)(st + at_p[c] + b * 4096);
+          y[c][b] = *(const f16x8*)(st + BYTES + at_q[c] + b * 4096);
+        }
     };
     int s = 0;  // the stage of run k
     // Run k is in registers: its products, while run k + 1 is read.
-    auto run = [&](int k, const f16x8 (&x)[4], const f16x8 (&y)[4], f16x8 (&nx)[4], f16x8 (&ny)[4]) INLINE {
+    auto run = [&](int k, const f16x8 (&x)[4][MB], const f16x8 (&y)[4][MB], f16x8 (&nx)[4][MB], f16x8 (&ny)[4][MB],
+                   auto firstc) INLINE {
       // Run k + 1 has landed, those after it are on their way; and everyone has
       // read the stage of run k - 1, which run k + NS - 1 goes to.
       wait_loads<(NS - 3) * 2 * N>();
       barrier();
-      load(k + NS - 1, s == 0 ? NS - 1 : s - 1);
+      const int free = s == 0 ? NS - 1 : s - 1;
       s = s == NS - 1 ? 0 : s + 1;
-      read(s, nx, ny);
+      const char* const st = smem + 2 * s * BYTES;
+      // The order is pinned: left alone, the reads end up behind the products.
+      constexpr int Q = 6 * MB * MB, R = 8 * MB, RQ = 2 * Q / 3, L = 2 * N;
 #pragma unroll
-      for (int ks = 0; ks < 2; ks++) {
-        acc[0][0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[ks], y[ks], acc[0][0], 0, 0, 0);
-        acc[0][0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[ks], y[2 + ks], acc[0][0], 0, 0, 0);
-        acc[0][0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[2 + ks], y[ks], acc[0][0], 0, 0, 0);
+      for (int i = 0; i < Q; i++) {
+        const int ks = i / (Q / 2), h = i / (MB * MB) % 3, n = i / MB % MB, m = i % MB;  // hi hi, hi lo, lo hi
+        multiply(firstc.value && ks == 0 && h < (APART ? 2 : 1), h == 0, m, n, x[ks + (h == 2 ? 2 : 0)][m],
+                 y[ks + (h == 1 ? 2 : 0)][n]);
+#pragma unroll
+        for (int r = i * R / RQ; r < (i + 1) * R / RQ && r < R; r++) {
+          // In the order of use.
+          const int c = r / (4 * MB) + (r / (2 * MB) % 2) * 2, b = r % MB;
+          if (r / MB % 2 == 0)
+            nx[c][b] = *(const f16x8*)(st + at_p[c] + b * 4096);
+          else
+            ny[c][b] = *(const f16x8*)(st + BYTES + at_q[c] + b * 4096);
+        }
+#pragma unroll
+        for (int l = (i - RQ) * L / (Q - RQ); i >= RQ && l < (i - RQ + 1) * L / (Q - RQ); l++)
+          l < N ? load_p(k + NS - 1, free, l) : load_q(k + NS - 1, free, l - N);
+        __builtin_amdgcn_sched_barrier(0);
       }
     };
     wait_loads<(NS - 2) * 2 * N>();
     barrier();
     read(0, p[0], q[0]);
+    run(0, p[0], q[0], p[1], q[1], std::true_type());
 #pragma unroll 1
-    for (int k = 0; k < a.runs; k += 2) {
-      run(k, p[0], q[0], p[1], q[1]);
-      if (k + 1 < a.runs) run(k + 1, p[1], q[1], p[0], q[0]);
+    for (int k = 1; k < a.runs; k += 2) {
+      run(k, p[1], q[1], p[0], q[0], std::false_type());
+      if (k + 1 < a.runs) run(k + 1, p[0], q[0], p[1], q[1], std::false_type());
     }
   } else {
     f16x8 ph0[MB], ph1[MB], pl[MB], qh0[MB], qh1[MB], ql[MB];
-    // Run 0 and the first operand's run 1.
+    // Runs 0 .. NS - 2, and the first operand's run NS - 1.
 #pragma unroll
-    for (int i = 0; i < N; i++) load_p(0, 0, i);
+    for (int k = 0; k < NS - 1; k++) {
 #pragma unroll
-    for (int i = 0; i < N; i++) load_q(0, 0, i);
-    wait_all();
+      for (int i = 0; i < N; i++) load_p(k, k, i);
+#pragma unroll
+      for (int i = 0; i < N; i++) load_q(k, k, i);
+    }
+    wait_loads<(NS - 2) * 2 * N>();
     barrier();
 #pragma unroll
-    for (int i = 0; i < N; i++) load_p(1, 1, i);
+    for (int i = 0; i < N; i++) load_p(NS - 1, NS - 1, i);
 #pragma unroll
     for (int b = 0; b < MB; b++) {
       ph0[b] = read_p(0, 0, 0, b);
       qh0[b] = read_q(0, 0, 0, b);
     }
-    // Run k in stage S, whose first hi fragments are in registers.  The other
-    // stage gets the second operand's run k + 1 here, and this one, once every
-    // wave has read it, the first operand's run k + 2.
+    // Run k in stage S, whose first hi fragments are in registers.  The stage
+    // before it gets the second operand's run k + NS - 1; S itself, once every
+    // wave has read it (and run k + 1 has landed), the first operand's run k + NS.
     auto run = [&](int k, auto sc, auto firstc) INLINE {
-      constexpr int S = decltype(sc)::value;
-      part(firstc, ph0, qh0, two,
+      constexpr int S = decltype(sc)::value, NEXT = (S + 1) % NS, LAST = (S + NS - 1) % NS;
+      part(firstc, hi, ph0, qh0, two,
            [&](int r) { r < MB ? (void)(ql[r] = read_q(S, 0, 1, r)) : (void)(pl[r - MB] = read_p(S, 0, 1, r - MB)); }, all,
-           [&](int i) { load_q(k + 1, 1 - S, i); });
-      part(std::false_type(), ph0, ql, one, [&](int r) { ph1[r] = read_p(S, 1, 0, r); }, none, nothing);
-      part(std::false_type(), pl, qh0, one, [&](int r) { qh1[r] = read_q(S, 1, 0, r); }, none, nothing);
-      part(std::false_type(), ph1, qh1, two,
+           [&](int i) { load_q(k + NS - 1, LAST, i); });
+      part(std::integral_constant<bool, firstc.value && APART>(), lo, ph0, ql, one, [&](int r) { ph1[r] = read_p(S, 1, 0, r); }, none, nothing);
+      part(std::false_type(), lo, pl, qh0, one, [&](int r) { qh1[r] = read_q(S, 1, 0, r); }, none, nothing);
+      part(std::false_type(), hi, ph1, qh1, two,
            [&](int r) { r < MB ? (void)(ql[r] = read_q(S, 1, 1, r)) : (void)(pl[r - MB] = read_p(S, 1, 1, r - MB)); }, none,
            nothing);
-      wait_all();
+      wait_loads<(NS - 2) * 2 * N, 0>();
       barrier();
-      part(std::false_type(), ph1, ql, one, [&](int r) { ph0[r] = read_p(1 - S, 0, 0, r); }, all, [&](int i) { load_p(k + 2, S, i); });
-      part(std::false_type(), pl, qh1, one, [&](int r) { qh0[r] = read_q(1 - S, 0, 0, r); }, none, nothing);
+      part(std::false_type(), lo, ph1, ql, one, [&](int r) { ph0[r] = read_p(NEXT, 0, 0, r); }, all,
+           [&](int i) { load_p(k + NS, S, i); });
+      part(std::false_type(), lo, pl, qh1, one, [&](int r) { qh0[r] = read_q(NEXT, 0, 0, r); }, none, nothing);
     };
     run(0, std::integral_constant<int, 0>(), std::true_type());
 #pragma unroll 1
-    for (int k = 1; k < a.runs; k += 2) {
+    for (int k = 1; k < a.runs; k += NS) {
       run(k, std::integral_constant<int, 1>(), std::false_type());
-      if (k + 1 < a.runs) run(k + 1, std::integral_constant<int, 0>(), std::false_type());
+      if (k + NS - 1 < a.runs) run(k + NS - 1, std::integral_constant<int, 0>(), std::false_type());
     }
   }
   // The last loads (zeros) have landed, and everyone has read the stages.
@@ -276,7 +328,7 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void ortho_product_kernel
 
   // A lane of block (m, n): C column lane % 32, rows 8 q + 4 (lane / 32) + 0..3.
   char* const st = smem + wave * 4096;
-  const int r = lane & 31, hi = lane >> 5;
+  const int r = lane & 31, upper = lane >> 5;
   const int m0 = T * mt + 32 * MB * wm, n0 = T * nt + 32 * MB * wn;
 #pragma unroll
   for (int n = 0; n < MB; n++)
@@ -286,7 +338,7 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void ortho_product_kernel
       const int row0 = m0 + 32 * m, col = n0 + 32 * n + r;
       float v[16];
 #pragma unroll
-      for (int j = 0; j < 16; j++) v[j] = acc[m][n][j] * a.mul;
+      for (int j = 0; j < 16; j++) v[j] = (APART ? acc[m][n][j] + low[APART ? m : 0][APART ? n : 0][j] : acc[m][n][j]) * a.mul;
       if constexpr (STAGE == ORTHO_POLY) {
         u32x2 (&o)[8] = own[EARLY ? n * MB + m : 0];
         if constexpr (!EARLY) fetch(m, n, o);
@@ -297,7 +349,7 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void ortho_product_kernel
           for (int j = 0; j < 4; j++) {
             const float w = half_value(x[j >> 1] >> (16 * (j & 1))) + half_value(y[j >> 1] >> (16 * (j & 1)));
             v[4 * q + j] = __builtin_fmaf(a.p_mul, w, v[4 * q + j]);
-            if (row0 + 8 * q + 4 * hi + j == col) v[4 * q + j] += a.diag;
+            if (row0 + 8 * q + 4 * upper + j == col) v[4 * q + j] += a.diag;
           }
         }
       }
@@ -306,7 +358,7 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void ortho_product_kernel
         for (int q = 0; q < 4; q++)
 #pragma unroll
           for (int j = 0; j < 4; j++) {
-            const int row = row0 + 8 * q + 4 * hi + j;
+            const int row = row0 + 8 * q + 4 * upper + j;
             if (row < a.rows && col < a.cols) {
               const int64_t o = mat * a.out_mat + (a.flip ? col * a.out_row + row : row * a.out_row + col);
               if (a.out_dtype == CBD_F32)
@@ -319,7 +371,7 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void ortho_product_kernel
         uint32_t w[16];
 #pragma unroll
         for (int j = 0; j < 16; j++) {
-          const int row = row0 + 8 * (j >> 2) + 4 * hi + (j & 3);
+          const int row = row0 + 8 * (j >> 2) + 4 * upper + (j & 3);
           w[j] = row < a.rows && col < a.cols ? split(v[j]) : 0u;
         }
         // 128 bytes of a row at a time: 8 lanes.
@@ -335,7 +387,7 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void ortho_product_kernel
         // C^T: row `col`, four neighbouring elements of a lane.
 #pragma unroll
         for (int q = 0; q < 4; q++) {
-          char* const s = st + r * 128 + (hi << 3);
+          char* const s = st + r * 128 + (upper << 3);
           *(u32x2*)(s + ((q ^ (r & 7)) << 4)) =
               u32x2{(w[4 * q] & 0xffffu) | w[4 * q + 1] << 16, (w[4 * q + 2] & 0xffffu) | w[4 * q + 3] << 16};
           *(u32x2*)(s + (((4 + q) ^ (r & 7)) << 4)) =
@@ -346,7 +398,7 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void ortho_product_kernel
         if (!SYM || mt != nt) {
 #pragma unroll
           for (int j = 0; j < 16; j++) {
-            const int row = 8 * (j >> 2) + 4 * hi + (j & 3);
+            const int row = 8 * (j >> 2) + 4 * upper + (j & 3);
             char* const s = st + row * 128 + 2 * (r & 7);
             *(uint16_t*)(s + (((r >> 3) ^ (row & 7)) << 4)) = (uint16_t)w[j];
             *(uint16_t*)(s + (((4 + (r >> 3)) ^ (row & 7)) << 4)) = (uint16_t)(w[j] >> 16);
@@ -452,10 +504,11 @@ __global__ __launch_bounds__(THREADS) void ortho_split_kernel(const OrthoSplit a
 }
 
 template <int STAGE>
-const void* pick(int tile) {
-  return tile == 256   ? (const void*)&ortho_product_kernel<4, STAGE>
-         : tile == 128 ? (const void*)&ortho_product_kernel<2, STAGE>
-                       : (const void*)&ortho_product_kernel<1, STAGE>;
+const void* pick(int tile, int64_t tiles) {
+  if (tile == 256) return (const void*)&ortho_product_kernel<4, STAGE, 2>;
+  if (tile == 64) return (const void*)&ortho_product_kernel<1, STAGE, 5>;
+  return tiles <= 256 ? (const void*)&ortho_product_kernel<2, STAGE, 4>
+                      : (const void*)&ortho_product_kernel<2, STAGE, 2>;
 }
 
 }  // namespace
@@ -476,10 +529,10 @@ int launch_ortho_product(const OrthoArgs& a, int stage, int tile, int64_t matric
   void* args[] = {const_cast<OrthoArgs*>(&a)};
   const bool sym = stage == ORTHO_SQUARE || stage == ORTHO_POLY;
   const int64_t per = sym ? (int64_t)a.tiles_m * (a.tiles_m + 1) / 2 : (int64_t)a.tiles_m * a.tiles_n;
-  const void* k = stage == ORTHO_SQUARE ? pick<ORTHO_SQUARE>(tile)
-                  : stage == ORTHO_POLY ? pick<ORTHO_POLY>(tile)
-                  : stage == ORTHO_STEP ? pick<ORTHO_STEP>(tile)
-                                        : pick<ORTHO_LAST>(tile);
+  const void* k = stage == ORTHO_SQUARE ? pick<ORTHO_SQUARE>(tile, per * matrices)
+                  : stage == ORTHO_POLY ? pick<ORTHO_POLY>(tile, per * matrices)
+                  : stage == ORTHO_STEP ? pick<ORTHO_STEP>(tile, per * matrices)
+                                        : pick<ORTHO_LAST>(tile, per * matrices);
   return (int)hipLaunchKernel(k, dim3((unsigned)(per * matrices)), dim3(THREADS), args, 0, (hipStream_t)stream);
 }
 

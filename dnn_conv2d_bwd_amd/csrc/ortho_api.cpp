@@ -28,19 +28,24 @@ bool exponent(double bound, int& e) {
   return true;
 }
 
-// Tile of a product with `count(t)` tiles of t x t: the one whose rounds over
-// the card take the least matrix time.
+// Tile of a product with count(t) tiles of t x t: the one whose rounds over the
+// card take the least time.  Measured, in us a run of 32 of the contracted side:
+// 64 x 64, one a compute unit 0.22 and two 0.5; 128 x 128 0.58 and 1.38; 256 x 256
+// (one, at the rate that the card's power allows when all are busy) 2.4.  So
+// the last product of a step takes (64 / 128 / 256 in us) 11 / 14 / 33 for 16
+// matrices of 256 x 512, 70 / 51 / 116 for one of 2048 x 2048, 483 / 354 / 303 for
+// one of 4096 x 4096 and 83 / 53 / 74 for four of 1024 x 2048.
 template <typename F>
 int pick_tile(F&& count) {
   struct {
-    int t, at_once;
-    double slower;
-  } const all[] = {{256, 256, 1.0}, {128, 512, 1.2}, {64, 1024, 1.6}};
+    int t;
+    double one, two;
+  } const all[] = {{256, 2.4, 4.8}, {128, 0.58, 1.38}, {64, 0.22, 0.5}};
   int best = 256;
   double least = 0.0;
   for (const auto& c : all) {
-    const double rounds = std::ceil((double)count(c.t) / c.at_once);
-    const double time = rounds * (c.at_once / 256) * c.t * c.t * c.slower;
+    const int64_t n = count(c.t), rest = n % 512;
+    const double time = (double)(n / 512) * c.two + (rest > 256 ? c.two : rest ? c.one : 0.0);
     if (c.t == 256 || time < least) {
       best = c.t;
       least = time;
@@ -97,6 +102,9 @@ cbd_status make_plan(const cbd_ortho_problem* q, cbd_ortho_plan_t** out) {
     return n * m * (m + 1) / 2;
   });
   p->tile_step = pick_tile([&](int64_t t) { return n * ((p->s + t - 1) / t) * ((p->l + t - 1) / t); });
+  const int64_t sym = up_to(p->s, p->tile_sym) / p->tile_sym, ts = up_to(p->s, p->tile_step) / p->tile_step;
+  const int64_t tiles = n * std::max(sym * sym, ts * (up_to(p->l, p->tile_step) / p->tile_step));
+  if (tiles > cbd::host::kMaxGrid) return fail(CBD_ERR_UNSUPPORTED, "too many tiles for one launch");
   const int64_t pad = std::max(p->tile_sym, p->tile_step);
   p->sp = up_to(p->s, pad);
   p->lp = up_to(p->l, pad);
@@ -258,6 +266,19 @@ extern "C" cbd_status cbd_ortho_plan(const cbd_ortho_problem* problem, cbd_ortho
 }
 
 extern "C" void cbd_ortho_plan_destroy(cbd_ortho_plan_t* plan) { delete plan; }
+
+extern "C" cbd_status cbd_ortho_plan_info(const cbd_ortho_plan_t* plan, cbd_ortho_info_t* out) {
+  return guarded([&]() -> cbd_status {
+    if (!plan || !out) return fail(CBD_ERR_INVALID_ARG, "NULL plan or output");
+    out->tile_symmetric = plan->tile_sym;
+    out->tile_step = plan->tile_step;
+    out->launches = plan->prob.matrices ? 2 + 3 * plan->prob.steps : 0;
+    out->reserved = 0;
+    out->flops = plan->prob.matrices * plan->prob.steps * plan->s * plan->s * (3 * plan->l + plan->s);
+    cbd::set_error("");
+    return CBD_OK;
+  });
+}
 
 extern "C" cbd_status cbd_ortho_workspace_size(const cbd_ortho_plan_t* plan, uint64_t* bytes) {
   return guarded([&]() -> cbd_status {

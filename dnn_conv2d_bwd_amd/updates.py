@@ -32,6 +32,11 @@ class OrthoStrides(ctypes.Structure):
                 ("out_matrix", ctypes.c_int64)]
 
 
+class OrthoInfo(ctypes.Structure):
+    _fields_ = [("tile_symmetric", ctypes.c_int32), ("tile_step", ctypes.c_int32), ("launches", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("flops", ctypes.c_int64)]
+
+
 def _bind():
     P = ctypes.POINTER
     V = ctypes.c_void_p
@@ -39,9 +44,10 @@ def _bind():
     _lib.cbd_ortho_plan.argtypes = [P(OrthoProblem), P(V)]
     _lib.cbd_ortho_plan_destroy.argtypes = [V]
     _lib.cbd_ortho_plan_destroy.restype = None
+    _lib.cbd_ortho_plan_info.argtypes = [V, P(OrthoInfo)]
     _lib.cbd_ortho_workspace_size.argtypes = [V, P(U)]
     _lib.cbd_orthogonalize.argtypes = [V, V, V, P(OrthoStrides), V, U, V]
-    for f in ("cbd_ortho_plan", "cbd_ortho_workspace_size", "cbd_orthogonalize"):
+    for f in ("cbd_ortho_plan", "cbd_ortho_plan_info", "cbd_ortho_workspace_size", "cbd_orthogonalize"):
         getattr(_lib, f).restype = ctypes.c_int
 
 
@@ -72,6 +78,12 @@ class OrthoPlan:
         _check(_lib.cbd_ortho_workspace_size(h, ctypes.byref(out)), "cbd_ortho_workspace_size")
         self._ws = int(out.value)
         self._tdtype = _torch_dtype(self.dtype)
+
+    def info(self) -> OrthoInfo:
+        """What a call launches."""
+        out = OrthoInfo()
+        _check(_lib.cbd_ortho_plan_info(self._h, ctypes.byref(out)), "cbd_ortho_plan_info")
+        return out
 
     def workspace_size(self) -> int:
         """Bytes of device workspace a call needs."""

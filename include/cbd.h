@@ -640,10 +640,20 @@ typedef struct cbd_ortho_plan_s cbd_ortho_plan_t; /* opaque; immutable */
 
 /* Host-only.  INVALID_ARG: NULL, sizes, types, steps, eps or scale out of the
  * ranges above, coefficients that are not finite; UNSUPPORTED: matrices, rows or
- * cols above them, and coefficients whose steps let singular values of [0, 1]
+ * cols above them, 2^24 tiles or more, and coefficients whose steps let singular values of [0, 1]
  * grow past 2^20 or shrink below 2^-20. */
 cbd_status cbd_ortho_plan(const cbd_ortho_problem* problem, cbd_ortho_plan_t** out_plan);
 void cbd_ortho_plan_destroy(cbd_ortho_plan_t* plan); /* NULL is allowed */
+
+typedef struct {
+  int32_t tile_symmetric; /* side of a workgroup's tile of A and B */
+  int32_t tile_step;      /* and of X */
+  int32_t launches;       /* kernels per call */
+  int32_t reserved;
+  int64_t flops;          /* of the formula, with the symmetric products halved */
+} cbd_ortho_info_t;
+
+cbd_status cbd_ortho_plan_info(const cbd_ortho_plan_t* plan, cbd_ortho_info_t* out);
 
 /* Device workspace (256-byte aligned; no initialisation, nothing kept; one per
  * stream in use). */

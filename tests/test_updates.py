@@ -1,13 +1,20 @@
 """Orthogonalised updates against their definition in 64 bits, and their
 refusals.
 
-Bounds.  The kernel's values have 22 bits where f32 has 24, its products are
-summed in f32: each of its roundings is at most 4 times one of the f32 form of
-the same formula.  How far roundings are amplified depends on the matrix, and is
-measured on it: the f32 form, computed on the CPU, is off by some error from 64
-bits, and the kernel may be off by 4 times that, and by 2^-22 of the result for
-its last product; in the largest element by 4 times the f32 form's and 2^-20 of
-the result's largest (a largest error of fewer roundings is less even).
+Bounds.  How far roundings are amplified depends on the matrix, and is measured
+on it with a form in f32: stored values are f32, and a sum of products is taken
+one term at a time, acc = f32(acc + a b).  The kernel's roundings, against that
+form's: a stored value has 22 bits where f32 has 24, so each of these roundings is
+at most 4 times as large; and a sum takes at most three additions (hi hi, hi lo, lo
+hi) for each term, in whatever order the matrix instructions add their 16 terms,
+each off by at most half a step of a partial sum: at most 3 times as much.  Where
+the form is off by some error from 64 bits, the kernel may therefore be off by 4
+times that, and by 2^-22 of the result for what it leaves out (lo lo, at most 2^-22
+of a product); in the largest element by 4 times the form's and 2^-20 of the
+result's largest (a largest error of few roundings is less even).
+(A form whose sums are taken in another order says nothing about this: a CPU's
+product of 2047 x 1990 by its transpose keeps many partial sums, and is off by
+several times less than additions in a row.)
 Results add half a step (bf16 2^-8, f32 2^-24)."""
 from __future__ import annotations
 
@@ -23,15 +30,32 @@ TORCH = {"bf16": torch.bfloat16, "f32": torch.float32}
 USUAL = (3.4445, -4.7750, 2.0315)
 
 
-def define(m, steps=5, coefficients=None, eps=1e-7, scale=1.0, dtype=torch.float64):
+def exact_product(a, b):
+    return a @ b
+
+
+def f32_product(a, b):
+    """In f32, one term at a time."""
+    acc = torch.zeros(a.shape[0], a.shape[1], b.shape[2], dtype=torch.float32, device=a.device)
+    a, b = a.double(), b.double()
+    for k in range(a.shape[2]):
+        acc = torch.addcmul(acc.double(), a[:, :, k:k + 1], b[:, k:k + 1]).float()
+    return acc
+
+
+def define(m, steps=5, coefficients=None, eps=1e-7, scale=1.0, f32=False):
     norm = m.double().square().sum((1, 2), keepdim=True).sqrt() + eps
-    x = (m.double() / norm).to(dtype)
+    x = m.double() / norm
+    if f32:
+        x = x.float()
+    product = f32_product if f32 else exact_product
     flip = m.shape[1] > m.shape[2]
-    x = x.transpose(1, 2) if flip else x
+    x = x.transpose(1, 2).contiguous() if flip else x
     for k in range(steps):
         a, b, c = USUAL if coefficients is None else coefficients[k]
-        q = x @ x.transpose(1, 2)
-        x = a * x + (b * q + c * (q @ q)) @ x
+        q = product(x, x.transpose(1, 2).contiguous())
+        p = b * q + c * product(q, q)
+        x = a * x + product(p, x)
     return (scale * x).transpose(1, 2) if flip else scale * x
 
 
@@ -44,7 +68,8 @@ def draw(n, rows, cols, dtype="f32", seed=0, rank=None, scale=1e-3):
 
 
 def near(got, m, dtype, name="", **kw):
-    want, plain = define(m, **kw), define(m, dtype=torch.float32, **kw).double()
+    m = m.cuda()  # for the form's many small steps
+    want, plain = define(m, **kw).cpu(), define(m, f32=True, **kw).double().cpu()
     got, half = got.double().cpu(), torch.finfo(TORCH[dtype]).eps / 2
     for i in range(m.shape[0]):
         w, err, err32 = want[i], (got[i] - want[i]).abs(), (plain[i] - want[i]).abs()
@@ -98,15 +123,24 @@ def test_against_definition(dtype, size):
     near(call(m), m, dtype, str(size))
 
 
+# matrices, rows, cols; tiles of A and B, and of X.  128 also with more tiles than
+# compute units (two workgroups on one).
+TILES = [((300, 64, 96), 64, 64), ((9, 512, 768), 64, 128), ((9, 700, 1100), 128, 128), ((17, 1500, 500), 128, 256),
+         ((1, 2047, 1990), 128, 128), ((14, 1030, 1900), 128, 128), ((7, 1000, 2040), 128, 256),
+         ((25, 1090, 1000), 256, 256)]
+
+
 @pytest.mark.gpu
-@pytest.mark.parametrize("size", [(9, 512, 768), (12, 700, 520), (30, 256, 256), (2, 1100, 2300), (300, 64, 96)], ids=str)
-def test_every_tile(size):
-    """Enough tiles that the larger ones are chosen, with edges inside them."""
-    print("[ortho] tiles", size, flush=True)
-    m = draw(*size, seed=size[1], rank=max(1, size[1] // 8))
-    got = call(m)
-    some = [0, size[0] // 2, size[0] - 1]
-    near(got[some], m[some], "f32", str(size))
+@pytest.mark.parametrize("size,symmetric,step", TILES, ids=str)
+def test_every_tile(size, symmetric, step):
+    """Sizes at which each tile is chosen, with edges inside tiles."""
+    info = cbd.ortho_plan(*size).info()
+    print("[ortho] tiles", size, info.tile_symmetric, info.tile_step, flush=True)
+    assert (info.tile_symmetric, info.tile_step) == (symmetric, step)
+    m = draw(*size, seed=size[1], rank=max(1, min(size[1:]) // 8))
+    got = call(m, steps=3)
+    some = [0, size[0] - 1] if size[0] > 1 else [0]
+    near(got[some], m[some], "f32", str(size), steps=3)
 
 
 @pytest.mark.gpu
@@ -225,7 +259,7 @@ def test_convenience_and_written():
 @pytest.mark.parametrize("over,status", [
     (dict(matrices=-1), 1), (dict(rows=0), 1), (dict(cols=-2), 1), (dict(dtype=2), 1), (dict(steps=0), 1),
     (dict(steps=65), 1), (dict(eps=0.0), 1), (dict(eps=float("nan")), 1), (dict(scale=float("inf")), 1),
-    (dict(matrices=65536), 2), (dict(rows=65537), 2), (dict(cols=65537), 2), (dict(matrices=0), 0), (dict(), 0),
+    (dict(matrices=65536), 2), (dict(rows=65537), 2), (dict(cols=65537), 2), (dict(matrices=65535, rows=65536, cols=65536), 2), (dict(matrices=0), 0), (dict(), 0),
     (dict(co=(3.0, float("nan"), 1.0)), 1), (dict(co=(0.0, 0.0, 0.0)), 2), (dict(co=(9.0, 9.0, 9.0)), 2),
     (dict(co=(1e-30, 0.0, 0.0)), 2), (dict(co=(1.5, -0.5, 0.0)), 0)])
 def test_plan_refusals(over, status):
@@ -259,6 +293,13 @@ def test_run_refusals():
     assert run(o=i + 4) == 1 and run(o=i, s=S(24, 384, 32, 512)) == 1 and run(o=ws) == 1 and run(i=ws + 64) == 1
     none = cbd.ortho_plan(0, 16, 24)
     assert run(plan=none._h, i=None, o=None, ws=None, size=0) == 0
+
+
+def test_info():
+    i = cbd.ortho_plan(8, 4096, 2048, steps=5).info()
+    assert (i.tile_symmetric, i.tile_step, i.launches) == (128, 256, 17)
+    assert i.flops == 8 * 5 * (3 * 2048 * 2048 * 4096 + 2048 ** 3)
+    assert cbd.ortho_plan(0, 16, 16).info().launches == 0
 
 
 def test_python_refusals_without_a_gpu():
