@@ -114,15 +114,14 @@ struct Operand {
     for (int i = 0; i < NV; i++) {
       const int idx = i * THREADS + (int)threadIdx.x;
       int row = idx / QUADS, col = 4 * (idx % QUADS);
+      [[maybe_unused]] int64_t second = 0;
       if constexpr (PAIR) {
         int& r = KC ? row : col;
-        q[i] = p + dev::Pair<R, 2>::part(r) * up;
+        second = dev::Pair<R, 2>::part(r) * up;
         r = dev::Pair<R, 2>::feat(r);
-      } else {
-        q[i] = p;
       }
       if (KC) {
-        q[i] += (row < rows ? row : rows - 1) * ld + col;
+        q[i] = p + (row < rows ? row : rows - 1) * ld + col;
         feats[i] = 4;
         back[i] = 0;
       } else {
@@ -131,9 +130,10 @@ struct Operand {
         // when it is staged: no wait for it in between.
         back[i] = rows - f < 4 && wide ? 4 - (rows - f) : 0;
         edge = edge || __any(back[i] != 0);
-        q[i] += row * ld + f - back[i];
+        q[i] = p + row * ld + f - back[i];
         feats[i] = rows - f + back[i];
       }
+      if constexpr (PAIR) q[i] += second;
     }
   }
   // The next step, of which `left` k are inside, into registers `slot`.

@@ -321,6 +321,12 @@ struct Feed {
 // added to what is there; or at any alignment and width, added or not.
 enum Out { WHOLE, WHOLE_ADD, ANY };
 
+// A gated tile's first feature and row.
+struct Where {
+  int m0, n0;
+};
+struct Nowhere {};
+
 template <typename TO, int FORM, int MB, int NB, bool DMA, Out OUT, int GATE = GATE_NONE>
 __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void expert_mfma_kernel(
     const std::conditional_t<GATE == GATE_NONE, ExpertArgs, GatedArgs> a) {
@@ -355,10 +361,9 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void expert_mfma_kernel(
   auto issue_b = [&](int stage, int i) CBD_INLINE { fb.issue(i, mb + (uint32_t)(stage * FeedB::BYTES + i * 1024)); };
 
   // A tile: its contracted length, and where and how much it writes.
-  struct Tile {
+  struct Tile : std::conditional_t<GATE == GATE_NONE, Nowhere, Where> {
     TO* out;
     int K, mrows, nrows;
-    int m0, n0;  // gated only
   };
   // Points the feeds at tile t and issues its first loads: of NS steps, but
   // with more than two stages not the rows of the last.
@@ -879,25 +884,29 @@ __global__ __launch_bounds__(THREADS, MB == 4 ? 1 : 2) void expert_mfma_kernel(
     if (OUT == WHOLE_ADD || (OUT == ANY && a.accumulate)) return;
     constexpr int PER = 16 / sizeof(TO), ROWS = THREADS / (FEATS / PER);
     const int tid = fresh_tid(), f = PER * (tid % (FEATS / PER));
-    auto clear = [&](TO* out, int64_t ld) CBD_INLINE {
 #pragma unroll 1
-      for (int row = tid / (FEATS / PER); row < BN && row < done.nrows; row += ROWS) {
-        TO* o = out + row * ld + f;
-        if (done.mrows - f >= PER) {
-          *(u32x4u*)o = u32x4{0u, 0u, 0u, 0u};
-        } else {
+    for (int row = tid / (FEATS / PER); row < BN && row < done.nrows; row += ROWS) {
+      TO* o = done.out + row * a.ldo + f;
+      if (done.mrows - f >= PER) {
+        *(u32x4u*)o = u32x4{0u, 0u, 0u, 0u};
+      } else {
 #pragma unroll 1
-          for (int j = 0; f + j < done.mrows; j++) o[j] = TO(0);
-        }
+        for (int j = 0; f + j < done.mrows; j++) o[j] = TO(0);
       }
-    };
-    clear(done.out, a.ldo);
-    if constexpr (GATE == GATE_FWD_SAVE) {
-      TO* const gs = (TO*)a.gu + done.n0 * a.ldgu + done.m0;
-      clear(gs, a.ldgu);
-      clear(gs + a.M, a.ldgu);
     }
-    if constexpr (GATE == GATE_BWD) clear(done.out + a.M, a.ldo);
+    if constexpr (GATE == GATE_FWD_SAVE || GATE == GATE_BWD) {
+      // The other places that the tile's features have.
+      const int64_t ld = GATE == GATE_BWD ? a.ldo : a.ldgu;
+      TO* const first = GATE == GATE_BWD ? done.out + a.M : (TO*)a.gu + done.n0 * a.ldgu + done.m0;
+#pragma unroll 1
+      for (int part = 0; part < (GATE == GATE_BWD ? 1 : 2); part++)
+#pragma unroll 1
+        for (int row = tid / (FEATS / PER); row < BN && row < done.nrows; row += ROWS) {
+          TO* o = first + part * (int64_t)a.M + row * ld + f;
+#pragma unroll 1
+          for (int j = 0; j < PER && f + j < done.mrows; j++) o[j] = TO(0);
+        }
+    }
   };
 
   do {
