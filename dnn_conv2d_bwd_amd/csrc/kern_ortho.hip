@@ -30,6 +30,9 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((__vector_size__(16 * sizeof(float))));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) char lds_char;
 #define INLINE __attribute__((always_inline))
@@ -327,11 +330,14 @@ __global__ __launch_bounds__(THREADS, MB == 4 || (MB == 2 && NS > 2) ? 1 : 2) vo
   barrier();
 
   // A lane of block (m, n): C column lane % 32, rows 8 q + 4 (lane / 32) + 0..3.
-  char* const st = smem + wave * 4096;
+  // Blocks are staged one column (MB of them) at a time, rows of PITCH words.
+  constexpr int PITCH = 36;
+  char* const stage = smem + wave * (MB * 32 * PITCH * 4);
+  char* const st = stage;
   const int r = lane & 31, upper = lane >> 5;
   const int m0 = T * mt + 32 * MB * wm, n0 = T * nt + 32 * MB * wn;
 #pragma unroll
-  for (int n = 0; n < MB; n++)
+  for (int n = 0; n < MB; n++) {
 #pragma unroll
     for (int m = 0; m < MB; m++) {
       if constexpr (MB == 4) asm volatile("" : "+a"(acc[m][n]));
@@ -354,19 +360,52 @@ __global__ __launch_bounds__(THREADS, MB == 4 || (MB == 2 && NS > 2) ? 1 : 2) vo
         }
       }
       if constexpr (STAGE == ORTHO_LAST) {
+        // A row of the output at a time, four elements a lane: 32 x 32 in f32, chunk
+        // c of row i at c ^ (i % 8).
+        float* const f = (float*)st;
+        if (a.flip) {
 #pragma unroll
-        for (int q = 0; q < 4; q++)
+          for (int q = 0; q < 4; q++)
+            *(f32x4*)(st + r * 128 + (((2 * q + upper) ^ (r & 7)) << 4)) =
+                f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+        } else {
 #pragma unroll
-          for (int j = 0; j < 4; j++) {
-            const int row = row0 + 8 * q + 4 * upper + j;
-            if (row < a.rows && col < a.cols) {
-              const int64_t o = mat * a.out_mat + (a.flip ? col * a.out_row + row : row * a.out_row + col);
-              if (a.out_dtype == CBD_F32)
-                ((float*)a.out)[o] = v[4 * q + j];
-              else
-                ((uint16_t*)a.out)[o] = (uint16_t)dev::bf16_rne(v[4 * q + j]);
+          for (int j = 0; j < 16; j++) {
+            const int i = 8 * (j >> 2) + 4 * upper + (j & 3);
+            f[32 * i + (((r >> 2) ^ (i & 7)) << 2) + (r & 3)] = v[j];
+          }
+        }
+        asm volatile("" ::: "memory");  // a wave's LDS accesses run in order
+        const int out0 = a.flip ? n0 + 32 * n : row0, in0 = a.flip ? row0 : n0 + 32 * n;
+        const int outs = a.flip ? a.cols : a.rows, ins = a.flip ? a.rows : a.cols;
+#pragma unroll
+        for (int it = 0; it < 4; it++) {
+          const int i = 8 * it + (lane >> 3), c = lane & 7;
+          const f32x4 w = *(const f32x4*)(st + i * 128 + ((c ^ (i & 7)) << 4));
+          const int left = out0 + i < outs ? ins - in0 - 4 * c : 0;
+          const int64_t o = mat * a.out_mat + (int64_t)(out0 + i) * a.out_row + in0 + 4 * c;
+          if (a.out_dtype == CBD_F32) {
+            float* const d = (float*)a.out + o;
+            if (left >= 4) {
+              *(f32x4u*)d = w;
+            } else {
+#pragma unroll
+              for (int j = 0; j < 3; j++)
+                if (j < left) d[j] = w[j];
+            }
+          } else {
+            uint16_t* const d = (uint16_t*)a.out + o;
+            const u32x2 b = {dev::bf16_pack2(w[0], w[1]), dev::bf16_pack2(w[2], w[3])};
+            if (left >= 4) {
+              *(u32x2u*)d = b;
+            } else {
+#pragma unroll
+              for (int j = 0; j < 3; j++)
+                if (j < left) d[j] = (uint16_t)(b[j >> 1] >> (16 * (j & 1)));
             }
           }
+        }
+        asm volatile("" ::: "memory");
       } else {
         uint32_t w[16];
 #pragma unroll
@@ -374,40 +413,53 @@ __global__ __launch_bounds__(THREADS, MB == 4 || (MB == 2 && NS > 2) ? 1 : 2) vo
           const int row = row0 + 8 * (j >> 2) + 4 * upper + (j & 3);
           w[j] = row < a.rows && col < a.cols ? split(v[j]) : 0u;
         }
-        // 128 bytes of a row at a time: 8 lanes.
-        auto leave = [&](uint16_t* o, int ld) INLINE {
-          asm volatile("" ::: "memory");  // a wave's LDS accesses run in order
+        // As C^T, row `col`: four neighbouring elements of a lane at a time, both
+        // halves of one in a word.
+        uint32_t* const t = (uint32_t*)(stage + m * (32 * PITCH * 4));
 #pragma unroll
-          for (int it = 0; it < 4; it++) {
-            const int row = 8 * it + (lane >> 3), c = lane & 7;
-            *(u32x4*)(o + (int64_t)row * ld + 8 * c) = *(const u32x4*)(st + row * 128 + ((c ^ (row & 7)) << 4));
-          }
-          asm volatile("" ::: "memory");
-        };
-        // C^T: row `col`, four neighbouring elements of a lane.
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-          char* const s = st + r * 128 + (upper << 3);
-          *(u32x2*)(s + ((q ^ (r & 7)) << 4)) =
-              u32x2{(w[4 * q] & 0xffffu) | w[4 * q + 1] << 16, (w[4 * q + 2] & 0xffffu) | w[4 * q + 3] << 16};
-          *(u32x2*)(s + (((4 + q) ^ (r & 7)) << 4)) =
-              u32x2{w[4 * q] >> 16 | (w[4 * q + 1] & 0xffff0000u), w[4 * q + 2] >> 16 | (w[4 * q + 3] & 0xffff0000u)};
-        }
-        leave(a.ct + mat * a.ct_mat + (int64_t)(n0 + 32 * n) * a.ldct + (row0 >> 5) * 64, a.ldct);
-        // C: by elements.  A diagonal tile of a symmetric matrix has both already.
-        if (!SYM || mt != nt) {
-#pragma unroll
-          for (int j = 0; j < 16; j++) {
-            const int row = 8 * (j >> 2) + 4 * upper + (j & 3);
-            char* const s = st + row * 128 + 2 * (r & 7);
-            *(uint16_t*)(s + (((r >> 3) ^ (row & 7)) << 4)) = (uint16_t)w[j];
-            *(uint16_t*)(s + (((4 + (r >> 3)) ^ (row & 7)) << 4)) = (uint16_t)(w[j] >> 16);
-          }
-          leave(a.c + mat * a.c_mat + (int64_t)row0 * a.ldc + ((n0 + 32 * n) >> 5) * 64, a.ldc);
-        }
+        for (int q = 0; q < 4; q++)
+          *(u32x4*)(t + PITCH * r + 8 * q + 4 * upper) = u32x4{w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]};
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    if constexpr (STAGE != ORTHO_LAST) {
+      // A column of blocks leaves: eight elements a lane, their hi and their lo.
+      asm volatile("" ::: "memory");  // a wave's LDS accesses run in order
+      auto leave = [&](const uint32_t (&w)[8], uint16_t* o) INLINE {
+        u32x4 hi, lo;
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          hi[j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], 0x05040100u);
+          lo[j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], 0x07060302u);
+        }
+        *(u32x4*)o = hi;
+        *(u32x4*)(o + 32) = lo;
+      };
+#pragma unroll
+      for (int m = 0; m < MB; m++)
+#pragma unroll
+        for (int it = 0; it < 2; it++) {
+          const int i = 16 * it + (lane >> 2), e = 8 * (lane & 3);
+          const uint32_t* const t = (const uint32_t*)(stage + m * (32 * PITCH * 4));
+          uint32_t w[8];
+#pragma unroll
+          for (int j = 0; j < 2; j++) {
+            const u32x4 x = *(const u32x4*)(t + PITCH * i + e + 4 * j);
+#pragma unroll
+            for (int k = 0; k < 4; k++) w[4 * j + k] = x[k];
+          }
+          leave(w, a.ct + mat * a.ct_mat + (int64_t)(n0 + 32 * n + i) * a.ldct + ((m0 >> 5) + m) * 64 + e);
+          // A diagonal tile of a symmetric matrix has both directions already.
+          if (!SYM || mt != nt) {
+#pragma unroll
+            for (int k = 0; k < 8; k++) w[k] = t[PITCH * (e + k) + i];
+            leave(w, a.c + mat * a.c_mat + (int64_t)(m0 + 32 * m + i) * a.ldc + ((n0 >> 5) + n) * 64 + e);
+          }
+        }
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
 }
 
 // ---- the input: norm, then both directions as two halves a value

@@ -28,30 +28,63 @@ bool exponent(double bound, int& e) {
   return true;
 }
 
-// Tile of a product with count(t) tiles of t x t: the one whose rounds over the
-// card take the least time.  Measured, in us a run of 32 of the contracted side:
-// 64 x 64, one a compute unit 0.22 and two 0.5; 128 x 128 0.58 and 1.38; 256 x 256
-// (one, at the rate that the card's power allows when all are busy) 2.4.  So
-// the last product of a step takes (64 / 128 / 256 in us) 11 / 14 / 33 for 16
-// matrices of 256 x 512, 70 / 51 / 116 for one of 2048 x 2048, 483 / 354 / 303 for
-// one of 4096 x 4096 and 83 / 53 / 74 for four of 1024 x 2048.
+struct Tile {
+  int t;
+  double one, two;
+};
+// Measured, in us a run of 32 of the contracted side, with one workgroup a compute
+// unit and with two (256 x 256: one after the other, at the rate that the card's
+// power allows when all are busy).  So the last product of a step takes (64 / 128 /
+// 256 in us) 11 / 14 / 33 for 16 matrices of 256 x 512, 70 / 51 / 116 for one of
+// 2048 x 2048, 483 / 354 / 303 for one of 4096 x 4096 and 83 / 53 / 74 for four of
+// 1024 x 2048.
+constexpr Tile kTiles[] = {{256, 2.4, 4.8}, {128, 0.58, 1.38}, {64, 0.22, 0.5}};
+constexpr double kLaunch = 4.0;  // us of another launch
+
+double time_of(const Tile& c, int64_t tiles) {
+  const int64_t rest = tiles % 512;
+  return (double)(tiles / 512) * c.two + (rest > 256 ? c.two : rest ? c.one : 0.0);
+}
+
+// How n matrices with tiles(t) tiles of t x t each and `runs` runs are computed:
+// in the tiles that take the least time over all their rounds on the card, or the
+// first ones in larger and the rest in smaller tiles, where that leaves fewer
+// units idle in the end (A of 8 matrices of 2048 x 4096, 36 tiles of 256 each: 7 in
+// one round of those and the last in tiles of 128 387 us, all in tiles of 128
+// 404).
 template <typename F>
-int pick_tile(F&& count) {
-  struct {
-    int t;
-    double one, two;
-  } const all[] = {{256, 2.4, 4.8}, {128, 0.58, 1.38}, {64, 0.22, 0.5}};
-  int best = 256;
+void share_out(int64_t n, int64_t runs, F&& tiles, cbd::OrthoShare (&out)[2]) {
+  auto best = [&](int64_t count, double& least) {
+    int at = 0;
+    least = 0.0;
+    for (int i = 0; i < 3; i++) {
+      const double time = time_of(kTiles[i], count * tiles(kTiles[i].t));
+      if (i == 0 || time < least) {
+        at = i;
+        least = time;
+      }
+    }
+    return at;
+  };
   double least = 0.0;
-  for (const auto& c : all) {
-    const int64_t n = count(c.t), rest = n % 512;
-    const double time = (double)(n / 512) * c.two + (rest > 256 ? c.two : rest ? c.one : 0.0);
-    if (c.t == 256 || time < least) {
-      best = c.t;
-      least = time;
+  out[0] = {kTiles[best(n, least)].t, n};
+  out[1] = {64, 0};
+  for (int i = 0; i < 2; i++) {
+    // Whole rounds of the larger tiles.
+    const int64_t per = tiles(kTiles[i].t), round = i == 0 ? 256 : 512;
+    for (int64_t r = 1; r <= 64 && r * round / per < n; r++) {
+      const int64_t k = r * round / per;
+      if (!k) continue;
+      double rest = 0.0;
+      const int at = best(n - k, rest);
+      const double time = time_of(kTiles[i], k * per) + rest + kLaunch / (double)runs;
+      if (at > i && time < least) {
+        least = time;
+        out[0] = {kTiles[i].t, k};
+        out[1] = {kTiles[at].t, n - k};
+      }
     }
   }
-  return best;
 }
 
 cbd_status make_plan(const cbd_ortho_problem* q, cbd_ortho_plan_t** out) {
@@ -82,8 +115,8 @@ cbd_status make_plan(const cbd_ortho_problem* q, cbd_ortho_plan_t** out) {
       p->coefficients.push_back(c[i]);
     }
     double most_b = 0.0, most_x = 0.0;
-    for (int i = 0; i <= 4096; i++) {
-      const double x = top * i / 4096, b = std::fabs(c[0] + x * x * (c[1] + x * x * c[2]));
+    for (int i = 0; i <= 512; i++) {
+      const double x = top * i / 512, b = std::fabs(c[0] + x * x * (c[1] + x * x * c[2]));
       most_b = std::max(most_b, b);
       most_x = std::max(most_x, b * x);
     }
@@ -97,15 +130,22 @@ cbd_status make_plan(const cbd_ortho_problem* q, cbd_ortho_plan_t** out) {
   p->s = std::min(q->rows, q->cols);
   p->l = std::max(q->rows, q->cols);
   const int64_t n = std::max<int64_t>(q->matrices, 1);
-  p->tile_sym = pick_tile([&](int64_t t) {
+  const int64_t runs = (p->s + 31) / 32;
+  auto sym = [&](int64_t t) {
     const int64_t m = (p->s + t - 1) / t;
-    return n * m * (m + 1) / 2;
-  });
-  p->tile_step = pick_tile([&](int64_t t) { return n * ((p->s + t - 1) / t) * ((p->l + t - 1) / t); });
-  const int64_t sym = up_to(p->s, p->tile_sym) / p->tile_sym, ts = up_to(p->s, p->tile_step) / p->tile_step;
-  const int64_t tiles = n * std::max(sym * sym, ts * (up_to(p->l, p->tile_step) / p->tile_step));
-  if (tiles > cbd::host::kMaxGrid) return fail(CBD_ERR_UNSUPPORTED, "too many tiles for one launch");
-  const int64_t pad = std::max(p->tile_sym, p->tile_step);
+    return m * (m + 1) / 2;
+  };
+  auto step = [&](int64_t t) { return ((p->s + t - 1) / t) * ((p->l + t - 1) / t); };
+  share_out(n, runs, sym, p->sym);
+  share_out(n, runs, step, p->step);
+  int64_t pad = 64;
+  for (const auto* shares : {p->sym, p->step})
+    for (int i = 0; i < 2; i++) {
+      if (!shares[i].count) continue;
+      pad = std::max<int64_t>(pad, shares[i].tile);
+      if (shares[i].count * std::max(step(shares[i].tile), sym(shares[i].tile)) > cbd::host::kMaxGrid)
+        return fail(CBD_ERR_UNSUPPORTED, "too many tiles for one launch");
+    }
   p->sp = up_to(p->s, pad);
   p->lp = up_to(p->l, pad);
   *out = p.release();
@@ -191,6 +231,23 @@ cbd_status run(const cbd_ortho_plan_t* plan, const void* in, void* out, const cb
   if (!err) err = cbd::launch_ortho_split(f, n, stream);
 
   auto tiles = [](int64_t v, int t) { return (int32_t)((v + t - 1) / t); };
+  // A product of all matrices, share by share.
+  auto product = [&](const cbd::OrthoArgs& all, int stage, const cbd::OrthoShare (&shares)[2]) {
+    int64_t first = 0;
+    for (const cbd::OrthoShare& h : shares) {
+      if (!h.count || err) continue;
+      cbd::OrthoArgs a = all;
+      a.p += first * a.p_mat;
+      a.q += first * a.q_mat;
+      if (a.c) a.c += first * a.c_mat;
+      if (a.ct) a.ct += first * a.ct_mat;
+      if (a.out) a.out = (char*)a.out + first * a.out_mat * es;
+      a.tiles_m = tiles(a.rows, h.tile);
+      a.tiles_n = tiles(a.cols, h.tile);
+      err = cbd::launch_ortho_product(a, stage, h.tile, h.count, stream);
+      first += h.count;
+    }
+  };
   for (int k = 0; k < q.steps && !err; k++) {
     const double* c = &plan->coefficients[3 * k];
     const int ex = plan->ex[k], ea = plan->ea[k], eb = plan->eb[k];
@@ -199,14 +256,12 @@ cbd_status run(const cbd_ortho_plan_t* plan, const void* in, void* out, const cb
     a.p_mat = a.q_mat = lay.x;
     a.ldp = a.ldq = ldx;
     a.runs = tiles(plan->l, 32);
-    a.tiles_m = a.tiles_n = tiles(plan->s, plan->tile_sym);
     a.rows = a.cols = (int32_t)plan->s;
     a.c = a.ct = sq;
     a.c_mat = a.ct_mat = lay.a;
     a.ldc = a.ldct = ldxt;
     a.mul = (float)std::ldexp(1.0, ea - 2 * ex);
-    err = cbd::launch_ortho_product(a, cbd::ORTHO_SQUARE, plan->tile_sym, n, stream);
-    if (err) break;
+    product(a, cbd::ORTHO_SQUARE, plan->sym);
 
     a.p = a.q = sq;
     a.p_mat = a.q_mat = lay.a;
@@ -216,8 +271,7 @@ cbd_status run(const cbd_ortho_plan_t* plan, const void* in, void* out, const cb
     a.mul = (float)std::ldexp(c[2], eb - 2 * ea);
     a.p_mul = (float)std::ldexp(c[1], eb - ea);
     a.diag = (float)std::ldexp(c[0], eb);
-    err = cbd::launch_ortho_product(a, cbd::ORTHO_POLY, plan->tile_sym, n, stream);
-    if (err) break;
+    product(a, cbd::ORTHO_POLY, plan->sym);
 
     const bool last = k == q.steps - 1;
     a = {};
@@ -228,8 +282,6 @@ cbd_status run(const cbd_ortho_plan_t* plan, const void* in, void* out, const cb
     a.q_mat = lay.x;
     a.ldq = ldxt;
     a.runs = tiles(plan->s, 32);
-    a.tiles_m = tiles(plan->s, plan->tile_step);
-    a.tiles_n = tiles(plan->l, plan->tile_step);
     a.rows = (int32_t)plan->s;
     a.cols = (int32_t)plan->l;
     if (last) {
@@ -248,7 +300,7 @@ cbd_status run(const cbd_ortho_plan_t* plan, const void* in, void* out, const cb
       a.ct_mat = lay.x;
       a.ldct = ldxt;
     }
-    err = cbd::launch_ortho_product(a, last ? cbd::ORTHO_LAST : cbd::ORTHO_STEP, plan->tile_step, n, stream);
+    product(a, last ? cbd::ORTHO_LAST : cbd::ORTHO_STEP, plan->step);
     std::swap(xt, xt_next);
   }
   if (err) {
@@ -270,9 +322,12 @@ extern "C" void cbd_ortho_plan_destroy(cbd_ortho_plan_t* plan) { delete plan; }
 extern "C" cbd_status cbd_ortho_plan_info(const cbd_ortho_plan_t* plan, cbd_ortho_info_t* out) {
   return guarded([&]() -> cbd_status {
     if (!plan || !out) return fail(CBD_ERR_INVALID_ARG, "NULL plan or output");
-    out->tile_symmetric = plan->tile_sym;
-    out->tile_step = plan->tile_step;
-    out->launches = plan->prob.matrices ? 2 + 3 * plan->prob.steps : 0;
+    const int sym = plan->sym[1].count ? 2 : 1, step = plan->step[1].count ? 2 : 1;
+    out->tile_symmetric = plan->sym[0].tile;
+    out->tile_step = plan->step[0].tile;
+    out->tile_symmetric_rest = plan->sym[1].count ? plan->sym[1].tile : 0;
+    out->tile_step_rest = plan->step[1].count ? plan->step[1].tile : 0;
+    out->launches = plan->prob.matrices ? 2 + plan->prob.steps * (2 * sym + step) : 0;
     out->reserved = 0;
     out->flops = plan->prob.matrices * plan->prob.steps * plan->s * plan->s * (3 * plan->l + plan->s);
     cbd::set_error("");

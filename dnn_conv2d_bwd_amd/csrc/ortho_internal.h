@@ -54,6 +54,12 @@ struct OrthoSplit {
 
 constexpr int kOrthoParts = 256;
 
+// The first `count` matrices (of those left) in tiles of `tile`; count 0: none.
+struct OrthoShare {
+  int tile;
+  int64_t count;
+};
+
 int launch_ortho_norm(const OrthoSplit& a, int64_t matrices, void* stream);
 int launch_ortho_split(const OrthoSplit& a, int64_t matrices, void* stream);
 int launch_ortho_product(const OrthoArgs& a, int stage, int tile, int64_t matrices, void* stream);
@@ -64,7 +70,7 @@ struct cbd_ortho_plan_s {
   cbd_ortho_problem prob;
   std::vector<double> coefficients;   // steps x 3
   int64_t s, l, sp, lp;               // sides, and their padded lengths
-  int tile_sym, tile_step;
+  cbd::OrthoShare sym[2], step[2];    // how A and B, and X, are computed
   // Exponents of X before each step, of A and of B.
   std::vector<int> ex, ea, eb;
 };

@@ -33,7 +33,8 @@ class OrthoStrides(ctypes.Structure):
 
 
 class OrthoInfo(ctypes.Structure):
-    _fields_ = [("tile_symmetric", ctypes.c_int32), ("tile_step", ctypes.c_int32), ("launches", ctypes.c_int32),
+    _fields_ = [("tile_symmetric", ctypes.c_int32), ("tile_step", ctypes.c_int32),
+                ("tile_symmetric_rest", ctypes.c_int32), ("tile_step_rest", ctypes.c_int32), ("launches", ctypes.c_int32),
                 ("reserved", ctypes.c_int32), ("flops", ctypes.c_int64)]
 
 

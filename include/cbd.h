@@ -648,6 +648,7 @@ void cbd_ortho_plan_destroy(cbd_ortho_plan_t* plan); /* NULL is allowed */
 typedef struct {
   int32_t tile_symmetric; /* side of a workgroup's tile of A and B */
   int32_t tile_step;      /* and of X */
+  int32_t tile_symmetric_rest, tile_step_rest; /* of the last matrices; 0: the same */
   int32_t launches;       /* kernels per call */
   int32_t reserved;
   int64_t flops;          /* of the formula, with the symmetric products halved */

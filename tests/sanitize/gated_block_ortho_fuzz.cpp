@@ -117,6 +117,7 @@ int launch_block_finish(const BlockFinish& a, void*) {
 
 static const char *ws_begin, *ws_end;
 static int64_t count;  // matrices
+static int64_t done;   // of them, by the launches of the product so far
 // Extents of halves that have been written, as (begin, rows, halves of a row that hold values, ld, mat).
 struct Area {
   const uint16_t* p;
@@ -150,6 +151,7 @@ int launch_ortho_norm(const OrthoSplit& a, int64_t matrices, void*) {
   launches++;
   count = matrices;
   written.clear();
+  done = 0;
   expect((const char*)a.partial >= ws_begin && (const char*)(a.partial + matrices * kOrthoParts) <= ws_end, "norms");
   return 0;
 }
@@ -161,8 +163,16 @@ int launch_ortho_split(const OrthoSplit& a, int64_t matrices, void*) {
   wrote(a.xt, c, 2 * r, a.ldxt, a.xt_mat);
   return 0;
 }
-int launch_ortho_product(const OrthoArgs& a, int stage, int tile, int64_t matrices, void*) {
+int launch_ortho_product(const OrthoArgs& share, int stage, int tile, int64_t matrices, void*) {
   launches++;
+  expect(matrices >= 1 && done + matrices <= count, "matrices of a product");
+  // As if one launch did them all.
+  OrthoArgs a = share;
+  a.p -= done * a.p_mat;
+  a.q -= done * a.q_mat;
+  if (a.c) a.c -= done * a.c_mat;
+  if (a.ct) a.ct -= done * a.ct_mat;
+  done = done + matrices == count ? 0 : done + matrices;
   const bool sym = stage == ORTHO_SQUARE || stage == ORTHO_POLY;
   expect(tile == 64 || tile == 128 || tile == 256, "tile");
   expect((int64_t)a.tiles_m * a.tiles_n * matrices < (int64_t(1) << 24), "grid");

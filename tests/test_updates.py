@@ -123,11 +123,12 @@ def test_against_definition(dtype, size):
     near(call(m), m, dtype, str(size))
 
 
-# matrices, rows, cols; tiles of A and B, and of X.  128 also with more tiles than
+# matrices, rows, cols; tiles of A and B, and of X, where the last matrices have
+# others both.  128 also with more tiles than
 # compute units (two workgroups on one).
 TILES = [((300, 64, 96), 64, 64), ((9, 512, 768), 64, 128), ((9, 700, 1100), 128, 128), ((17, 1500, 500), 128, 256),
          ((1, 2047, 1990), 128, 128), ((14, 1030, 1900), 128, 128), ((7, 1000, 2040), 128, 256),
-         ((25, 1090, 1000), 256, 256)]
+         ((25, 1090, 1000), 256, 256), ((30, 1000, 1010), (256, 128), 256), ((32, 512, 1408), 64, (256, 128))]
 
 
 @pytest.mark.gpu
@@ -136,7 +137,8 @@ def test_every_tile(size, symmetric, step):
     """Sizes at which each tile is chosen, with edges inside tiles."""
     info = cbd.ortho_plan(*size).info()
     print("[ortho] tiles", size, info.tile_symmetric, info.tile_step, flush=True)
-    assert (info.tile_symmetric, info.tile_step) == (symmetric, step)
+    tiles = (info.tile_symmetric, info.tile_symmetric_rest), (info.tile_step, info.tile_step_rest)
+    assert tiles == tuple(t if isinstance(t, tuple) else (t, 0) for t in (symmetric, step))
     m = draw(*size, seed=size[1], rank=max(1, min(size[1:]) // 8))
     got = call(m, steps=3)
     some = [0, size[0] - 1] if size[0] > 1 else [0]
@@ -297,7 +299,8 @@ def test_run_refusals():
 
 def test_info():
     i = cbd.ortho_plan(8, 4096, 2048, steps=5).info()
-    assert (i.tile_symmetric, i.tile_step, i.launches) == (128, 256, 17)
+    assert (i.tile_symmetric, i.tile_symmetric_rest, i.tile_step, i.tile_step_rest) == (256, 128, 256, 0)
+    assert i.launches == 2 + 5 * 5 and cbd.ortho_plan(8, 64, 64, steps=2).info().launches == 2 + 2 * 3
     assert i.flops == 8 * 5 * (3 * 2048 * 2048 * 4096 + 2048 ** 3)
     assert cbd.ortho_plan(0, 16, 16).info().launches == 0
 
