@@ -15,10 +15,16 @@
 // A row stays in registers from its one load to its stores, 16 bytes a thread: a
 // workgroup (or, up to 64 threads a row, a part of one) takes rows i, i + grid,
 // ..., loads the next one before it joins the sums of this one, and keeps its
-// columns' sums in registers to the end.  z is rounded where it is stored, not where n is made
-// of it.
+// columns' sums in registers to the end, from where they go to memory, one row of
+// them a workgroup, for a second launch to join in a fixed order.  z is rounded
+// where it is stored, not where n is made of it.
 //
-// Bound: HBM.
+// Bound: HBM.  32768 x 4096 in bf16, vectors for all three: forward 212 us (5.1
+// TB/s; a copy on this card reaches 4.7), backward 302 (5.3) and 5 for the
+// joining; 65536 x 1024 94 and 165, 65536 x 128 13.4 and 20 (67 and 100 MB: the
+// caches hold a part); in f32 8192 x 2048 45 and 79.  With all sums through
+// LDS and the vectors held as f32, rows of 4096 took 393 us backward.  One row: 3
+// us, one round to memory and two sums over the waves.
 #include <type_traits>
 
 #include "block_internal.h"
@@ -27,6 +33,7 @@
 namespace cbd {
 namespace {
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x4_2 __attribute__((ext_vector_type(4), aligned(2)));
@@ -149,6 +156,13 @@ constexpr int kWaves = CH > 1 ? 1 : LANES < 64 ? 3 : 4;
 // The next row is loaded ahead; with more chunks a thread has no room for it.
 template <int CH>
 constexpr bool kAhead = CH == 1;
+// Backward, a thread with more than 8 elements a row has no room for what both
+// rounds over the row need, nor for its columns' sums: it reads its chunks again
+// in the second one, and keeps the sums in LDS (4096 rows of 10240 in
+// bf16 166 us, held, with spills, 484; of 16384 224 / 503; 2048 rows of 16384 in
+// f32 300 / 495; 4096 of 8192, which fit, 161 held and 211 read again).
+template <typename T, int CH>
+constexpr bool kHeld = CH * sizeof(u32x4) / sizeof(T) <= 8;
 
 // What a thread has of its rows: CH chunks, LANES chunks apart.
 template <typename T, int LANES, int CH>
@@ -166,29 +180,35 @@ struct Rows {
     row = (int64_t)blockIdx.x * per + sub;
     step = (int64_t)gridDim.x * per;
   }
+  __device__ inline void load(Chunk<T>& v, const void* p, int64_t at, int i) const {
+    v.load((const T*)p + at + N * (lane + LANES * i), n[i]);
+  }
   __device__ inline void load(Chunk<T> (&v)[CH], const void* p, int64_t at) const {
-    const T* q = (const T*)p + at + N * lane;
 #pragma unroll
-    for (int i = 0; i < CH; i++) v[i].load(q + N * LANES * i, n[i]);
+    for (int i = 0; i < CH; i++) load(v[i], p, at, i);
+  }
+  __device__ inline void store(const Chunk<T>& v, void* p, int64_t at, int i) const {
+    v.store((T*)p + at + N * (lane + LANES * i), n[i]);
   }
   __device__ inline void store(const Chunk<T> (&v)[CH], void* p, int64_t at) const {
-    T* q = (T*)p + at + N * lane;
 #pragma unroll
-    for (int i = 0; i < CH; i++) v[i].store(q + N * LANES * i, n[i]);
+    for (int i = 0; i < CH; i++) store(v[i], p, at, i);
   }
   __device__ inline static void zero(Chunk<T> (&v)[CH]) {
 #pragma unroll
     for (int i = 0; i < CH; i++) v[i].zero();
   }
   // A vector, or ones in its place: factors that change nothing.
-  __device__ inline void vector(Chunk<T> (&v)[CH], const void* p) const {
+  __device__ inline void vector(Chunk<T>& v, const void* p, int i) const {
     constexpr uint32_t one = sizeof(T) == 4 ? 0x3f800000u : 0x3f803f80u;
-    if (p) {
-      load(v, p, 0);
-    } else {
+    if (p)
+      load(v, p, 0, i);
+    else
+      v.v = u32x4{one, one, one, one};
+  }
+  __device__ inline void vector(Chunk<T> (&v)[CH], const void* p) const {
 #pragma unroll
-      for (int i = 0; i < CH; i++) v[i].v = u32x4{one, one, one, one};
-    }
+    for (int i = 0; i < CH; i++) vector(v[i], p, i);
   }
 };
 
@@ -299,47 +319,91 @@ __device__ inline void finish_column(const BlockFinish& a, int which, int col, d
 template <typename T, int LANES, int CH>
 __global__ __launch_bounds__(kThreads<LANES>, (kWaves<LANES, CH>)) void block_bwd_kernel(const BlockArgs a) {
   constexpr int N = Chunk<T>::N;
+  constexpr bool HELD = kHeld<T, CH>;
   __shared__ float part[2][3][RowSum<LANES, 3>::W];
   RowSum<LANES, 3> sum{part};
   Rows<T, LANES, CH> rows(a);
   Chunk<T> wq[CH], gq[CH], wp[CH];
-  rows.vector(wq, a.w_post);
-  rows.vector(gq, a.gate_rows ? nullptr : a.gate);
-  rows.vector(wp, a.w_pre);
-  float pre[CH][N], post[CH][N];  // the columns' sums
+  if (HELD) {
+    rows.vector(wq, a.w_post);
+    rows.vector(gq, a.gate_rows ? nullptr : a.gate);
+    rows.vector(wp, a.w_pre);
+  }
+  // The columns' sums.
+  __shared__ f32x4 sums[HELD ? 1 : 2 * CH * N / 4][HELD ? 1 : kThreads<LANES>];
+  float pre[CH][N], post[CH][N];
+  // Takes in (out of) registers what LDS has of chunk i.
+  auto take = [&](float (&v)[N], int at) {
 #pragma unroll
-  for (int i = 0; i < CH; i++)
+    for (int j = 0; j < N; j += 4) {
+      const f32x4 q = sums[at * (N / 4) + j / 4][threadIdx.x];
+#pragma unroll
+      for (int k = 0; k < 4; k++) v[j + k] = q[k];
+    }
+  };
+  auto leave = [&](const float (&v)[N], int at) {
+#pragma unroll
+    for (int j = 0; j < N; j += 4) sums[at * (N / 4) + j / 4][threadIdx.x] = f32x4{v[j], v[j + 1], v[j + 2], v[j + 3]};
+  };
+#pragma unroll
+  for (int i = 0; i < CH; i++) {
 #pragma unroll
     for (int j = 0; j < N; j++) pre[i][j] = post[i][j] = 0.f;
+    if (!HELD) {
+      leave(pre[i], i);
+      leave(post[i], CH + i);
+    }
+  }
   Chunk<T> r[CH], y[CH], g[CH], dz[CH], dn[CH];
   float ry1 = 1.f, rz1 = 1.f;
   Rows<T, LANES, CH>::zero(y);
   Rows<T, LANES, CH>::zero(dz);
   Rows<T, LANES, CH>::zero(dn);
-  auto fetch = [&](int64_t row) {
-    rows.load(r, a.r, row * a.ldr);
-    if (a.y) rows.load(y, a.y, row * a.ldy);
-    if (a.dz) rows.load(dz, a.dz, row * a.lddz);
-    if (a.dn) rows.load(dn, a.dn, row * a.lddn);
-    if (a.gate_rows) rows.load(g, a.gate, row * a.ldgate);
+  auto fetch = [&](int64_t row, int i) {
+    rows.load(r[i], a.r, row * a.ldr, i);
+    if (a.y) rows.load(y[i], a.y, row * a.ldy, i);
+    if (a.dz) rows.load(dz[i], a.dz, row * a.lddz, i);
+    if (a.dn) rows.load(dn[i], a.dn, row * a.lddn, i);
+    if (a.gate_rows) rows.load(g[i], a.gate, row * a.ldgate, i);
+  };
+  auto statistics = [&](int64_t row) {
     if (a.w_post) ry1 = a.stats[2 * row];
     if (a.w_pre) rz1 = a.stats[2 * row + 1];
   };
-  if (kAhead<CH> && rows.row < a.rows) fetch(rows.row);
+  auto fetch_all = [&](int64_t row) {
+#pragma unroll
+    for (int i = 0; i < CH; i++) fetch(row, i);
+    statistics(row);
+  };
+  if (kAhead<CH> && rows.row < a.rows) fetch_all(rows.row);
   const float inv_c = 1.f / (float)a.c;
   for (int64_t row = rows.row; row < a.rows; row += rows.step) {
-    if (!kAhead<CH>) fetch(row);
+    if (!HELD)
+      statistics(row);
+    else if (!kAhead<CH>)
+      fetch_all(row);
     const float ry = ry1, rz = rz1;
-    as_loaded(wq);
-    as_loaded(gq);
-    as_loaded(wp);
+    if (HELD) {
+      as_loaded(wq);
+      as_loaded(gq);
+      as_loaded(wp);
+    }
     float zn[CH][N], yn[CH][N], e[CH][N];
-    float s[3] = {0.f, 0.f, 0.f};
     Chunk<T> gr[CH];
-#pragma unroll
-    for (int i = 0; i < CH; i++) gr[i] = a.gate_rows ? g[i] : gq[i];
-#pragma unroll
-    for (int i = 0; i < CH; i++)
+    float s[3] = {0.f, 0.f, 0.f};
+    // Chunk i of zn, yn and e; in the first round over the row also the sums.
+    auto chunk = [&](int i, bool sums) {
+      if (!HELD) {
+        y[i].zero();
+        dz[i].zero();
+        dn[i].zero();
+        g[i].zero();
+        fetch(row, i);
+        rows.vector(wq[i], a.w_post, i);
+        rows.vector(gq[i], a.gate_rows ? nullptr : a.gate, i);
+        rows.vector(wp[i], a.w_pre, i);
+      }
+      gr[i] = a.gate_rows ? g[i] : gq[i];
 #pragma unroll
       for (int j = 0; j < N; j++) {
         const float d = dn[i].get(j);
@@ -348,18 +412,31 @@ __global__ __launch_bounds__(kThreads<LANES>, (kWaves<LANES, CH>)) void block_bw
         zn[i][j] = (r[i].get(j) + cy) * rz;
         const float v = d * wp[i].get(j);
         e[i][j] = __builtin_fmaf(rz, v, dz[i].get(j));
+        if (!sums) continue;
         pre[i][j] = __builtin_fmaf(d, zn[i][j], pre[i][j]);
         s[0] = __builtin_fmaf(v, zn[i][j], s[0]);
         s[1] = __builtin_fmaf(cy, e[i][j], s[1]);
         s[2] = __builtin_fmaf(cy, zn[i][j], s[2]);
       }
-    if (kAhead<CH> && row + rows.step < a.rows) fetch(row + rows.step);
-    sum(s);
-    const float along = rz * s[0] * inv_c;           // of zn in dz'
-    const float back = (s[1] - along * s[2]) * inv_c;  // of yn in dy
-    Chunk<T> o_r[CH], o_y[CH], o_g[CH];
+    };
 #pragma unroll
     for (int i = 0; i < CH; i++) {
+      if (!HELD) take(pre[i], i);
+      chunk(i, true);
+      if (!HELD) leave(pre[i], i);
+      if (!HELD) __builtin_amdgcn_sched_barrier(0);
+    }
+    if (kAhead<CH> && row + rows.step < a.rows) fetch_all(row + rows.step);
+    sum(s);
+    const float along = rz * s[0] * inv_c;             // of zn in dz'
+    const float back = (s[1] - along * s[2]) * inv_c;  // of yn in dy
+#pragma unroll
+    for (int i = 0; i < CH; i++) {
+      if (!HELD) {
+        chunk(i, false);
+        take(post[i], CH + i);
+      }
+      Chunk<T> o_r, o_y, o_g;
       float fr[N], fy[N], fg[N];
 #pragma unroll
       for (int j = 0; j < N; j++) {
@@ -370,13 +447,15 @@ __global__ __launch_bounds__(kThreads<LANES>, (kWaves<LANES, CH>)) void block_bw
         post[i][j] = __builtin_fmaf(a.gate_rows ? dg : da, yn[i][j], post[i][j]);
         fy[j] = a.w_post ? ry * __builtin_fmaf(-back, yn[i][j], dg * w) : dg;
       }
-      o_r[i].put(fr);
-      o_y[i].put(fy);
-      o_g[i].put(fg);
+      if (!HELD) leave(post[i], CH + i);
+      o_r.put(fr);
+      o_y.put(fy);
+      o_g.put(fg);
+      if (a.dr) rows.store(o_r, a.dr, row * a.lddr, i);
+      if (a.dy) rows.store(o_y, a.dy, row * a.lddy, i);
+      if (a.dgate) rows.store(o_g, a.dgate, row * a.lddgate, i);
+      if (!HELD) __builtin_amdgcn_sched_barrier(0);
     }
-    if (a.dr) rows.store(o_r, a.dr, row * a.lddr);
-    if (a.dy) rows.store(o_y, a.dy, row * a.lddy);
-    if (a.dgate) rows.store(o_g, a.dgate, row * a.lddgate);
   }
   const bool alone = gridDim.x == 1;  // no one to join
   if (!a.partial) return;
@@ -410,6 +489,10 @@ __global__ __launch_bounds__(kThreads<LANES>, (kWaves<LANES, CH>)) void block_bw
 #pragma unroll
   for (int i = 0; i < CH; i++) {
     const int at = N * (rows.lane + LANES * i);
+    if (!HELD) {
+      take(pre[i], i);
+      take(post[i], CH + i);
+    }
 #pragma unroll
     for (int j = 0; j < N; j++)
       if (at + j < a.c) {

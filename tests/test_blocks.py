@@ -289,6 +289,24 @@ def test_in_place_is_the_same():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,c", [("bf16", 8200), ("bf16", 12301), ("f32", 8190), ("f32", 8196), ("f32", 13001)])
+def test_wide_rows(dtype, c):
+    """More rows than workgroups, of widths that a thread reads twice; in place too."""
+    for gate in ("row", "channel"):
+        print("[block]", dtype, c, gate, flush=True)
+        b = Block(300, c, dtype=dtype, gate=gate)
+        b.check()
+        d = b.device()
+        args = (d["w_post"], d["gate"], d["w_pre"])
+        dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+        z, n, stats = cbd.block_forward(b.plan, d["r"], d["y"], *args, save=True)
+        dz, dn = b.dz.to(dt).cuda(), b.dn.to(dt).cuda()
+        want = cbd.block_bwd(b.plan, dz, dn, d["r"], d["y"], stats, *args)
+        got = cbd.block_bwd(b.plan, dz, dn, d["r"], d["y"], stats, *args, dr=dz, dy=dn)
+        assert got[0] is dz and got[1] is dn and all(torch.equal(u, v) for u, v in zip(got, want))
+
+
+@pytest.mark.gpu
 def test_masks_and_empty():
     b = Block(17, 80, gate="row")
     whole = b.bwd()
