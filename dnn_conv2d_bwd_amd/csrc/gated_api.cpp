@@ -40,7 +40,10 @@ ExpertLaunch choose(const cbd_expert_plan_s& plan, bool bwd, bool narrow_strides
     return (m + bm - 1) / bm * (p.tokens / bn + spans);
   };
   l.kernel = plan.opt.force_kernel;
-  // Few rows an expert, as for the expert products.
+  // Few rows an expert: 64 experts of 2048 inputs and 2 x 1408 outputs, stream /
+  // mfma in us at 8, 16, 20 and 32 rows an expert 142 / 168, 169 / 171, 186 / 172
+  // and 235 / 175 (AK), 128 / 131, 133 / 134, 140 / 136 and 158 / 141 (AM; alike up
+  // to 24, as for the expert products).
   const int stream_bm = (l.form == cbd::EXPERT_AK ? 32 : 128) / 2;
   const bool stream_ok = !bwd && narrow_strides && grid(stream_bm, 32) <= kMaxGrid;
   if (l.kernel == CBD_EXPERT_KERNEL_AUTO)
@@ -60,14 +63,21 @@ ExpertLaunch choose(const cbd_expert_plan_s& plan, bool bwd, bool narrow_strides
   if (l.kernel == CBD_EXPERT_KERNEL_MFMA) {
     l.dma = dma && n % 8 == 0;
     // 256 x 256 tiles by the rule of the expert products, whose features these
-    // `parts * m` are.
+    // `parts * m` are (256 / 128 in us, forward: 64 experts of 2048 inputs and 2 x
+    // 1408 outputs at 160 rows an expert 232 / 213, 192 228 / 234, 256 259 / 292,
+    // 384 340 / 389, 32 of 2048 and 2 x 1024 at 256 rows 104 / 107; backward, 1408
+    // features, whose last tile of 256 is half used, at 256 rows 205 / 184, 384
+    // 242 / 238).
     const bool half = (parts * m + 127) / 128 % 2 != 0;
     const bool many = p.tokens >= (half ? 384 : 192) * p.experts;
     tile = l.dma && whole_out && many && grid(256 / parts, 256) >= 512 ? 256 : 128;
   } else {
-    auto covered = [&](int64_t b) { return (parts * m + b - 1) / b * b; };
-    const bool small = grid(128 / parts, 128) < 512 || covered(128) * 10 > covered(64) * 11;
-    tile = small && grid(64 / parts, 64) <= kMaxGrid ? 64 : 128;
+    // 64 x 64 (of the expert products' two tiles: 64 / 128 in us, f32, 4 experts,
+    // 16384 rows, 2048 inputs, 2 x 2048 outputs 2565 / 2465 and backward 1355 /
+    // 1338; 8192 rows, 2 x 1024 743 / 738 and 420 / 462; 8 experts, 4096 rows, 1024
+    // inputs, 2 x 1024 186 / 214 and 114 / 157; 64 experts, 8192 rows, 2 x 704 278 /
+    // 368 and 169 / 234).
+    tile = 64;
   }
   l.bm = (int32_t)(tile / parts);
   l.bn = (int32_t)tile;
