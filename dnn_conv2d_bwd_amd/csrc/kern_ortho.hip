@@ -12,12 +12,30 @@
 // most and the smallest ones' lo out of the subnormals.
 //
 // A and B are symmetric: only tiles on and above the diagonal are computed, and
-// each is stored twice.
+// each is stored twice.  Where A has few of them, workgroups take slices of its
+// long side, whose f32 sums a small launch joins.
 //
 // A workgroup of 4 waves (2 x 2) computes a tile of 64 MB x 64 MB in runs of 32
-// k: 128 bytes of a row, hi and lo, go straight to one of two LDS stages
+// k: 128 bytes of a row, hi and lo, go straight to one of NS LDS stages
 // (buffer_load ... lds), in chunks of 16 bytes, chunk c of row r at c ^ (r / 2 %
 // 8), so that reads of 32 rows spread over the banks.
+//
+// Bound: large matrices by the matrix instructions, at the rate that the card's
+// power allows.  8 x 4096 x 2048, a step: A 303 + 76 us (7 matrices in tiles of
+// 256, one in tiles of 128 for the units that those leave idle), B 174 + 48, X 655
+// (1.26 PFLOP/s of halves; a library product of 8192 x 8192 x 8192 in bf16 reaches
+// 1.26), the last 607 (1.36: it writes a quarter of the bytes); the five with norm
+// 31 us (4.3 TB/s) and split 140 (4.2 TB/s, two directions of 4 bytes written)
+// 6.3 - 6.6 ms.  Results leave through LDS in whole columns of blocks: 0.3 ms less
+// than block by block.  Small ones by latency: 16 x 256 x 512 takes 7 to 11 us a
+// launch for 8 to 16 runs.
+//
+// Stages: one workgroup of 64 x 64 a compute unit waits for every load and LDS
+// read, so four runs are in flight and one in registers (5 / 3 / 2 stages: A of
+// 1024 x 1024 12 / 26 / 25 us, of 2048 x 2048 in larger tiles alike); tiles of 128
+// likewise while there is one a unit (4 / 2 stages: 136 tiles of 64 runs 46 / 62
+// us), two a unit hide each other's ways (363 tiles of 44 runs 74 / 55); tiles of
+// 256 have LDS for two stages, and 96 products a run to hide their loads.
 #include <type_traits>
 
 #include "cbd_device.h"
@@ -67,41 +85,46 @@ __device__ inline void barrier() {
   asm volatile("" ::: "memory");
 }
 
+// Tile (mt, nt), n >= m, of a symmetric matrix of n x n tiles: groups of W columns,
+// in each row by row; neighbours, which one XCD has, share both operands.
+__device__ inline void upper_tile(int local, int n, int W, int& mt, int& nt) {
+  int c0 = 0, w = n < W ? n : W;
+  while (local >= c0 * w + w * (w + 1) / 2) {
+    local -= c0 * w + w * (w + 1) / 2;
+    c0 += w;
+    w = n - c0 < W ? n - c0 : W;
+  }
+  if (local < c0 * w) {
+    mt = local / w;
+    nt = c0 + local - mt * w;
+  } else {
+    local -= c0 * w;
+    int r = 0;
+    for (; local >= w - r; r++) local -= w - r;
+    mt = c0 + r;
+    nt = mt + local;
+  }
+}
+
 template <int MB, int STAGE, int NS>
 __global__ __launch_bounds__(THREADS, MB == 4 || (MB == 2 && NS > 2) ? 1 : 2) void ortho_product_kernel(const OrthoArgs a) {
   constexpr int T = 64 * MB;
   constexpr int BYTES = T * 128;      // of an operand's stage
   constexpr int N = BYTES / 4096;     // 1 KiB blocks of it that a wave fills
-  constexpr bool SYM = STAGE == ORTHO_SQUARE || STAGE == ORTHO_POLY;
+  constexpr bool SLICE = STAGE == ORTHO_SLICE, SYM = STAGE == ORTHO_SQUARE || STAGE == ORTHO_POLY || SLICE;
   __shared__ __attribute__((aligned(1024))) char smem[2 * NS * BYTES];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave & 1, wn = wave >> 1;
 
   // The matrix and the tile.
   const int per = SYM ? a.tiles_m * (a.tiles_m + 1) / 2 : a.tiles_m * a.tiles_n;
-  const int t = dev::logical_tile((int)blockIdx.x, (int)gridDim.x, 1);
+  const int block = dev::logical_tile((int)blockIdx.x, (int)gridDim.x, 1), t = SLICE ? block / a.slices : block;
+  const int run0 = SLICE ? __builtin_amdgcn_readfirstlane((block - t * a.slices) * a.slice) : 0;
+  const int runs = SLICE && a.runs - run0 > a.slice ? a.slice : a.runs - run0;
   const int mat = __builtin_amdgcn_readfirstlane(t / per);
   int local = __builtin_amdgcn_readfirstlane(t - mat * per), mt, nt;
   if (SYM) {
-    // Groups of W columns; in each, row by row: neighbours, which one XCD has,
-    // share both operands.
-    const int W = gridDim.x <= 256 ? 4 : 8;
-    int c0 = 0, w = a.tiles_n < W ? a.tiles_n : W;
-    while (local >= c0 * w + w * (w + 1) / 2) {
-      local -= c0 * w + w * (w + 1) / 2;
-      c0 += w;
-      w = a.tiles_n - c0 < W ? a.tiles_n - c0 : W;
-    }
-    if (local < c0 * w) {
-      mt = local / w;
-      nt = c0 + local - mt * w;
-    } else {
-      local -= c0 * w;
-      int r = 0;
-      for (; local >= w - r; r++) local -= w - r;
-      mt = c0 + r;
-      nt = mt + local;
-    }
+    upper_tile(local, a.tiles_n, gridDim.x <= 256 ? 4 : 8, mt, nt);
   } else {
     // Groups of 8 rows of tiles by all columns.
     const int g = local / (8 * a.tiles_n), in = local - g * 8 * a.tiles_n;
@@ -134,8 +157,8 @@ __global__ __launch_bounds__(THREADS, MB == 4 || (MB == 2 && NS > 2) ? 1 : 2) vo
   }
 
   // Loads: row lane / 8 of every 8, chunk lane % 8 in LDS.
-  uint64_t bp = (uint64_t)(a.p + mat * a.p_mat + (int64_t)mt * T * a.ldp);
-  uint64_t bq = (uint64_t)(a.q + mat * a.q_mat + (int64_t)nt * T * a.ldq);
+  uint64_t bp = (uint64_t)(a.p + mat * a.p_mat + (int64_t)mt * T * a.ldp + run0 * 64);
+  uint64_t bq = (uint64_t)(a.q + mat * a.q_mat + (int64_t)nt * T * a.ldq + run0 * 64);
   uint32_t vp[N], vq[N];
 #pragma unroll
   for (int i = 0; i < N; i++) {
@@ -156,10 +179,10 @@ __global__ __launch_bounds__(THREADS, MB == 4 || (MB == 2 && NS > 2) ? 1 : 2) vo
   // Run k of an operand into stage s; past the last there is nothing to load
   // (a record count of 0 gives zeros), but the count of loads stays.
   auto load_p = [&](int k, int s, int i) INLINE {
-    issue(bp, k < a.runs ? rec_p : 0u, vp[i], (uint32_t)k * 128u, base + (uint32_t)(2 * s * BYTES + i * 1024));
+    issue(bp, k < runs ? rec_p : 0u, vp[i], (uint32_t)k * 128u, base + (uint32_t)(2 * s * BYTES + i * 1024));
   };
   auto load_q = [&](int k, int s, int i) INLINE {
-    issue(bq, k < a.runs ? rec_q : 0u, vq[i], (uint32_t)k * 128u, base + (uint32_t)((2 * s + 1) * BYTES + i * 1024));
+    issue(bq, k < runs ? rec_q : 0u, vq[i], (uint32_t)k * 128u, base + (uint32_t)((2 * s + 1) * BYTES + i * 1024));
   };
 
   // Fragments: 32 rows by 16 k; half h (0: hi, 1: lo) of k 16 ks ...
@@ -276,9 +299,9 @@ __global__ __launch_bounds__(THREADS, MB == 4 || (MB == 2 && NS > 2) ? 1 : 2) vo
     read(0, p[0], q[0]);
     run(0, p[0], q[0], p[1], q[1], std::true_type());
 #pragma unroll 1
-    for (int k = 1; k < a.runs; k += 2) {
+    for (int k = 1; k < runs; k += 2) {
       run(k, p[1], q[1], p[0], q[0], std::false_type());
-      if (k + 1 < a.runs) run(k + 1, p[0], q[0], p[1], q[1], std::false_type());
+      if (k + 1 < runs) run(k + 1, p[0], q[0], p[1], q[1], std::false_type());
     }
   } else {
     f16x8 ph0[MB], ph1[MB], pl[MB], qh0[MB], qh1[MB], ql[MB];
@@ -320,9 +343,9 @@ __global__ __launch_bounds__(THREADS, MB == 4 || (MB == 2 && NS > 2) ? 1 : 2) vo
     };
     run(0, std::integral_constant<int, 0>(), std::true_type());
 #pragma unroll 1
-    for (int k = 1; k < a.runs; k += NS) {
+    for (int k = 1; k < runs; k += NS) {
       run(k, std::integral_constant<int, 1>(), std::false_type());
-      if (k + NS - 1 < a.runs) run(k + NS - 1, std::integral_constant<int, 0>(), std::false_type());
+      if (k + NS - 1 < runs) run(k + NS - 1, std::integral_constant<int, 0>(), std::false_type());
     }
   }
   // The last loads (zeros) have landed, and everyone has read the stages.
@@ -359,7 +382,12 @@ __global__ __launch_bounds__(THREADS, MB == 4 || (MB == 2 && NS > 2) ? 1 : 2) vo
           }
         }
       }
-      if constexpr (STAGE == ORTHO_LAST) {
+      if constexpr (SLICE) {
+        float* const o = a.sums + (int64_t)block * (T * T) + (32 * MB * wn + 32 * n + r) * T + 32 * MB * wm + 32 * m;
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+          *(f32x4*)(o + 8 * q + 4 * upper) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+      } else if constexpr (STAGE == ORTHO_LAST) {
         // A row of the output at a time, four elements a lane: 32 x 32 in f32, chunk
         // c of row i at c ^ (i % 8).
         float* const f = (float*)st;
@@ -422,7 +450,7 @@ __global__ __launch_bounds__(THREADS, MB == 4 || (MB == 2 && NS > 2) ? 1 : 2) vo
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    if constexpr (STAGE != ORTHO_LAST) {
+    if constexpr (STAGE != ORTHO_LAST && !SLICE) {
       // A column of blocks leaves: eight elements a lane, their hi and their lo.
       asm volatile("" ::: "memory");  // a wave's LDS accesses run in order
       auto leave = [&](const uint32_t (&w)[8], uint16_t* o) INLINE {
@@ -460,6 +488,37 @@ __global__ __launch_bounds__(THREADS, MB == 4 || (MB == 2 && NS > 2) ? 1 : 2) vo
       __builtin_amdgcn_sched_barrier(0);
     }
   }
+}
+
+// A block of 32 x 32 of A: its slices' sums, added in their order, in both directions.
+__global__ __launch_bounds__(THREADS) void ortho_join_kernel(const OrthoArgs a) {
+  __shared__ uint32_t block[32][33];
+  const int t = blockIdx.x >> 2, per = a.tiles_n * (a.tiles_n + 1) / 2, mat = t / per;
+  const int hm = blockIdx.x & 1, hn = blockIdx.x >> 1 & 1, i = threadIdx.x >> 3, e = 4 * (threadIdx.x & 7);
+  int mt, nt;
+  upper_tile(t - mat * per, a.tiles_n, 4, mt, nt);
+  const float* const p = a.sums + (int64_t)t * a.slices * 4096 + (32 * hn + i) * 64 + 32 * hm + e;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int s = 0; s < a.slices; s++) v += *(const f32x4*)(p + (int64_t)s * 4096);
+  const int row0 = 64 * mt + 32 * hm, col0 = 64 * nt + 32 * hn;
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    w[j] = row0 + e + j < a.rows && col0 + i < a.cols ? split(v[j] * a.mul) : 0u;
+    block[i][e + j] = w[j];
+  }
+  auto leave = [&](uint16_t* o) INLINE {
+    *(u32x2*)o = u32x2{__builtin_amdgcn_perm(w[1], w[0], 0x05040100u), __builtin_amdgcn_perm(w[3], w[2], 0x05040100u)};
+    *(u32x2*)(o + 32) =
+        u32x2{__builtin_amdgcn_perm(w[1], w[0], 0x07060302u), __builtin_amdgcn_perm(w[3], w[2], 0x07060302u)};
+  };
+  leave(a.ct + mat * a.ct_mat + (int64_t)(col0 + i) * a.ldct + (row0 >> 5) * 64 + e);
+  if (mt == nt) return;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 4; j++) w[j] = block[e + j][i];
+  leave(a.c + mat * a.c_mat + (int64_t)(row0 + i) * a.ldc + (col0 >> 5) * 64 + e);
 }
 
 // ---- the input: norm, then both directions as two halves a value
@@ -577,11 +636,19 @@ int launch_ortho_split(const OrthoSplit& a, int64_t matrices, void* stream) {
   return (int)hipLaunchKernel(k, dim3((unsigned)((a.cols + 63) / 64), (unsigned)((a.rows + 63) / 64), (unsigned)matrices),
                               dim3(THREADS), args, 0, (hipStream_t)stream);
 }
+int launch_ortho_join(const OrthoArgs& a, int64_t matrices, void* stream) {
+  void* args[] = {const_cast<OrthoArgs*>(&a)};
+  const int64_t tiles = (int64_t)a.tiles_n * (a.tiles_n + 1) / 2 * matrices;
+  return (int)hipLaunchKernel((const void*)&ortho_join_kernel, dim3((unsigned)(4 * tiles)), dim3(THREADS), args, 0,
+                              (hipStream_t)stream);
+}
 int launch_ortho_product(const OrthoArgs& a, int stage, int tile, int64_t matrices, void* stream) {
   void* args[] = {const_cast<OrthoArgs*>(&a)};
-  const bool sym = stage == ORTHO_SQUARE || stage == ORTHO_POLY;
-  const int64_t per = sym ? (int64_t)a.tiles_m * (a.tiles_m + 1) / 2 : (int64_t)a.tiles_m * a.tiles_n;
-  const void* k = stage == ORTHO_SQUARE ? pick<ORTHO_SQUARE>(tile, per * matrices)
+  const bool sym = stage == ORTHO_SQUARE || stage == ORTHO_POLY || stage == ORTHO_SLICE;
+  const int64_t per = stage == ORTHO_SLICE ? (int64_t)a.tiles_m * (a.tiles_m + 1) / 2 * a.slices
+                      : sym                ? (int64_t)a.tiles_m * (a.tiles_m + 1) / 2 : (int64_t)a.tiles_m * a.tiles_n;
+  const void* k = stage == ORTHO_SLICE ? (const void*)&ortho_product_kernel<1, ORTHO_SLICE, 5>
+                  : stage == ORTHO_SQUARE ? pick<ORTHO_SQUARE>(tile, per * matrices)
                   : stage == ORTHO_POLY ? pick<ORTHO_POLY>(tile, per * matrices)
                   : stage == ORTHO_STEP ? pick<ORTHO_STEP>(tile, per * matrices)
                                         : pick<ORTHO_LAST>(tile, per * matrices);

@@ -40,6 +40,7 @@ struct Tile {
 // 1024 x 2048.
 constexpr Tile kTiles[] = {{256, 2.4, 4.8}, {128, 0.58, 1.38}, {64, 0.22, 0.5}};
 constexpr double kLaunch = 4.0;  // us of another launch
+constexpr double kJoin = 6.0;    // and of one that joins slices' sums
 
 double time_of(const Tile& c, int64_t tiles) {
   const int64_t rest = tiles % 512;
@@ -138,6 +139,19 @@ cbd_status make_plan(const cbd_ortho_problem* q, cbd_ortho_plan_t** out) {
   auto step = [&](int64_t t) { return ((p->s + t - 1) / t) * ((p->l + t - 1) / t); };
   share_out(n, runs, sym, p->sym);
   share_out(n, runs, step, p->step);
+  // A's sums in slices of its contracted side, of 8 runs at least, where its tiles
+  // leave most of the card idle and take longer than a launch that joins them (5
+  // steps in us, whole / in slices: 256 x 4096, 16 of them, 232 / 138; 64 x 16384
+  // 591 / 126; 8 matrices of 64 x 4096 220 / 125; 768 x 2304, 3 slices, 230 / 202;
+  // 4 of 256 x 1536 159 / 149).
+  p->slices = 1;
+  if (p->sym[0].tile == 64 && !p->sym[1].count) {
+    const int64_t all = (p->l + 31) / 32, most = std::min(256 / (n * sym(64)), all / 8);
+    if (most > 1 && (double)(all - (all + most - 1) / most) * kTiles[2].one > kJoin) {
+      p->slice = (all + most - 1) / most;
+      p->slices = (all + p->slice - 1) / p->slice;
+    }
+  }
   int64_t pad = 64;
   for (const auto* shares : {p->sym, p->step})
     for (int i = 0; i < 2; i++) {
@@ -156,13 +170,15 @@ cbd_status make_plan(const cbd_ortho_problem* q, cbd_ortho_plan_t** out) {
 // Halves of a matrix in each of the workspace's arrays, and the whole.
 struct Layout {
   int64_t x, a;               // halves of X (either direction) and of A or B
-  uint64_t parts, bytes;
+  uint64_t parts, sums, bytes;
   explicit Layout(const cbd_ortho_plan_s& p) {
     const uint64_t n = (uint64_t)p.prob.matrices;
     x = 2 * p.sp * p.lp;
     a = 2 * p.sp * p.sp;
     parts = (n * cbd::kOrthoParts * sizeof(double) + 255) / 256 * 256;
-    bytes = parts + n * 2 * (3 * (uint64_t)x + 2 * (uint64_t)a) + 256;
+    const uint64_t side = (uint64_t)(p.s + 63) / 64, blocks = n * (side * (side + 1) / 2) * (uint64_t)p.slices;
+    sums = p.slices > 1 ? blocks * 64 * 64 * sizeof(float) : 0;
+    bytes = parts + sums + n * 2 * (3 * (uint64_t)x + 2 * (uint64_t)a) + 256;
   }
 };
 
@@ -205,7 +221,8 @@ cbd_status run(const cbd_ortho_plan_t* plan, const void* in, void* out, const cb
   const bool tall = q.rows > q.cols;
   const int64_t n = q.matrices;
   double* const partial = (double*)ws;
-  uint16_t* const x = (uint16_t*)((char*)ws + lay.parts);  // rows: the smaller side
+  float* const sums = (float*)((char*)ws + lay.parts);
+  uint16_t* const x = (uint16_t*)((char*)sums + lay.sums);  // rows: the smaller side
   uint16_t* xt = x + n * lay.x;                            // rows: the larger one
   uint16_t* xt_next = xt + n * lay.x;
   uint16_t* const sq = xt_next + n * lay.x;                // A
@@ -261,7 +278,19 @@ cbd_status run(const cbd_ortho_plan_t* plan, const void* in, void* out, const cb
     a.c_mat = a.ct_mat = lay.a;
     a.ldc = a.ldct = ldxt;
     a.mul = (float)std::ldexp(1.0, ea - 2 * ex);
-    product(a, cbd::ORTHO_SQUARE, plan->sym);
+    if (plan->slices > 1) {
+      a.sums = sums;
+      a.slices = (int32_t)plan->slices;
+      a.slice = (int32_t)plan->slice;
+      const float mul = a.mul;
+      a.mul = 1.f;  // with the joining
+      product(a, cbd::ORTHO_SLICE, plan->sym);
+      a.mul = mul;
+      a.tiles_m = a.tiles_n = tiles(plan->s, 64);
+      if (!err) err = cbd::launch_ortho_join(a, n, stream);
+    } else {
+      product(a, cbd::ORTHO_SQUARE, plan->sym);
+    }
 
     a.p = a.q = sq;
     a.p_mat = a.q_mat = lay.a;
@@ -327,8 +356,8 @@ extern "C" cbd_status cbd_ortho_plan_info(const cbd_ortho_plan_t* plan, cbd_orth
     out->tile_step = plan->step[0].tile;
     out->tile_symmetric_rest = plan->sym[1].count ? plan->sym[1].tile : 0;
     out->tile_step_rest = plan->step[1].count ? plan->step[1].tile : 0;
-    out->launches = plan->prob.matrices ? 2 + plan->prob.steps * (2 * sym + step) : 0;
-    out->reserved = 0;
+    out->launches = plan->prob.matrices ? 2 + plan->prob.steps * (2 * sym + step + (plan->slices > 1)) : 0;
+    out->slices = (int32_t)plan->slices;
     out->flops = plan->prob.matrices * plan->prob.steps * plan->s * plan->s * (3 * plan->l + plan->s);
     cbd::set_error("");
     return CBD_OK;

@@ -21,7 +21,8 @@ enum OrthoStage {
   ORTHO_SQUARE = 0,  // A = X X^T
   ORTHO_POLY = 1,    // B = a I + b A + c A A
   ORTHO_STEP = 2,    // X = B X, in both directions
-  ORTHO_LAST = 3     // the same, to the output
+  ORTHO_LAST = 3,    // the same, to the output
+  ORTHO_SLICE = 4    // sums of slices of A's contracted side, for launch_ortho_join
 };
 
 struct OrthoArgs {
@@ -39,6 +40,8 @@ struct OrthoArgs {
   void* out;                 // ORTHO_LAST
   int64_t out_row, out_mat;
   int32_t out_dtype, flip;   // flip: the output is C^T
+  float* sums;               // ORTHO_SLICE: [matrix][tile][slice] tiles of 64 columns of 64
+  int32_t slices, slice;     // how many, and runs of each but the last
 };
 
 struct OrthoSplit {
@@ -62,6 +65,8 @@ struct OrthoShare {
 
 int launch_ortho_norm(const OrthoSplit& a, int64_t matrices, void* stream);
 int launch_ortho_split(const OrthoSplit& a, int64_t matrices, void* stream);
+// A from the sums of its slices, which are added in their order.
+int launch_ortho_join(const OrthoArgs& a, int64_t matrices, void* stream);
 int launch_ortho_product(const OrthoArgs& a, int stage, int tile, int64_t matrices, void* stream);
 
 }  // namespace cbd
@@ -71,6 +76,7 @@ struct cbd_ortho_plan_s {
   std::vector<double> coefficients;   // steps x 3
   int64_t s, l, sp, lp;               // sides, and their padded lengths
   cbd::OrthoShare sym[2], step[2];    // how A and B, and X, are computed
+  int64_t slices, slice;              // of A's sums, in runs; slices is 1 where they are not split
   // Exponents of X before each step, of A and of B.
   std::vector<int> ex, ea, eb;
 };

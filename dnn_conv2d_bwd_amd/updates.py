@@ -35,7 +35,7 @@ class OrthoStrides(ctypes.Structure):
 class OrthoInfo(ctypes.Structure):
     _fields_ = [("tile_symmetric", ctypes.c_int32), ("tile_step", ctypes.c_int32),
                 ("tile_symmetric_rest", ctypes.c_int32), ("tile_step_rest", ctypes.c_int32), ("launches", ctypes.c_int32),
-                ("reserved", ctypes.c_int32), ("flops", ctypes.c_int64)]
+                ("slices", ctypes.c_int32), ("flops", ctypes.c_int64)]
 
 
 def _bind():

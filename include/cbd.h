@@ -650,7 +650,7 @@ typedef struct {
   int32_t tile_step;      /* and of X */
   int32_t tile_symmetric_rest, tile_step_rest; /* of the last matrices; 0: the same */
   int32_t launches;       /* kernels per call */
-  int32_t reserved;
+  int32_t slices;         /* of A's sums, which a launch of its own joins; 1: not split */
   int64_t flops;          /* of the formula, with the symmetric products halved */
 } cbd_ortho_info_t;
 

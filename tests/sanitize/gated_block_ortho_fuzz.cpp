@@ -117,6 +117,7 @@ int launch_block_finish(const BlockFinish& a, void*) {
 
 static const char *ws_begin, *ws_end;
 static int64_t count;  // matrices
+static const float* sliced;  // sums that wait to be joined
 static int64_t done;   // of them, by the launches of the product so far
 // Extents of halves that have been written, as (begin, rows, halves of a row that hold values, ld, mat).
 struct Area {
@@ -173,7 +174,7 @@ int launch_ortho_product(const OrthoArgs& share, int stage, int tile, int64_t ma
   if (a.c) a.c -= done * a.c_mat;
   if (a.ct) a.ct -= done * a.ct_mat;
   done = done + matrices == count ? 0 : done + matrices;
-  const bool sym = stage == ORTHO_SQUARE || stage == ORTHO_POLY;
+  const bool sym = stage == ORTHO_SQUARE || stage == ORTHO_POLY || stage == ORTHO_SLICE;
   expect(tile == 64 || tile == 128 || tile == 256, "tile");
   expect((int64_t)a.tiles_m * a.tiles_n * matrices < (int64_t(1) << 24), "grid");
   expect(a.tiles_m == (a.rows + tile - 1) / tile && a.tiles_n == (a.cols + tile - 1) / tile, "tiles");
@@ -182,6 +183,17 @@ int launch_ortho_product(const OrthoArgs& share, int stage, int tile, int64_t ma
   read(a.p, a.rows, (int64_t)tile * a.tiles_m, 64 * a.runs, a.ldp, a.p_mat);
   read(a.q, a.cols, (int64_t)tile * a.tiles_n, 64 * a.runs, a.ldq, a.q_mat);
   const int64_t m = (int64_t)tile * a.tiles_m, n = (int64_t)tile * a.tiles_n;
+  if (stage == ORTHO_SLICE) {
+    const char* const b = (const char*)a.sums;
+    const int64_t tiles = a.tiles_m * (a.tiles_m + 1) / 2 * count;
+    expect(tile == 64 && matrices == count && tiles * a.slices <= 256, "slices in one round");
+    expect(a.slices >= 2 && a.slice * (a.slices - 1) < a.runs && a.runs <= a.slice * a.slices, "every run in one slice");
+    expect(b >= ws_begin && ((uintptr_t)b & 15) == 0 && b + tiles * a.slices * 64 * 64 * 4 <= ws_end, "sums");
+    for (const Area& w : written)
+      expect(b + tiles * a.slices * 64 * 64 * 4 <= (const char*)w.p || (const char*)(w.p + count * w.mat) <= b, "sums over a matrix");
+    sliced = a.sums;
+    return 0;
+  }
   if (stage == ORTHO_POLY) inside(a.p, (m - 1) * a.ldp + 2 * n, a.p_mat, "A outside the workspace");
   if (stage == ORTHO_LAST) {
     expect(a.out && a.out_row >= (a.flip ? a.rows : a.cols), "output");
@@ -191,6 +203,14 @@ int launch_ortho_product(const OrthoArgs& share, int stage, int tile, int64_t ma
   wrote(a.c, m, 2 * n, a.ldc, a.c_mat);
   wrote(a.ct, n, 2 * m, a.ldct, a.ct_mat);
   expect(!sym || (a.c == a.ct && a.ldc == a.ldct && a.rows == a.cols), "symmetric");
+  return 0;
+}
+int launch_ortho_join(const OrthoArgs& a, int64_t matrices, void*) {
+  launches++;
+  expect(a.sums && a.sums == sliced && matrices == count && a.tiles_m == (a.rows + 63) / 64 && a.tiles_n == a.tiles_m, "joining");
+  expect(a.c == a.ct && a.ldc == a.ldct && a.rows == a.cols && a.c != a.p, "symmetric");
+  sliced = nullptr;
+  wrote(a.c, 64 * a.tiles_m, 2 * 64 * a.tiles_n, a.ldc, a.c_mat);
   return 0;
 }
 }  // namespace cbd

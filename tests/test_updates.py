@@ -145,6 +145,21 @@ def test_every_tile(size, symmetric, step):
     near(got[some], m[some], "f32", str(size), steps=3)
 
 
+# A few tiles of A and a long contracted side, whose slices are joined: an edge
+# inside the last slice, a last slice of one run, more than one matrix.
+SLICED = [(1, 256, 4096), (1, 16, 4096), (1, 5, 8200), (3, 40, 2047), (1, 3000, 70), (2, 130, 3001), (5, 321, 2081), (1, 1, 65536)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("size", SLICED, ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_slices(dtype, size):
+    print("[ortho] slices", dtype, size, flush=True)
+    assert cbd.ortho_plan(*size).info().slices > 1
+    m = draw(*size, dtype=dtype, seed=size[1])
+    near(call(m, steps=3), m, dtype, str(size), steps=3)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("gap,space,off", [(8, 0, 0), (1, 0, 1), (0, 3, 0), (5, 2, 3)])
 def test_strides_and_alignment(gap, space, off):
@@ -303,6 +318,8 @@ def test_info():
     assert i.launches == 2 + 5 * 5 and cbd.ortho_plan(8, 64, 64, steps=2).info().launches == 2 + 2 * 3
     assert i.flops == 8 * 5 * (3 * 2048 * 2048 * 4096 + 2048 ** 3)
     assert cbd.ortho_plan(0, 16, 16).info().launches == 0
+    i = cbd.ortho_plan(1, 256, 4096, steps=5).info()
+    assert (i.tile_symmetric, i.slices, i.launches) == (64, 16, 2 + 5 * 4) and cbd.ortho_plan(8, 64, 64).info().slices == 1
 
 
 def test_python_refusals_without_a_gpu():
