@@ -32,10 +32,10 @@
 //
 // Stages: one workgroup of 64 x 64 a compute unit waits for every load and LDS
 // read, so four runs are in flight and one in registers (5 / 3 / 2 stages: A of
-// 1024 x 1024 12 / 26 / 25 us, of 2048 x 2048 in larger tiles alike); tiles of 128
-// likewise while there is one a unit (4 / 2 stages: 136 tiles of 64 runs 46 / 62
-// us), two a unit hide each other's ways (363 tiles of 44 runs 74 / 55); tiles of
-// 256 have LDS for two stages, and 96 products a run to hide their loads.
+// 1024 x 1024 12 / 26 / 25 us); tiles of 128 likewise while there is one a unit (4
+// / 2 stages: 136 tiles of 64 runs 46 / 62 us), two a unit hide each other's ways
+// (363 tiles of 44 runs 74 / 55); tiles of 256 have LDS for two stages, and 96
+// products a run to hide their loads.
 #include <type_traits>
 
 #include "cbd_device.h"
