@@ -24,9 +24,9 @@
 // power allows.  8 x 4096 x 2048, a step: A 303 + 76 us (7 matrices in tiles of
 // 256, one in tiles of 128 for the units that those leave idle), B 174 + 48, X 655
 // (1.26 PFLOP/s of halves; a library product of 8192 x 8192 x 8192 in bf16 reaches
-// 1.26), the last 607 (1.36: it writes a quarter of the bytes); the five with norm
-// 31 us (4.3 TB/s) and split 140 (4.2 TB/s, two directions of 4 bytes written)
-// 6.3 - 6.6 ms.  Results leave through LDS in whole columns of blocks: 0.3 ms less
+// 1.26), the last 607 (1.36: it writes a quarter of the bytes); five steps with
+// norm (31 us, 4.3 TB/s) and split (115, 5.8 TB/s, two directions of 4 bytes
+// written) 6.3 - 6.6 ms.  Results leave through LDS in whole columns of blocks: 0.3 ms less
 // than block by block.  Small ones by latency: 16 x 256 x 512 takes 7 to 11 us a
 // launch for 8 to 16 runs.
 //
@@ -590,9 +590,12 @@ __global__ __launch_bounds__(THREADS) void ortho_split_kernel(const OrthoSplit a
   for (int i = 0; i < kOrthoParts / 64; i++) s += a.partial[mat * kOrthoParts + 64 * i + lane];
 #pragma unroll
   for (int m = 32; m > 0; m >>= 1) s += __shfl_xor(s, m, 64);
-  const double f = a.up / (__builtin_sqrt(s) + a.eps);
+  // The factor as m 2^e: it may be past f32, and products in 64 bits take a third
+  // of the time that 16 x 256 x 512 take (14 us; 9 so).
+  int e2;
+  const float m2 = (float)frexp(a.up / (__builtin_sqrt(s) + a.eps), &e2);
 #pragma unroll
-  for (int i = 0; i < 16; i++) tile[4 * i + wave][lane] = split((float)((double)v[i] * f));
+  for (int i = 0; i < 16; i++) tile[4 * i + wave][lane] = split(ldexpf(v[i], e2) * m2);
   __syncthreads();
   // A row of the tile is two runs, 16 pieces of 16 bytes: a lane takes one.
   const int piece = lane & 15, e = 32 * (piece >> 3) + 8 * (piece & 3);
@@ -608,7 +611,8 @@ __global__ __launch_bounds__(THREADS) void ortho_split_kernel(const OrthoSplit a
       u[j] = __builtin_amdgcn_perm(tile[row][e + 2 * j + 1], tile[row][e + 2 * j], sel);
       v[j] = __builtin_amdgcn_perm(tile[e + 2 * j + 1][row], tile[e + 2 * j][row], sel);
     }
-    // Past the caches: 8 matrices of 4096 x 2048 195 -> 161 us.
+    // Past the caches: 8 matrices of 4096 x 2048 161 us, otherwise 195; 16 of 256 x
+    // 512 alike.
     __builtin_nontemporal_store(u, (u32x4*)(x + (int64_t)row * a.ldx));
     __builtin_nontemporal_store(v, (u32x4*)(xt + (int64_t)row * a.ldxt));
   }

@@ -226,6 +226,19 @@ def test_extremes():
 
 
 @pytest.mark.gpu
+def test_powers_of_two_cancel():
+    """Also where the factor to the norm, or the norm's square, is past f32."""
+    for dtype in ("f32", "bf16"):
+        m = draw(3, 48, 70, dtype=dtype, scale=1.0)
+        m[1] = 0.0
+        want = call(m, eps=1e-300)
+        assert not want[1].any() and bool(want[0].any())
+        for power in (-110, -60, 100):  # (the smallest elements stay normal)
+            m2 = torch.where(m.float().abs() < 2.0 ** -14, torch.zeros_like(m), m)
+            assert torch.equal(call(m2.double().mul(2.0 ** power).to(m.dtype), eps=1e-300), call(m2, eps=1e-300)), power
+
+
+@pytest.mark.gpu
 def test_in_place_streams_repeats_and_graph_replays():
     m = draw(4, 100, 180, dtype="bf16")
     want = call(m)
