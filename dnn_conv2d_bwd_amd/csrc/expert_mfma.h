@@ -40,6 +40,17 @@
 // gradient in f32 1.1 ms (1.0 PFLOP/s); 16384 x 2048 x 1408, 64 experts, data
 // gradient 132 us (3.6 TB/s, 0.71 PFLOP/s).
 //
+// Gated forward, a wave's features are half the gate's and half the same ones of
+// the other projection (dev::Pair), so that a lane ends with both and their
+// product never leaves it; the workgroup's loads take the two places of W in
+// turn.  32768 x 4096 x 2 x 2048, 32 experts: 935 - 953 us, as the plain product
+// of 65536 x 4096 x 2048 needs; 993 - 1016 with both projections saved (268 MB
+// more to write while the next tile's products run); matrix units busy 61 % of the
+// clocks, the rest as above.  Gated backward, the tile's gates are read where its
+// results go: 128 wide ahead of the last step's products (1408 outputs x 2048, 64
+// experts, 16384 rows: 168 us, 620 MB at 3.7 TB/s; the plain product, which moves
+// 184 MB less, 130), 256 wide block by block, for want of registers.
+//
 // Two stages of 64 k against four of 32 k (dW has no k-contiguous operand, so
 // its lines are whole either way): dW 1130 / 1100 us, 64 experts of 1408
 // outputs and 1024 rows each 443 / 476 us.

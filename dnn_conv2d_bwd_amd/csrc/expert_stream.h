@@ -17,7 +17,9 @@
 //
 // Gated (GATE_FWD, GATE_FWD_SAVE), half of a workgroup's rows of weights are
 // the gate's and half the same features of the other projection: AK the two
-// 16-feature blocks, AM rows 0..7 and 8..15 of every MFMA.
+// 16-feature blocks, AM rows 0..7 and 8..15 of every MFMA.  64 experts of 2048 x 2
+// x 1408, 8 rows each: AK 134 us (5.5 TB/s), AM 128 (5.8); 8 of them with a row
+// each 17.
 //
 // Rows of the activations are read straight from L2 (every workgroup of an
 // expert reads the same few).  Any alignment of 2 bytes will do.
