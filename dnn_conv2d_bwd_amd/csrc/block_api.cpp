@@ -36,11 +36,16 @@ cbd_status make_plan(const cbd_block_problem* q, cbd_block_plan_t** out) {
   const int64_t groups = (q->rows + per - 1) / per;
   // Workgroups that stay.  Forward, as many as the compute units hold at once (8
   // waves a SIMD; half as many: 4096 rows of 4096 in bf16 27 / 30 us, 32768 rows
-  // alike).  Backward, one of 512 or 1024 threads a compute unit: twice as many
-  // have more sums to join (32768 x 4096 in bf16 301 / 324 us and 5.0 / 6.4 for
-  // the joining, 512 rows 15 / 21 and 4.0 / 4.7; 65536 x 128 20 / 22 and 4.4 / 6.7).
+  // alike).  Backward, as many as have 512 threads with elements a compute unit:
+  // twice that have more sums to join (32768 x 4096 in bf16 301 / 324 us and 5.0 /
+  // 6.4 for the joining, 512 rows 15 / 21 and 4.0 / 4.7; 65536 x 128 20 / 22 and 4.4
+  // / 6.7), and counted with the idle threads of a row's last part there are too few
+  // loads on their way (250 MB in bf16, of 1032 335 / 453 us, 264 328 / 445, 2560
+  // 302 / 347).  Below 64 threads a row three workgroups fit.
+  const int chunks = (int)((q->c * esize(q->dtype) + 15) / 16), most = p->shape.lanes < 64 ? 3 : 1024 / threads;
+  const int active = std::min(chunks, p->shape.lanes) * per, wanted = (512 + active / 2) / active;
   p->grid_fwd = std::min<int64_t>(groups, 256 * (2048 / threads));
-  p->grid_bwd = std::min<int64_t>(groups, 256 * std::max(512 / threads, 1));
+  p->grid_bwd = std::min<int64_t>(groups, 256 * std::max(1, std::min(wanted, most)));
   // A few rows (groups of them) by one workgroup, which then needs no second
   // launch to join its sums with others' (one / many and the joining, us: a row of
   // 4096 9.1 / 12.9, four 13.1 / 13.1, eight 18.2 / 13.2; four groups of four rows

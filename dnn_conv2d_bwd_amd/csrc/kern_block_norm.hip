@@ -22,7 +22,9 @@
 // Bound: HBM.  32768 x 4096 in bf16, vectors for all three: forward 212 us (5.1
 // TB/s; a copy on this card reaches 4.7), backward 302 (5.3) and 5 for the
 // joining; 65536 x 1024 94 and 165, 65536 x 128 13.4 and 20 (67 and 100 MB: the
-// caches hold a part); in f32 8192 x 2048 45 and 79.  With all sums through
+// caches hold a part); in f32 8192 x 2048 45 and 79.  Of 250 MB, other widths from 72
+// to 8192 reach 3.9 - 5.4 TB/s forward and 4.2 - 5.5 backward, the least just
+// above a power of two, where half the threads have nothing.  With all sums through
 // LDS and the vectors held as f32, rows of 4096 took 393 us backward.  One row: 3
 // us, one round to memory and two sums over the waves.
 #include <type_traits>
