@@ -105,13 +105,14 @@ struct Operand {
   int feats[NV];   // feature-contiguous: features of the vector inside the operand
   int back[NV];    // and by how many it is loaded early
   bool edge;       // some of the wave's are
+  bool wide;       // a vector has four elements, inside the contracted length
   f32x4 v[2][NV];  // two steps
 
   // p: element (row 0, k 0) of the tile; rows: inside the operand, >= 1.
   // width: features of the whole operand.
   CBD_INLINE __device__ void init(const T* p, int64_t ld, int rows, int width, int64_t up = 0) {
     step = KC ? BK : BK * ld;
-    const bool wide = width >= 4;
+    wide = KC || width >= 4;
     edge = false;
 #pragma unroll
     for (int i = 0; i < NV; i++) {
@@ -149,6 +150,15 @@ struct Operand {
         v[slot][i] = KC ? load4(q[i], 4) : load4(q[i], feats[i]);
       else
         v[slot][i] = load4(q[i], KC ? left - k : k < left ? feats[i] : 0);
+      q[i] += step;
+    }
+  }
+  // A step that is inside, where vectors are wide: no branch, so that a later wait
+  // counts the loads after it.
+  CBD_INLINE __device__ void load_whole(int slot) {
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+      v[slot][i] = load4(q[i], 4);
       q[i] += step;
     }
   }
@@ -244,7 +254,7 @@ __global__ __launch_bounds__(THREADS, NB == 4 ? 3 : 4) void expert_generic_kerne
 #pragma unroll
     for (int j = 0; j < NB; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  auto step = [&](auto sc, int k0) CBD_INLINE {
+  auto step = [&](auto sc, auto whole, int k0) CBD_INLINE {
     constexpr int S = decltype(sc)::value;
     float* la = lds[S];
     float* lb = la + OpA::LDS;
@@ -253,8 +263,13 @@ __global__ __launch_bounds__(THREADS, NB == 4 ? 3 : 4) void expert_generic_kerne
     // One barrier a step: buffer S was last read two steps ago, before the
     // previous step's barrier.
     __syncthreads();
-    oa.load(S, K - k0 - 2 * BK);
-    ob.load(S, K - k0 - 2 * BK);
+    if constexpr (decltype(whole)::value) {
+      oa.load_whole(S);
+      ob.load_whole(S);
+    } else {
+      oa.load(S, K - k0 - 2 * BK);
+      ob.load(S, K - k0 - 2 * BK);
+    }
 #pragma unroll
     for (int kb = 0; kb < BK; kb += 16) {
       float fa[NB][4], fb[NB][4];
@@ -272,14 +287,32 @@ __global__ __launch_bounds__(THREADS, NB == 4 ? 3 : 4) void expert_generic_kerne
       }
     }
   };
-  oa.load(0, K);
-  ob.load(0, K);
-  oa.load(1, K - BK);
-  ob.load(1, K - BK);
+  constexpr std::integral_constant<int, 0> even{};
+  constexpr std::integral_constant<int, 1> odd{};
+  // Steps whose loads two steps ahead are inside, then the others, whose branches
+  // make the compiler wait for all loads every second step.
+  int k0 = 0;
+  if (oa.wide && ob.wide && K >= 4 * BK) {
+    oa.load_whole(0);
+    ob.load_whole(0);
+    __builtin_amdgcn_sched_barrier(0);  // in this order, which the waits count on
+    oa.load_whole(1);
+    ob.load_whole(1);
 #pragma unroll 1
-  for (int k0 = 0; k0 < K; k0 += 2 * BK) {
-    step(std::integral_constant<int, 0>(), k0);
-    if (k0 + BK < K) step(std::integral_constant<int, 1>(), k0 + BK);
+    for (; k0 + 4 * BK <= K; k0 += 2 * BK) {
+      step(even, std::true_type(), k0);
+      step(odd, std::true_type(), k0 + BK);
+    }
+  } else {
+    oa.load(0, K);
+    ob.load(0, K);
+    oa.load(1, K - BK);
+    ob.load(1, K - BK);
+  }
+#pragma unroll 1
+  for (; k0 < K; k0 += 2 * BK) {
+    step(even, std::false_type(), k0);
+    if (k0 + BK < K) step(odd, std::false_type(), k0 + BK);
   }
 
   // Lane: column (n) lane % 16 of a block, rows (m) 4 * (lane / 16) + r.
