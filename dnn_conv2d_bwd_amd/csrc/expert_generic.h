@@ -22,11 +22,13 @@
 //
 // Bound: the f32 matrix rate (154 TFLOP/s reached by a large product; a 128 x
 // 128 tile does 32 flops per loaded byte in f32).  8192 x 2048 x 2048, 4
-// experts: 97 TFLOP/s; 3001 x 515 x 389, 7 experts: 29 us, of which 16 are
+// experts: 118 TFLOP/s; 3001 x 515 x 389, 7 experts: 25 us, of which 16 are
 // MFMAs of the compute units that get two of the 357 tiles.  Gated, rows of weights
-// in pairs as in expert_mfma.h, 64 x 64 tiles: 8192 x 2048 x 2 x 1024 93 TFLOP/s;
-// 3001 x 515 x 2 x 389 with both projections saved 42 us, of which 21 are MFMAs of
-// the units with three of the 702 tiles.
+// in pairs as in expert_mfma.h, 64 x 64 tiles: 8192 x 2048 x 2 x 1024 120 TFLOP/s;
+// 3001 x 515 x 2 x 389 with both projections saved 36 us, of which 21 are MFMAs of
+// the units with three of the 702 tiles.  With the branches of the last steps in
+// all of them, and so a wait for all loads every second step: 743 us instead of 572,
+// and 39.
 #pragma once
 #include <type_traits>
 

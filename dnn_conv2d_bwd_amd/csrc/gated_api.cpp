@@ -73,10 +73,10 @@ ExpertLaunch choose(const cbd_expert_plan_s& plan, bool bwd, bool narrow_strides
     tile = l.dma && whole_out && many && grid(256 / parts, 256) >= 512 ? 256 : 128;
   } else {
     // 64 x 64 (of the expert products' two tiles: 64 / 128 in us, f32, 4 experts,
-    // 16384 rows, 2048 inputs, 2 x 2048 outputs 2565 / 2465 and backward 1355 /
-    // 1338; 8192 rows, 2 x 1024 743 / 738 and 420 / 462; 8 experts, 4096 rows, 1024
-    // inputs, 2 x 1024 186 / 214 and 114 / 157; 64 experts, 8192 rows, 2 x 704 278 /
-    // 368 and 169 / 234).
+    // 16384 rows, 2048 inputs, 2 x 2048 outputs 2354 / 2308 and backward 1306 /
+    // 1309; 8192 rows, 2 x 1024 572 / 627 and 342 / 423; 8 experts, 4096 rows, 1024
+    // inputs, 2 x 1024 165 / 197 and 105 / 151; 64 experts, 8192 rows, 2 x 704 247 /
+    // 332 and 154 / 219).
     tile = 64;
   }
   l.bm = (int32_t)(tile / parts);
