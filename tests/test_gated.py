@@ -164,6 +164,33 @@ def test_against_definition(dtype, lay, size):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [640, 3305, 4096])
+@pytest.mark.parametrize("lay", LAYS)
+def test_long_f32_sums(lay, n):
+    """1 and n - 1 terms of 2^-25, which one sum from the front would lose (n 2^-25
+    of 1).  In sums of 128 terms, the last of up to 255, that are joined, a term
+    is in at most 255 + n / 128 + 2 additions, each off by at most 2^-24 of what
+    it adds up to."""
+    print("[gated] long sums", lay, n, flush=True)
+    terms = torch.full((n,), 2.0 ** -25)
+    terms[0] = 1.0
+    want = 1.0 + (n - 1) * 2.0 ** -25
+    tol = (255 + n / 128 + 2) * 2.0 ** -24 * want
+    assert tol < (n - 1) * 2.0 ** -25 or n < 1000
+    t, k, ends = 40, 24, torch.tensor([40], dtype=torch.int32, device="cuda")
+    ones, w = torch.ones(t, n, device="cuda"), terms.cuda().expand(1, 2 * k, n).contiguous()
+    h, gu = cbd.expert_gated_forward(cbd.expert_plan(t, 1, n, 2 * k, lay, "f32"), ones,
+                                     w if lay == "ekc" else w.transpose(1, 2).contiguous(), ends, act="relu", save=True)
+    assert float((gu.double() - want).abs().max()) <= tol
+    assert float((h.double() - want * want).abs().max()) <= 2.0 ** -24 * want * want + 2.1 * tol
+    down = w[:, :k]
+    dgu = cbd.expert_gated_bwd(cbd.expert_plan(t, 1, k, n, lay, "f32"), ones,
+                               down.transpose(1, 2).contiguous() if lay == "ekc" else down.contiguous(),
+                               torch.ones_like(gu), ends, act="relu")
+    assert float((dgu.double() - want).abs().max()) <= tol
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("lay", LAYS)
 def test_activations(lay, act):
