@@ -234,6 +234,7 @@ cbd_status bwd(const cbd_block_plan_t* plan, const void* dz, const void* dn, con
     cbd::BlockArgs a = arguments(q, o, r, y);
     a.dz = dz;
     a.dn = dn;
+    if (!dn) a.w_pre = nullptr;
     a.dr = g.dr;
     a.dy = g.dy;
     a.dgate = dgate_row;

@@ -22,7 +22,7 @@ struct BlockFinish {
 };
 
 struct BlockArgs {
-  const void *r, *y, *gate, *w_post, *w_pre;  // gate: a vector, or rows (gate_row != 0)
+  const void *r, *y, *gate, *w_post, *w_pre;  // gate: a vector, or rows (gate_rows != 0); bwd: w_pre only with dn
   const void *dz, *dn;                        // bwd; NULL: zeros
   void *z, *n;                                // forward; NULL: not written
   void *dr, *dy, *dgate;                      // bwd; dgate: of a gate of rows

@@ -10,7 +10,9 @@
 // S2 = sum c * yn * (dz + rz * v) - rz * S1 / C * sum c * yn * zn, so that the
 // three sums of a row come from one round over its threads.  The vectors'
 // gradients need sum dn * zn and sum scale * dz' * yn over the rows: w_post and
-// a gate vector are factors of the second that a column shares.
+// a gate vector are factors of the second that a column shares.  Without dn the
+// second norm takes no part (w_pre is NULL then): what r and w_pre hold, which may
+// be infinite, reaches nothing.
 //
 // A row stays in registers from its one load to its stores, 16 bytes a thread: a
 // workgroup (or, up to 64 threads a row, a part of one) takes rows i, i + grid,
@@ -430,8 +432,9 @@ __global__ __launch_bounds__(kThreads<LANES>, (kWaves<LANES, CH>)) void block_bw
     }
     if (kAhead<CH> && row + rows.step < a.rows) fetch_all(row + rows.step);
     sum(s);
-    const float along = rz * s[0] * inv_c;             // of zn in dz'
-    const float back = (s[1] - along * s[2]) * inv_c;  // of yn in dy
+    // (Where there is no norm, nothing is taken off: not 0 times infinity.)
+    const float along = a.w_pre ? rz * s[0] * inv_c : 0.f;                 // of zn in dz'
+    const float back = (a.w_pre ? s[1] - along * s[2] : s[1]) * inv_c;  // of yn in dy
 #pragma unroll
     for (int i = 0; i < CH; i++) {
       if (!HELD) {
@@ -442,7 +445,6 @@ __global__ __launch_bounds__(kThreads<LANES>, (kWaves<LANES, CH>)) void block_bw
       float fr[N], fy[N], fg[N];
 #pragma unroll
       for (int j = 0; j < N; j++) {
-        // (Where there is no norm, nothing is taken off: not 0 times infinity.)
         fr[j] = a.w_pre ? __builtin_fmaf(-along, zn[i][j], e[i][j]) : e[i][j];
         const float da = a.scale * fr[j], dg = da * gr[i].get(j), w = wq[i].get(j);
         fg[j] = da * yn[i][j] * w;
@@ -461,6 +463,8 @@ __global__ __launch_bounds__(kThreads<LANES>, (kWaves<LANES, CH>)) void block_bw
   }
   const bool alone = gridDim.x == 1;  // no one to join
   if (!a.partial) return;
+  // No second norm or no dn: dw_pre is 0, not the sum of 0 times what r holds.
+  auto first = [&](int i, int j) { return a.w_pre ? pre[i][j] : 0.f; };
   float* const out = a.partial + (int64_t)blockIdx.x * 2 * a.c;
   if constexpr (LANES <= 64) {
     // The groups' sums, joined in their order.
@@ -470,7 +474,7 @@ __global__ __launch_bounds__(kThreads<LANES>, (kWaves<LANES, CH>)) void block_bw
     for (int i = 0; i < CH; i++)
 #pragma unroll
       for (int j = 0; j < N; j++) {
-        join[0][i * N + j][threadIdx.x] = pre[i][j];
+        join[0][i * N + j][threadIdx.x] = first(i, j);
         join[1][i * N + j][threadIdx.x] = post[i][j];
       }
     __syncthreads();
@@ -499,10 +503,10 @@ __global__ __launch_bounds__(kThreads<LANES>, (kWaves<LANES, CH>)) void block_bw
     for (int j = 0; j < N; j++)
       if (at + j < a.c) {
         if (alone) {
-          finish_column(a.finish, 0, at + j, pre[i][j]);
+          finish_column(a.finish, 0, at + j, first(i, j));
           finish_column(a.finish, 1, at + j, post[i][j]);
         } else {
-          out[at + j] = pre[i][j];
+          out[at + j] = first(i, j);
           out[a.c + at + j] = post[i][j];
         }
       }

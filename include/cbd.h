@@ -505,7 +505,9 @@ cbd_status cbd_expert_gated_info(const cbd_expert_plan_t* plan, int32_t bwd, cbd
  * NULL (then n is NULL): no n.  The gate is one vector for all rows or has a
  * row for each.  stats receives 1 / sqrt(mean + eps) of y and of z, 1 where
  * there is no norm.  Backward, from the gradients of z and n (NULL: zeros):
- * dr, dy, dw_post, dgate and dw_pre, each NULL where it is not wanted.
+ * dr, dy, dw_post, dgate and dw_pre, each NULL where it is not wanted.  A
+ * second norm whose result has no gradient (no w_pre, or no dn) takes no part:
+ * infinities and NaN that reach only n reach none of them.
  *
  * Everything is computed in f32 from the inputs, sums included (a row whose
  * squares pass f32's range has norm(v) = 0), and each result is rounded once;

@@ -270,6 +270,40 @@ def test_extreme_rows():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,rows,c", [("bf16", 6, 96), ("f32", 700, 515), ("bf16", 700, 4096), ("bf16", 6, 8200), ("f32", 6, 8196)])
+@pytest.mark.parametrize("form", FORMS, ids=str)
+def test_a_norm_without_a_gradient_takes_no_part(form, dtype, rows, c):
+    """Where n is not there, or has no gradient, r and w_pre are no part of the
+    results: what they hold changes no bit, infinities and NaN included."""
+    inf, nan = float("inf"), float("nan")
+    print("[block]", form, dtype, rows, c, flush=True)
+    without = Block(rows, c, dtype=dtype, pre=False, **form)
+    want = without.bwd()
+    assert torch.equal(want[0].double().cpu(), without.dz)
+    without.a["r"][1], without.a["r"][2, 3], without.a["r"][4] = inf, nan, -inf
+    b = Block(rows, c, dtype=dtype, **form)
+    b.a["r"][1], b.a["r"][2, 3], b.a["r"][4], b.a["w_pre"][5] = inf, nan, -inf, inf
+    for got in (without.bwd(), b.bwd(dn=False)):
+        for u, v in zip(want[:4], got):
+            assert (u is None) == (v is None) and (u is None or torch.equal(u, v))
+    assert torch.equal(got[4], torch.zeros_like(got[4]))
+    if not form["post"] and form["gate"] == "none":
+        # dy is scale * dz: y is no part of it either.
+        b.a["y"][3] = inf
+        got = b.bwd(dn=False)
+        assert all(torch.equal(u, v) for u, v in zip(want[:2], got)) and not got[4].any()
+
+
+@pytest.mark.gpu
+def test_a_norm_alone_without_a_gradient():
+    for dtype, c in (("bf16", 72), ("f32", 8196)):
+        b = Block(5, c, dtype=dtype, y=False)
+        b.a["r"][1], b.a["w_pre"][0] = float("inf"), float("nan")
+        dr, dy, _, _, dw = b.bwd(dn=False)
+        assert torch.equal(dr.double().cpu(), b.dz) and dy is None and torch.equal(dw, torch.zeros_like(dw))
+
+
+@pytest.mark.gpu
 def test_in_place_is_the_same():
     b = Block(50, 600)
     d = b.device()
