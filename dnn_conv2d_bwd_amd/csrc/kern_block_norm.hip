@@ -315,8 +315,9 @@ __device__ inline void finish_column(const BlockFinish& a, int which, int col, d
   if (which == 0) {
     put(a.dw_pre, s);
   } else {
-    put(a.dw_post, s * vector(a.gate));
-    put(a.dgate, s * vector(a.w_post));
+    // (No rows: zeros, whatever the vectors hold.)
+    put(a.dw_post, a.n ? s * vector(a.gate) : 0.0);
+    put(a.dgate, a.n ? s * vector(a.w_post) : 0.0);
   }
 }
 

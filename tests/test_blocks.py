@@ -356,6 +356,13 @@ def test_masks_and_empty():
 
 
 @pytest.mark.gpu
+def test_no_rows_and_vectors_that_are_not_finite():
+    none = Block(0, 80)
+    none.a["gate"][3], none.a["w_post"][5], none.a["w_pre"][7] = float("inf"), float("nan"), float("inf")
+    assert all(torch.equal(v, torch.zeros_like(v)) for v in none.bwd()[2:])
+
+
+@pytest.mark.gpu
 def test_streams_repeats_and_graph_replays():
     b = Block(700, 264)
     want = [*b.forward(), *b.bwd()]
