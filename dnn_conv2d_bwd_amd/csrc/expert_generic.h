@@ -385,14 +385,17 @@ __global__ __launch_bounds__(THREADS, NB == 4 ? 3 : 4) void expert_generic_kerne
 #pragma unroll
       for (int c = 0; c < NB; c++) {
         const int m = FORM == EXPERT_AK ? wm + 16 * c + 4 * (lane >> 4) : wm + NB * 4 * (lane >> 4) + 4 * c;
-        const f32x4 g = load4(gu + n * a.ldgu + m, mrows - m), u = load4(gu + n * a.ldgu + a.M + m, mrows - m);
-        f32x4 dg, du;
+        // Rows past the last expert's (K is 0) are +0, whatever gu holds there.
+        f32x4 dg = {0.f, 0.f, 0.f, 0.f}, du = dg;
+        if (K > 0) {
+          const f32x4 g = load4(gu + n * a.ldgu + m, mrows - m), u = load4(gu + n * a.ldgu + a.M + m, mrows - m);
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-          const float dh = FORM == EXPERT_AK ? acc[c][y][j] : acc[(4 * c + j) % NB][y][(4 * c + j) / NB];
-          float slope;
-          du[j] = dh * gate.template act<FINE>(g[j], slope);
-          dg[j] = dh * u[j] * slope;
+          for (int j = 0; j < 4; j++) {
+            const float dh = FORM == EXPERT_AK ? acc[c][y][j] : acc[(4 * c + j) % NB][y][(4 * c + j) / NB];
+            float slope;
+            du[j] = dh * gate.template act<FINE>(g[j], slope);
+            dg[j] = dh * u[j] * slope;
+          }
         }
         store4(o + m, dg, mrows - m, false);
         store4(o + a.M + m, du, mrows - m, false);

@@ -265,6 +265,26 @@ def test_rows_and_experts_stay_apart(lay):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("lay", LAYS)
+def test_rows_of_nobody_are_plus_zero(lay, act):
+    """Whatever their operands hold, the saved projections included: NaN,
+    infinities, and values whose products with 0 are -0."""
+    inf, nan = float("inf"), float("nan")
+    for kernel, dtype in ((cbd.EXPERT_KERNEL_GENERIC, "f32"), (cbd.EXPERT_KERNEL_GENERIC, "bf16"),
+                          (cbd.EXPERT_KERNEL_MFMA, "bf16"), (cbd.EXPERT_KERNEL_STREAM, "bf16")):
+        for c, k in ((40, 56), (17, 3)):
+            print("[gated] nobody's", lay, act, kernel, dtype, c, k, flush=True)
+            g = Gated(lay, 70, 4, c, k, [20, 20, 50, 60], dtype=dtype, act=act, kernel=kernel)
+            g.x[60:], g.dy[60:], g.gu[60:] = -1.0, -1.0, -3.0
+            g.x[61], g.dy[62], g.gu[63], g.gu[64], g.gu[65, 0], g.gu[66, k] = nan, inf, nan, inf, -inf, -inf
+            g.gu[67, :k], g.gu[68, k:] = 2.0, 2.0
+            for v in (*g.forward(True), g.forward(False)[0], g.bwd()):
+                assert torch.equal(v[60:], torch.zeros_like(v[60:])) and not torch.signbit(v[60:]).any()
+                assert torch.isfinite(v).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ACTS)
 def test_extreme_gates(act):
     """Far gates give what the formula's limits are, through every kernel."""
     big = [0.0, -0.0, 1e-30, 50.0, -50.0, 200.0, -200.0, 3e4, -3e4, 1e20, -1e20, 3e38, -3e38]
