@@ -264,6 +264,19 @@ __global__ __launch_bounds__(THREADS, NB == 4 ? 3 : 4) void expert_generic_kerne
 #pragma unroll
     for (int j = 0; j < NB; j++) total[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+  auto join = [&](int k0) CBD_INLINE {
+    if constexpr (GATE != GATE_NONE)
+      if (k0 % 128 == 0) {
+#pragma unroll
+        for (int i = 0; i < NB; i++)
+#pragma unroll
+          for (int j = 0; j < NB; j++) {
+            total[i][j] += acc[i][j];
+            acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+          }
+      }
+  };
+
   auto step = [&](auto sc, auto whole, int k0) CBD_INLINE {
     constexpr int S = decltype(sc)::value;
     float* la = lds[S];
@@ -310,16 +323,7 @@ __global__ __launch_bounds__(THREADS, NB == 4 ? 3 : 4) void expert_generic_kerne
     ob.load_whole(1);
 #pragma unroll 1
     for (; k0 + 4 * BK <= K; k0 += 2 * BK) {
-      if constexpr (GATE != GATE_NONE)
-        if (k0 % 128 == 0) {
-#pragma unroll
-          for (int i = 0; i < NB; i++)
-#pragma unroll
-            for (int j = 0; j < NB; j++) {
-              total[i][j] += acc[i][j];
-              acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-            }
-        }
+      join(k0);
       step(even, std::true_type(), k0);
       step(odd, std::true_type(), k0 + BK);
     }
@@ -331,6 +335,7 @@ __global__ __launch_bounds__(THREADS, NB == 4 ? 3 : 4) void expert_generic_kerne
   }
 #pragma unroll 1
   for (; k0 < K; k0 += 2 * BK) {
+    join(k0);
     step(even, std::false_type(), k0);
     if (k0 + BK < K) step(odd, std::false_type(), k0 + BK);
   }

@@ -191,6 +191,31 @@ def test_long_f32_sums(lay, n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("k", [1, 2, 3])
+@pytest.mark.parametrize("n", [640, 3305, 4096])
+@pytest.mark.parametrize("lay", LAYS)
+def test_long_f32_sums_of_few_features(lay, n, k):
+    """As test_long_f32_sums, with fewer features than a vector holds; one sum
+    from the front would be off by most of what the small terms add up to."""
+    print("[gated] long sums", lay, n, k, flush=True)
+    terms = torch.full((n,), 2.0 ** -25)
+    terms[0] = 1.0
+    want = 1.0 + (n - 1) * 2.0 ** -25
+    tol = (255 + n / 128 + 2) * 2.0 ** -24 * want
+    t, ends = 40, torch.tensor([40], dtype=torch.int32, device="cuda")
+    ones, w = torch.ones(t, n, device="cuda"), terms.cuda().expand(1, 2 * k, n).contiguous()
+    h, gu = cbd.expert_gated_forward(cbd.expert_plan(t, 1, n, 2 * k, lay, "f32"), ones,
+                                     w if lay == "ekc" else w.transpose(1, 2).contiguous(), ends, act="relu", save=True)
+    down = w[:, :k]
+    dgu = cbd.expert_gated_bwd(cbd.expert_plan(t, 1, k, n, lay, "f32"), ones,
+                               down.transpose(1, 2).contiguous() if lay == "ekc" else down.contiguous(),
+                               torch.ones_like(gu), ends, act="relu")
+    off = [float((v.double() - want).abs().max()) for v in (gu, dgu)]
+    assert max(off) <= tol, f"{off} off, {tol} allowed"
+    assert float((h.double() - want * want).abs().max()) <= 2.0 ** -24 * want * want + 2.1 * tol
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("lay", LAYS)
 def test_activations(lay, act):
