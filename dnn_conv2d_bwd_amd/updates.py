@@ -9,16 +9,17 @@ c A A) X with A = X X^T, which draws the singular values towards 1 and leaves
 the singular vectors; the result times `scale`.  Weights of experts [E, K, C]
 are such a stack as they are; matrices and rows may be strided.
 
-`orthogonalized(m)` makes the plan itself.  Nothing is recorded by autograd; a
-tensor that is written to counts as changed in place.  include/cbd.h states the
-operation in full.
+`orthogonalized(m)` makes the plan itself.  Nothing is recorded by autograd:
+where an operand requires gradients the call is refused (use torch.no_grad()).
+A tensor that is written to counts as changed in place.  include/cbd.h states
+the operation in full.
 """
 from __future__ import annotations
 
 import ctypes
 
 from . import F32, _check, _dtype, _lib, _torch_dtype
-from .experts import _handle, _on, _strided, _written
+from .experts import _any_records, _handle, _on, _strided, _written
 
 
 class OrthoProblem(ctypes.Structure):
@@ -110,6 +111,9 @@ def orthogonalize(p: OrthoPlan, m, out=None, workspace=None, stream=None):
     out is allocated unless given, may be m itself, and is returned."""
     import torch
 
+    if _any_records((m,)):
+        raise ValueError("orthogonalize is not recorded by autograd and m requires gradients (or has a tangent); "
+                         "call under torch.no_grad()")
     shape = (p.matrices, p.rows, p.cols)
     s_in = _strided(m, shape, p._tdtype, None, "m")
     dev = m.device

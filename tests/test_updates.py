@@ -348,6 +348,22 @@ def test_python_refusals_without_a_gpu():
         cbd.orthogonalized(torch.zeros(4, 4, dtype=torch.float64))
 
 
+def test_what_autograd_would_lose_is_refused():
+    p = cbd.ortho_plan(1, 4, 4)
+    m = torch.zeros(1, 4, 4, requires_grad=True)
+    for call_ in (lambda: cbd.orthogonalize(p, m), lambda: cbd.orthogonalized(m), lambda: cbd.orthogonalized(m[0])):
+        with pytest.raises(ValueError, match="autograd"):
+            call_()
+        with torch.no_grad(), pytest.raises(ValueError, match="GPU"):
+            call_()
+    import torch.autograd.forward_ad as forward
+
+    with forward.dual_level():
+        dual = forward.make_dual(m.detach(), torch.ones(1, 4, 4))
+        with pytest.raises(ValueError, match="tangent"):
+            cbd.orthogonalize(p, dual)
+
+
 @pytest.mark.gpu
 def test_python_refusals():
     p = cbd.ortho_plan(2, 4, 8)
