@@ -65,11 +65,12 @@ class OrthoPlan:
         self.dtype, self.steps = _dtype(dtype), int(steps)
         flat = None
         if coefficients is not None:
-            flat = [float(v) for c in coefficients for v in c]
-            if len(flat) == 3 and self.steps > 0:
-                flat *= self.steps
-            if len(flat) != 3 * self.steps:
+            triples = [[float(v) for v in c] for c in coefficients]
+            if len(triples) == 1:
+                triples *= max(self.steps, 0)
+            if len(triples) != self.steps or any(len(c) != 3 for c in triples):
                 raise ValueError(f"coefficients must be {self.steps} triples, or one for all steps")
+            flat = [v for c in triples for v in c]
             flat = (ctypes.c_double * len(flat))(*flat)
         prob = OrthoProblem(self.matrices, self.rows, self.cols, self.dtype, self.steps, float(eps), float(scale),
                             None if flat is None else ctypes.cast(flat, ctypes.POINTER(ctypes.c_double)))

@@ -364,6 +364,15 @@ def test_what_autograd_would_lose_is_refused():
             cbd.orthogonalize(p, dual)
 
 
+def test_coefficients_that_are_no_triples_are_refused():
+    """Also where there are three numbers a step all together."""
+    for steps, co in ((2, [(1.0, 2.0)] * 3), (2, [(1.5, -0.5, 0.0, 1.5, -0.5, 0.0)]), (1, [(1.5,), (-0.5,), (0.0,)]),
+                      (3, [(1.5, -0.5, 0.0)] * 2)):
+        with pytest.raises(ValueError, match="triples"):
+            cbd.ortho_plan(1, 4, 4, steps=steps, coefficients=co)
+    assert cbd.ortho_plan(1, 4, 4, steps=2, coefficients=[(1.5, -0.5, 0.0)] * 2).steps == 2
+
+
 @pytest.mark.gpu
 def test_python_refusals():
     p = cbd.ortho_plan(2, 4, 8)
