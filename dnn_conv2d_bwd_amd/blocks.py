@@ -184,6 +184,8 @@ def block_forward(p: BlockPlan, r, y=None, w_post=None, gate=None, w_pre=None, s
         if z is not None or n is not None or stats is not None:
             raise ValueError("autograd cannot record a call into a given output: an operand requires gradients "
                              "(or has a tangent); leave the outputs out or call under torch.no_grad()")
+        if not r.is_cuda:
+            raise ValueError("r must be a GPU torch tensor")
         with _on(r.device, stream):
             z, n, stats = _recorder().apply(r, y, w_post, gate, w_pre, p)
     else:

@@ -525,6 +525,16 @@ def test_python_refusals_without_a_gpu():
         cbd.block_norm(r, r[:2], w_pre=w)
 
 
+def test_operands_on_the_host_are_refused_with_gradients_too():
+    p = cbd.block_plan(4, 8)
+    r, w = torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(8, dtype=torch.bfloat16)
+    for a, b in ((r.clone().requires_grad_(), w), (r, w.clone().requires_grad_())):
+        with pytest.raises(ValueError, match="GPU"):
+            cbd.block_forward(p, a, w_pre=b)
+        with pytest.raises(ValueError, match="GPU"):
+            cbd.block_norm(a, w_pre=b)
+
+
 @pytest.mark.gpu
 def test_python_refusals():
     p = cbd.block_plan(4, 8)
