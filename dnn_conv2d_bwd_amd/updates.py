@@ -103,7 +103,7 @@ class OrthoPlan:
 def ortho_plan(matrices, rows, cols, dtype="f32", steps=5, coefficients=None, eps=1e-7, scale=1.0) -> OrthoPlan:
     """coefficients: (a, b, c) of each step, [(a, b, c)] for all; None: (3.4445,
     -4.7750, 2.0315), whose five steps bring singular values above 0.01 of the
-    norm to between 0.7 and 1.2."""
+    norm to between 0.68 and 1.14."""
     return OrthoPlan(matrices, rows, cols, dtype, steps, coefficients, eps, scale)
 
 

@@ -335,6 +335,16 @@ def test_info():
     assert (i.tile_symmetric, i.slices, i.launches) == (64, 16, 2 + 5 * 4) and cbd.ortho_plan(8, 64, 64).info().slices == 1
 
 
+def test_range_of_the_usual_coefficients():
+    """What ortho_plan's description says of five steps: singular values above 0.01
+    of the norm end between 0.68 and 1.14."""
+    x = torch.linspace(0.01, 1.0, 1000001, dtype=torch.float64)
+    for _ in range(5):
+        x = USUAL[0] * x + USUAL[1] * x ** 3 + USUAL[2] * x ** 5
+    assert 0.68 <= float(x.min()) < 0.69 and 1.13 < float(x.max()) <= 1.14
+    assert "0.68 and 1.14" in " ".join(cbd.ortho_plan.__doc__.split())
+
+
 def test_python_refusals_without_a_gpu():
     with pytest.raises(ValueError, match="GPU"):
         cbd.orthogonalize(cbd.ortho_plan(1, 4, 4), torch.zeros(1, 4, 4))
