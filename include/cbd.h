@@ -479,8 +479,10 @@ typedef struct {
 
 /* gu of the forward call may be NULL: it is not written then.  Errors as for
  * the expert calls, plus INVALID_ARG for an unknown act and a forward plan with
- * odd k, and UNSUPPORTED for a plan with a forced kernel that does not take
- * the call (gated_bwd has no stream kernel and runs the MFMA one). */
+ * odd k.  Where a forced stream kernel does not take a call the MFMA one runs, as
+ * in the expert calls: in gated_bwd always (cbd_expert_gated_info says so), in
+ * gated_forward where 256 rows of W pass 2^31 bytes or the call has 2^24
+ * workgroups or more. */
 cbd_status cbd_expert_gated_forward(const cbd_expert_plan_t* plan, const void* x, const void* w,
                                     const void* ends, void* h, void* gu, int32_t act,
                                     const cbd_gated_strides* strides, void* stream);

@@ -572,6 +572,18 @@ def test_kernel_choice():
     assert i.grid > 0 and i.flops == 2 * 65536 * 2048 * 2816
 
 
+def test_a_forced_stream_kernel_that_does_not_take_the_call():
+    """The MFMA kernel runs in its place, and the call's information says so."""
+    forced = dict(force_kernel=cbd.EXPERT_KERNEL_STREAM)
+    for lay in LAYS:
+        p = cbd.expert_plan(4096, 4, 64, 128, lay, **forced)
+        assert cbd.expert_gated_info(p).kernel == cbd.EXPERT_KERNEL_STREAM
+        assert cbd.expert_gated_info(cbd.expert_plan(4096, 4, 64, 64, lay, **forced), True).kernel == cbd.EXPERT_KERNEL_MFMA
+        # 2^24 workgroups or more of the stream kernel's 32 rows.
+        p = cbd.expert_plan(1 << 30, 4, 8, 2, lay, **forced)
+        assert cbd.expert_gated_info(p).kernel == cbd.EXPERT_KERNEL_MFMA
+
+
 def test_python_refusals_without_a_gpu():
     p, d = cbd.expert_plan(4, 2, 8, 8), cbd.expert_plan(4, 2, 4, 8)
     x, w = torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(2, 8, 8, dtype=torch.bfloat16)
