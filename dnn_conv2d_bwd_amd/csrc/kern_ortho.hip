@@ -592,8 +592,9 @@ __global__ __launch_bounds__(THREADS) void ortho_split_kernel(const OrthoSplit a
   for (int m = 32; m > 0; m >>= 1) s += __shfl_xor(s, m, 64);
   // The factor as m 2^e: it may be past f32, and products in 64 bits take a third
   // of the time that 16 x 256 x 512 take (14 us; 9 so).
+  // (Zeros stay zeros with an eps whose inverse is past f64, too.)
   int e2;
-  const float m2 = (float)frexp(a.up / (__builtin_sqrt(s) + a.eps), &e2);
+  const float m2 = (float)frexp(s == 0.0 ? 0.0 : a.up / (__builtin_sqrt(s) + a.eps), &e2);
 #pragma unroll
   for (int i = 0; i < 16; i++) tile[4 * i + wave][lane] = split(ldexpf(v[i], e2) * m2);
   __syncthreads();

@@ -226,6 +226,16 @@ def test_extremes():
 
 
 @pytest.mark.gpu
+def test_zeros_whatever_eps_is():
+    m = draw(3, 20, 30)
+    m[1] = 0.0
+    for eps in (1e-300, 1e-310, 5e-324):
+        got = call(m, eps=eps)
+        assert torch.equal(got[1], torch.zeros_like(got[1])) and torch.isfinite(got).all()
+        near(got[[0, 2]], m[[0, 2]], "f32", eps=eps)
+
+
+@pytest.mark.gpu
 def test_powers_of_two_cancel():
     """Also where the factor to the norm, or the norm's square, is past f32."""
     for dtype in ("f32", "bf16"):
