@@ -368,6 +368,12 @@ __global__ __launch_bounds__(THREADS, MB == 4 || (MB == 2 && NS > 2) ? 1 : 2) vo
       float v[16];
 #pragma unroll
       for (int j = 0; j < 16; j++) v[j] = (APART ? acc[m][n][j] + low[APART ? m : 0][APART ? n : 0][j] : acc[m][n][j]) * a.mul;
+      // (A power of two and the scale apart: together they may be below f32's normal
+      // numbers where the result is not.)
+      if constexpr (STAGE == ORTHO_LAST) {
+#pragma unroll
+        for (int j = 0; j < 16; j++) v[j] *= a.scale;
+      }
       if constexpr (STAGE == ORTHO_POLY) {
         u32x2 (&o)[8] = own[EARLY ? n * MB + m : 0];
         if constexpr (!EARLY) fetch(m, n, o);

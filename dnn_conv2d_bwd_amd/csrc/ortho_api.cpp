@@ -314,7 +314,8 @@ cbd_status run(const cbd_ortho_plan_t* plan, const void* in, void* out, const cb
     a.rows = (int32_t)plan->s;
     a.cols = (int32_t)plan->l;
     if (last) {
-      a.mul = (float)(std::ldexp(1.0, -eb - ex) * q.scale);
+      a.mul = (float)std::ldexp(1.0, -eb - ex);
+      a.scale = (float)q.scale;
       a.out = out;
       a.out_row = s.out_row;
       a.out_mat = s.out_matrix;

@@ -38,6 +38,7 @@ struct OrthoArgs {
   float mul;                 // C is the products' sum times this
   float p_mul, diag;         // ORTHO_POLY: and P times p_mul, and diag on the diagonal
   void* out;                 // ORTHO_LAST
+  float scale;               // and the result is C times this
   int64_t out_row, out_mat;
   int32_t out_dtype, flip;   // flip: the output is C^T
   float* sums;               // ORTHO_SLICE: [matrix][tile][slice] tiles of 64 columns of 64

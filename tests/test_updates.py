@@ -191,6 +191,14 @@ def test_scale_and_eps():
 
 
 @pytest.mark.gpu
+def test_small_scales():
+    """Down to results that are just normal numbers."""
+    m = draw(2, 20, 30)
+    for scale in (3e-30, 3e-36, -7e-36):
+        near(call(m, scale=scale), m, "f32", scale=scale)
+
+
+@pytest.mark.gpu
 def test_known_results():
     """Matrices whose singular values are all alike come out as multiples of
     themselves: signed permutations, and a Hadamard matrix."""
