@@ -7,9 +7,16 @@
 // f32 sums; lo lo is below 2^-22 of it.  A value keeps 22 bits: each step's
 // rounding is some 2^-24 of it, next to sums of f32 products, whose own are
 // larger; and halves go at 16 times the rate of the f32 instructions, so that
-// three of them are 5 times as fast.  One exponent a matrix, chosen by the plan
-// from the bounds of the singular values, keeps the largest value at 2^14 at
-// most and the smallest ones' lo out of the subnormals.
+// three of them are 5 times as fast.
+//
+// One exponent a matrix, chosen by the plan from the bounds of the singular values,
+// keeps the largest value at 2^14 at most.  Halves end at 2^-24, so small values have
+// fewer bits: with lo as it is, those below 2^-3 (2^-17 of the bound).  Rows of 256 x
+// 512 that are 1e-6 as large as the others were off by 3.2e-4 then; times 2^11, lo is
+// as large as hi, 22 bits reach down to 2^-14, 2^-28 of the bound, and those rows are
+// off by 2.8e-7, an f32 form's by 3.5e-7.  The sums of hi lo and lo hi are then 2^11
+// times as large as those of hi hi and wait for their own place in registers, or for
+// their own turn (TWICE below).
 //
 // A and B are symmetric: only tiles on and above the diagonal are computed, and
 // each is stored twice.  Where A has few of them, workgroups take slices of its
@@ -35,7 +42,12 @@
 // 1024 x 1024 12 / 26 / 25 us); tiles of 128 likewise while there is one a unit (4
 // / 2 stages: 136 tiles of 64 runs 46 / 62 us), two a unit hide each other's ways
 // (363 tiles of 44 runs 74 / 55); tiles of 256 have LDS for two stages, and 96
-// products a run to hide their loads.
+// products a run to hide their loads.  Tiles of 256 that sum twice have 64 products a
+// run and more to read for each: five stages of one operand, all of the LDS, where
+// each is filled again as soon as it is free, 7.26 ms for 8 x 4096 x 2048 in f32, two
+// of both 7.42 (the joined sums of bf16 6.37); matrix units busy 61 - 74 % of the
+// clocks instead of 74 - 86, for half as many LDS reads again and 64-byte lines in the
+// second turn.
 #include <type_traits>
 
 #include "cbd_device.h"
@@ -59,10 +71,11 @@ constexpr int THREADS = 256;
 
 __device__ inline uint16_t half_bits(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
 __device__ inline float half_value(uint32_t b) { return (float)__builtin_bit_cast(_Float16, (uint16_t)b); }
-// The two halves of a value: hi in bits 0-15, lo in bits 16-31.
-__device__ inline uint32_t split(float v) {
+// The two halves of a value: hi in bits 0-15, lo, `up` times what hi leaves, in
+// bits 16-31.
+__device__ inline uint32_t split(float v, float up) {
   const uint16_t hi = half_bits(v);
-  return hi | (uint32_t)half_bits(v - half_value(hi)) << 16;
+  return hi | (uint32_t)half_bits((v - half_value(hi)) * up) << 16;
 }
 
 // s_waitcnt: every load and LDS access is done.
@@ -106,13 +119,13 @@ __device__ inline void upper_tile(int local, int n, int W, int& mt, int& nt) {
   }
 }
 
-template <int MB, int STAGE, int NS>
+template <int MB, int STAGE, int NS, bool TWICE = false>
 __global__ __launch_bounds__(THREADS, MB == 4 || (MB == 2 && NS > 2) ? 1 : 2) void ortho_product_kernel(const OrthoArgs a) {
   constexpr int T = 64 * MB;
   constexpr int BYTES = T * 128;      // of an operand's stage
   constexpr int N = BYTES / 4096;     // 1 KiB blocks of it that a wave fills
   constexpr bool SLICE = STAGE == ORTHO_SLICE, SYM = STAGE == ORTHO_SQUARE || STAGE == ORTHO_POLY || SLICE;
-  __shared__ __attribute__((aligned(1024))) char smem[2 * NS * BYTES];
+  __shared__ __attribute__((aligned(1024))) char smem[TWICE ? 5 * BYTES : 2 * NS * BYTES];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave & 1, wn = wave >> 1;
 
@@ -184,6 +197,15 @@ __global__ __launch_bounds__(THREADS, MB == 4 || (MB == 2 && NS > 2) ? 1 : 2) vo
   auto load_q = [&](int k, int s, int i) INLINE {
     issue(bq, k < runs ? rec_q : 0u, vq[i], (uint32_t)k * 128u, base + (uint32_t)((2 * s + 1) * BYTES + i * 1024));
   };
+  // The same where after the runs come their hi alone, 64 of them at a time: chunks
+  // 4 .. 7 of a row are then those of the next run, 64 bytes further on than its lo.
+  // (c / 4 of the chunks above, with N * wave even.)
+  const int doubles = (runs + 1) / 2;
+  [[maybe_unused]] const uint32_t further[2] = {(uint32_t)(lane & 4) << 4, (uint32_t)(~lane & 4) << 4};
+  [[maybe_unused]] auto load_twice = [&](uint64_t b, uint32_t rec, uint32_t voff, int k, int i, uint32_t m0v) INLINE {
+    const int h = k - runs;
+    issue(b, h < doubles ? rec : 0u, voff + (h < 0 ? 0u : further[i & 1]), (uint32_t)(h < 0 ? k * 128 : h * 256), m0v);
+  };
 
   // Fragments: 32 rows by 16 k; half h (0: hi, 1: lo) of k 16 ks ...
   int at_p[4], at_q[4];
@@ -203,9 +225,9 @@ __global__ __launch_bounds__(THREADS, MB == 4 || (MB == 2 && NS > 2) ? 1 : 2) vo
   };
 
   // Sums of hi hi and, apart where registers allow it, of hi lo and lo hi: these
-  // are 2^-11 of the others, and so are their roundings then (3 steps of 9
-  // matrices of 512 x 768 are off by 1.15e-6 together, 0.73e-6 apart; an f32 library
-  // product's form by 0.85e-6).
+  // are 2^-11 of the others, and so are their roundings then.  Tiles of 256 have
+  // registers for one set: they join the two kinds (lo_up is 1 then) or sum them
+  // one after the other (TWICE).
   constexpr bool APART = MB < 4;
   f32x16 acc[MB][MB], low[APART ? MB : 1][APART ? MB : 1];
 
@@ -238,7 +260,72 @@ __global__ __launch_bounds__(THREADS, MB == 4 || (MB == 2 && NS > 2) ? 1 : 2) vo
   constexpr std::integral_constant<int, N> all{};
   auto nothing = [](int) {};
 
-  if constexpr (NS > 2) {
+  if constexpr (TWICE) {
+    // All runs for hi lo and lo hi, then all of them again, 64 k at a time, for hi hi.
+    // LDS is a ring of five stages of one operand: run k's are 2 k and 2 k + 1, modulo
+    // 5.  While run k is multiplied, the first operand of run k + 2 goes to the stage
+    // before them (everyone has read it: the last barrier), and the second, once
+    // everyone has read run k, to its first stage.  Before that barrier run k + 1 has
+    // landed, and only the loads of the first operand of k + 2 may be on their way.
+    static_assert(MB == 4 && !SLICE && 5 * BYTES <= 163840, "a run's 64 products a wave, and all of the LDS");
+    const int total = runs + doubles;
+    auto load_p2 = [&](int k, uint32_t s, int i) INLINE {
+      load_twice(bp, rec_p, vp[i], k, i, base + s + (uint32_t)(i * 1024));
+    };
+    auto load_q2 = [&](int k, uint32_t s, int i) INLINE {
+      load_twice(bq, rec_q, vq[i], k, i, base + s + (uint32_t)(i * 1024));
+    };
+    f16x8 x0[MB], y0[MB], x1[MB], y1[MB];
+    auto read = [&](uint32_t at, int b) INLINE { return *(const f16x8*)(smem + at + b * 4096); };
+    auto both = [&](uint32_t p, uint32_t q, int r, f16x8 (&x)[MB], f16x8 (&y)[MB]) INLINE {
+      r < MB ? (void)(x[r] = read(p, r)) : (void)(y[r - MB] = read(q, r - MB));
+    };
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+#pragma unroll
+      for (int i = 0; i < N; i++) load_p2(k, (uint32_t)(2 * k * BYTES), i);
+#pragma unroll
+      for (int i = 0; i < N; i++) load_q2(k, (uint32_t)((2 * k + 1) * BYTES), i);
+    }
+    wait_loads<2 * N>();
+    barrier();
+    uint32_t sp = 0, sq = BYTES;  // the stages of run k
+#pragma unroll
+    for (int r = 0; r < 2 * MB; r++) both(at_p[0] + sp, at_q[2] + sq, r, x0, y0);
+    auto run = [&](int k, auto crossc, auto firstc) INLINE {
+      constexpr bool CROSS = decltype(crossc)::value;
+      // Which quarter (hi of k 0-15, hi of 16-31, then lo or the next run's hi) of
+      // either operand a part of 16 k takes.
+      constexpr int P[4] = {0, CROSS ? 2 : 1, CROSS ? 1 : 2, 3}, Q[4] = {CROSS ? 2 : 0, CROSS ? 0 : 1, CROSS ? 3 : 2, CROSS ? 1 : 3};
+      const uint32_t before = sp == 0 ? 4 * BYTES : sp - BYTES, old = sp;
+      part(firstc, hi, x0, y0, two, [&](int r) { both(at_p[P[1]] + sp, at_q[Q[1]] + sq, r, x1, y1); }, all,
+           [&](int i) { load_p2(k + 2, before, i); });
+      part(lo, hi, x1, y1, two, [&](int r) { both(at_p[P[2]] + sp, at_q[Q[2]] + sq, r, x0, y0); }, none, nothing);
+      part(lo, hi, x0, y0, two, [&](int r) { both(at_p[P[3]] + sp, at_q[Q[3]] + sq, r, x1, y1); }, none, nothing);
+      wait_loads<N, 0>();
+      barrier();
+      sp = sp >= 3 * BYTES ? sp - 3 * BYTES : sp + 2 * BYTES;
+      sq = sq >= 3 * BYTES ? sq - 3 * BYTES : sq + 2 * BYTES;
+      const uint32_t next = k + 1 < runs ? at_q[2] : at_q[0];
+      part(lo, hi, x1, y1, two, [&](int r) { both(at_p[0] + sp, next + sq, r, x0, y0); }, all,
+           [&](int i) { load_q2(k + 2, old, i); });
+    };
+    run(0, std::true_type(), std::true_type());
+#pragma unroll 1
+    for (int k = 1; k < runs; k++) run(k, std::true_type(), std::false_type());
+#pragma unroll
+    for (int m = 0; m < MB; m++)
+#pragma unroll
+      for (int n = 0; n < MB; n++) {
+        // (One block at a time: all of them find no room outside the accumulation registers.)
+        asm volatile("" : "+a"(acc[m][n]));
+        acc[m][n] *= a.lo_down;
+        asm volatile("" : "+a"(acc[m][n]));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll 1
+    for (int k = runs; k < total; k++) run(k, std::false_type(), std::false_type());
+  } else if constexpr (NS > 2) {
     // One workgroup's matrix instructions hide neither a load's nor an LDS
     // read's way: NS - 1 runs are in flight, and one is read ahead.
     auto load = [&](int k, int s) INLINE {
@@ -367,7 +454,7 @@ __global__ __launch_bounds__(THREADS, MB == 4 || (MB == 2 && NS > 2) ? 1 : 2) vo
       const int row0 = m0 + 32 * m, col = n0 + 32 * n + r;
       float v[16];
 #pragma unroll
-      for (int j = 0; j < 16; j++) v[j] = (APART ? acc[m][n][j] + low[APART ? m : 0][APART ? n : 0][j] : acc[m][n][j]) * a.mul;
+      for (int j = 0; j < 16; j++) v[j] = (APART ? __builtin_fmaf(low[APART ? m : 0][APART ? n : 0][j], a.lo_down, acc[m][n][j]) : acc[m][n][j]) * a.mul;
       // (A power of two and the scale apart: together they may be below f32's normal
       // numbers where the result is not.)
       if constexpr (STAGE == ORTHO_LAST) {
@@ -382,7 +469,8 @@ __global__ __launch_bounds__(THREADS, MB == 4 || (MB == 2 && NS > 2) ? 1 : 2) vo
           const u32x2 x = o[q], y = o[4 + q];
 #pragma unroll
           for (int j = 0; j < 4; j++) {
-            const float w = half_value(x[j >> 1] >> (16 * (j & 1))) + half_value(y[j >> 1] >> (16 * (j & 1)));
+            const float w =
+                __builtin_fmaf(half_value(y[j >> 1] >> (16 * (j & 1))), a.lo_down, half_value(x[j >> 1] >> (16 * (j & 1))));
             v[4 * q + j] = __builtin_fmaf(a.p_mul, w, v[4 * q + j]);
             if (row0 + 8 * q + 4 * upper + j == col) v[4 * q + j] += a.diag;
           }
@@ -445,7 +533,7 @@ __global__ __launch_bounds__(THREADS, MB == 4 || (MB == 2 && NS > 2) ? 1 : 2) vo
 #pragma unroll
         for (int j = 0; j < 16; j++) {
           const int row = row0 + 8 * (j >> 2) + 4 * upper + (j & 3);
-          w[j] = row < a.rows && col < a.cols ? split(v[j]) : 0u;
+          w[j] = row < a.rows && col < a.cols ? split(v[j], a.lo_up) : 0u;
         }
         // As C^T, row `col`: four neighbouring elements of a lane at a time, both
         // halves of one in a word.
@@ -511,7 +599,7 @@ __global__ __launch_bounds__(THREADS) void ortho_join_kernel(const OrthoArgs a) 
   uint32_t w[4];
 #pragma unroll
   for (int j = 0; j < 4; j++) {
-    w[j] = row0 + e + j < a.rows && col0 + i < a.cols ? split(v[j] * a.mul) : 0u;
+    w[j] = row0 + e + j < a.rows && col0 + i < a.cols ? split(v[j] * a.mul, a.lo_up) : 0u;
     block[i][e + j] = w[j];
   }
   auto leave = [&](uint16_t* o) INLINE {
@@ -582,14 +670,17 @@ __global__ __launch_bounds__(THREADS) void ortho_split_kernel(const OrthoSplit a
   __shared__ uint32_t tile[64][65];
   const int64_t mat = blockIdx.z;
   const int row0 = blockIdx.y * 64, col0 = blockIdx.x * 64, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  // (From inside always: loads in branches would each be waited for.)
+  const int col = col0 + lane < a.cols ? col0 + lane : a.cols - 1;
   float v[16];
 #pragma unroll
   for (int i = 0; i < 16; i++) {
-    const int row = 4 * i + wave;
-    v[i] = row0 + row < a.rows && col0 + lane < a.cols
-               ? value<T>(a.in, mat * a.in_mat + (int64_t)(row0 + row) * a.in_row + col0 + lane)
-               : 0.f;
+    const int row = row0 + 4 * i + wave < a.rows ? row0 + 4 * i + wave : a.rows - 1;
+    v[i] = value<T>(a.in, mat * a.in_mat + (int64_t)row * a.in_row + col);
   }
+#pragma unroll
+  for (int i = 0; i < 16; i++)
+    if (row0 + 4 * i + wave >= a.rows || col0 + lane >= a.cols) v[i] = 0.f;
   // Every wave adds the parts in the same order.
   double s = 0.0;
 #pragma unroll
@@ -598,11 +689,11 @@ __global__ __launch_bounds__(THREADS) void ortho_split_kernel(const OrthoSplit a
   for (int m = 32; m > 0; m >>= 1) s += __shfl_xor(s, m, 64);
   // The factor as m 2^e: it may be past f32, and products in 64 bits take a third
   // of the time that 16 x 256 x 512 take (14 us; 9 so).
-  // (Zeros stay zeros with an eps whose inverse is past f64, too.)
   int e2;
-  const float m2 = (float)frexp(s == 0.0 ? 0.0 : a.up / (__builtin_sqrt(s) + a.eps), &e2);
+  float m2 = (float)frexp(a.up / (__builtin_sqrt(s) + a.eps), &e2);
+  if (s == 0.0) m2 = 0.f;  // zeros, also where the inverse of eps is past f64
 #pragma unroll
-  for (int i = 0; i < 16; i++) tile[4 * i + wave][lane] = split(ldexpf(v[i], e2) * m2);
+  for (int i = 0; i < 16; i++) tile[4 * i + wave][lane] = split(ldexpf(v[i], e2) * m2, a.lo_up);
   __syncthreads();
   // A row of the tile is two runs, 16 pieces of 16 bytes: a lane takes one.
   const int piece = lane & 15, e = 32 * (piece >> 3) + 8 * (piece & 3);
@@ -626,8 +717,9 @@ __global__ __launch_bounds__(THREADS) void ortho_split_kernel(const OrthoSplit a
 }
 
 template <int STAGE>
-const void* pick(int tile, int64_t tiles) {
-  if (tile == 256) return (const void*)&ortho_product_kernel<4, STAGE, 2>;
+const void* pick(int tile, int64_t tiles, bool twice) {
+  if (tile == 256)
+    return twice ? (const void*)&ortho_product_kernel<4, STAGE, 2, true> : (const void*)&ortho_product_kernel<4, STAGE, 2>;
   if (tile == 64) return (const void*)&ortho_product_kernel<1, STAGE, 5>;
   return tiles <= 256 ? (const void*)&ortho_product_kernel<2, STAGE, 4>
                       : (const void*)&ortho_product_kernel<2, STAGE, 2>;
@@ -659,10 +751,10 @@ int launch_ortho_product(const OrthoArgs& a, int stage, int tile, int64_t matric
   const int64_t per = stage == ORTHO_SLICE ? (int64_t)a.tiles_m * (a.tiles_m + 1) / 2 * a.slices
                       : sym                ? (int64_t)a.tiles_m * (a.tiles_m + 1) / 2 : (int64_t)a.tiles_m * a.tiles_n;
   const void* k = stage == ORTHO_SLICE ? (const void*)&ortho_product_kernel<1, ORTHO_SLICE, 5>
-                  : stage == ORTHO_SQUARE ? pick<ORTHO_SQUARE>(tile, per * matrices)
-                  : stage == ORTHO_POLY ? pick<ORTHO_POLY>(tile, per * matrices)
-                  : stage == ORTHO_STEP ? pick<ORTHO_STEP>(tile, per * matrices)
-                                        : pick<ORTHO_LAST>(tile, per * matrices);
+                  : stage == ORTHO_SQUARE ? pick<ORTHO_SQUARE>(tile, per * matrices, a.lo_up != 1.f)
+                  : stage == ORTHO_POLY ? pick<ORTHO_POLY>(tile, per * matrices, a.lo_up != 1.f)
+                  : stage == ORTHO_STEP ? pick<ORTHO_STEP>(tile, per * matrices, a.lo_up != 1.f)
+                                        : pick<ORTHO_LAST>(tile, per * matrices, a.lo_up != 1.f);
   return (int)hipLaunchKernel(k, dim3((unsigned)(per * matrices)), dim3(THREADS), args, 0, (hipStream_t)stream);
 }
 

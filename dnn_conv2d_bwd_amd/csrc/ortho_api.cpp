@@ -160,6 +160,12 @@ cbd_status make_plan(const cbd_ortho_problem* q, cbd_ortho_plan_t** out) {
       if (shares[i].count * std::max(step(shares[i].tile), sym(shares[i].tile)) > cbd::host::kMaxGrid)
         return fail(CBD_ERR_UNSUPPORTED, "too many tiles for one launch");
     }
+  // Tiles of 256 take 1.14 times as long where lo is scaled, which makes them sum hi
+  // lo and lo hi, then hi hi (5 steps of 8 matrices of 4096 x 2048 7.26 ms, 6.37).  So
+  // bf16 updates with such tiles go without: their values have 22 bits down to 2^-17
+  // of the bounds below, not to 2^-28, and are off by 2^-39 of them at most, where
+  // the results have 8 bits.
+  p->lo_up = q->dtype == CBD_BF16 && pad == 256 ? 1.f : 2048.f;
   p->sp = up_to(p->s, pad);
   p->lp = up_to(p->l, pad);
   *out = p.release();
@@ -239,6 +245,7 @@ cbd_status run(const cbd_ortho_plan_t* plan, const void* in, void* out, const cb
   f.partial = partial;
   f.eps = q.eps;
   f.up = std::ldexp(1.0, plan->ex[0]);
+  f.lo_up = plan->lo_up;
   f.x = tall ? xt : x;
   f.ldx = tall ? ldxt : ldx;
   f.xt = tall ? x : xt;
@@ -254,6 +261,8 @@ cbd_status run(const cbd_ortho_plan_t* plan, const void* in, void* out, const cb
     for (const cbd::OrthoShare& h : shares) {
       if (!h.count || err) continue;
       cbd::OrthoArgs a = all;
+      a.lo_up = plan->lo_up;
+      a.lo_down = 1.f / plan->lo_up;
       a.p += first * a.p_mat;
       a.q += first * a.q_mat;
       if (a.c) a.c += first * a.c_mat;
@@ -287,6 +296,7 @@ cbd_status run(const cbd_ortho_plan_t* plan, const void* in, void* out, const cb
       product(a, cbd::ORTHO_SLICE, plan->sym);
       a.mul = mul;
       a.tiles_m = a.tiles_n = tiles(plan->s, 64);
+      a.lo_up = plan->lo_up;
       if (!err) err = cbd::launch_ortho_join(a, n, stream);
     } else {
       product(a, cbd::ORTHO_SQUARE, plan->sym);

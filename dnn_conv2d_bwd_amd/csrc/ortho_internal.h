@@ -9,8 +9,8 @@
 namespace cbd {
 
 // Split matrices: a value v is held as two halves, hi = half(v 2^e) and lo =
-// half(v 2^e - hi), with one exponent e for the matrix.  Rows are runs of 64
-// halves: hi of 32 neighbouring elements, then their lo.
+// half((v 2^e - hi) lo_up), with one exponent e for the matrix and lo_up 2^11 or 1.
+// Rows are runs of 64 halves: hi of 32 neighbouring elements, then their lo.
 //
 // X is the matrix with its smaller side as rows (S of them, L columns); it is
 // kept in both directions, since each product contracts along rows of both its
@@ -36,6 +36,7 @@ struct OrthoArgs {
   int64_t c_mat, ct_mat;
   int32_t ldc, ldct;
   float mul;                 // C is the products' sum times this
+  float lo_up, lo_down;      // what lo is multiplied by, and 1 / that
   float p_mul, diag;         // ORTHO_POLY: and P times p_mul, and diag on the diagonal
   void* out;                 // ORTHO_LAST
   float scale;               // and the result is C times this
@@ -51,6 +52,7 @@ struct OrthoSplit {
   int32_t rows, cols, dtype;
   double* partial;           // [matrices][kOrthoParts] sums of squares
   double eps, up;            // up = 2^e
+  float lo_up;
   uint16_t *x, *xt;          // rows x cols in the input's direction, and the other
   int64_t x_mat, xt_mat;
   int32_t ldx, ldxt;
@@ -78,6 +80,7 @@ struct cbd_ortho_plan_s {
   int64_t s, l, sp, lp;               // sides, and their padded lengths
   cbd::OrthoShare sym[2], step[2];    // how A and B, and X, are computed
   int64_t slices, slice;              // of A's sums, in runs; slices is 1 where they are not split
+  float lo_up;                        // of the split values
   // Exponents of X before each step, of A and of B.
   std::vector<int> ex, ea, eb;
 };

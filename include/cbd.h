@@ -620,7 +620,10 @@ cbd_status cbd_grad_clip(const cbd_grad_plan_t* plan, const void* const* grads, 
  * for each of the `matrices` M (rows x cols) by itself; with more rows than
  * columns the same polynomial is taken from the other side (A = X^T X).  The
  * norm is in 64 bits; products are of values of 22 bits with f32 sums, and the
- * result is rounded once to its type.  A zero matrix gives zeros; a NaN or
+ * result is rounded once to its type.  Values that are small next to their matrix
+ * have fewer bits: below 2^-28 of the bound that the coefficients give (1 for the
+ * first X) they are off by up to 2^-50 of it; in bf16 plans with tiles of 256 below
+ * 2^-17, by up to 2^-39.  A zero matrix gives zeros; a NaN or
  * infinity anywhere in a matrix gives NaN in all of it.  The same inputs give
  * the same bits. */
 typedef struct {

@@ -160,6 +160,52 @@ def test_slices(dtype, size):
     near(call(m, steps=3), m, dtype, str(size), steps=3)
 
 
+def near_in_parts(got, m, dtype, part, name="", steps=5, coarse=False):
+    """near's bound for each half of the rows (or columns) by itself, and what a
+    value that is small next to its matrix loses.
+
+    A stored value is off by at most 2^-50 of the plan's bound (bf16 with tiles of
+    256: 2^-39), where that is more than 2^-22 of itself; the bounds are at most 2 for X and A, 4 for B (powers of
+    two above 1.21, 1.46 and 3.45).  In a row of the smaller side that adds to a
+    step's result (norms, with |X| and |A| at most 1.46): sqrt(l) 2^-49 for X
+    itself; sqrt(s) 2^-49 times |b + 2 c A| <= 10.8 for A, and sqrt(s) 2^-48 for B,
+    both times |X|: sqrt(s) 2^-49 (10.8 + 2) 1.21.  A step makes at most 3.45
+    times as much of it.  A column has the same bound with the sides exchanged, so
+    both are taken."""
+    m = m.cuda()
+    want, plain = define(m, steps=steps).cpu(), define(m, steps=steps, f32=True).double().cpu()
+    got, half = got.double().cpu(), torch.finfo(TORCH[dtype]).eps / 2
+    s, l = min(m.shape[1:]), max(m.shape[1:])
+    floor = sum(3.45 ** k for k in range(steps + 1)) * 2.0 ** -49 * (l ** 0.5 + 15.5 * (s ** 0.5 + l ** 0.5))
+    floor *= 2.0 ** 11 if coarse else 1.0
+    n = m.shape[part + 1] // 2
+    for i in range(m.shape[0]):
+        for at in (slice(0, n), slice(n, None)):
+            w, g, p = ((v[i][at] if part == 0 else v[i][:, at]) for v in (want, got, plain))
+            ok = 4 * (p - w).norm() + (2.0 ** -22 + half) * w.norm() + floor * w.shape[part] ** 0.5
+            err = (g - w).norm()
+            assert err <= ok, f"{name} matrix {i}, {at}: {float(err / w.norm())} off, {float(ok / w.norm())} allowed"
+
+
+# Tiles of 64, of 64 in slices, of 128 with one and with two a unit, of 256, both ways.
+PARTED = [(2, 256, 512), (2, 200, 64), (1, 100, 3000), (9, 700, 1100), (20, 700, 600), (25, 1090, 1000), (32, 512, 1408)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("small,dtype", [(1e-4, "f32"), (1e-6, "f32"), (1e-5, "bf16"), (1e-8, "bf16")])
+@pytest.mark.parametrize("size", PARTED, ids=str)
+def test_rows_and_columns_of_different_size(size, small, dtype):
+    """Rows that a gradient seldom reaches keep an accuracy of their own."""
+    for part in (0, 1):
+        print("[ortho] parts", size, small, part, dtype, flush=True)
+        m = draw(*size, seed=size[1])
+        (m[:, size[1] // 2:] if part == 0 else m[:, :, size[2] // 2:]).mul_(small)
+        m = m.to(TORCH[dtype])
+        some, steps, i = [0, size[0] - 1][:size[0]], 5 if min(size[1:]) < 500 else 3, cbd.ortho_plan(*size, dtype).info()
+        tiles = i.tile_symmetric, i.tile_symmetric_rest, i.tile_step, i.tile_step_rest
+        near_in_parts(call(m, steps=steps)[some], m[some], dtype, part, f"{size} {small} {part}", steps, dtype == "bf16" and 256 in tiles)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("gap,space,off", [(8, 0, 0), (1, 0, 1), (0, 3, 0), (5, 2, 3)])
 def test_strides_and_alignment(gap, space, off):
