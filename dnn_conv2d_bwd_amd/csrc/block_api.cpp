@@ -46,6 +46,11 @@ cbd_status make_plan(const cbd_block_problem* q, cbd_block_plan_t** out) {
   const int active = std::min(chunks, p->shape.lanes) * per, wanted = (512 + active / 2) / active;
   p->grid_fwd = std::min<int64_t>(groups, 256 * (2048 / threads));
   p->grid_bwd = std::min<int64_t>(groups, 256 * std::max(1, std::min(wanted, most)));
+  // Sums that are held in LDS are of no more than kBlockJoin rows each, with more
+  // workgroups than the card has at once; past 4096 of them (2^19 rows, 9 GB at least)
+  // of a 4096th of the rows.
+  if (!cbd::block_held(p->shape.chunks, esize(q->dtype)))
+    p->grid_bwd = std::max(p->grid_bwd, std::min<int64_t>((q->rows + cbd::kBlockJoin - 1) / cbd::kBlockJoin, 4096));
   // A few rows (groups of them) by one workgroup, which then needs no second
   // launch to join its sums with others' (one / many and the joining, us: a row of
   // 4096 9.1 / 12.9, four 13.1 / 13.1, eight 18.2 / 13.2; four groups of four rows

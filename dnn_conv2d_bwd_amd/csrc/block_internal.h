@@ -48,6 +48,10 @@ inline BlockShape block_shape(int64_t c, int es) {
     if (chunks <= lanes) return {lanes, 1};
   return {1024, chunks <= 2048 ? 2 : 4};
 }
+// Backward, whether a thread holds its columns' sums in registers, or in LDS.
+constexpr bool block_held(int chunks, int es) { return chunks * 16 / es <= 8; }
+// Rows that one f32 sum of a column takes at most.
+constexpr int kBlockJoin = 128;
 inline int block_threads(BlockShape s) { return s.lanes <= 64 ? 256 : s.lanes; }
 
 }  // namespace cbd

@@ -17,8 +17,9 @@
 // A row stays in registers from its one load to its stores, 16 bytes a thread: a
 // workgroup (or, up to 64 threads a row, a part of one) takes rows i, i + grid,
 // ..., loads the next one before it joins the sums of this one, and keeps its
-// columns' sums in registers to the end, from where they go to memory, one row of
-// them a workgroup, for a second launch to join in a fixed order.  z is rounded
+// columns' sums in registers for 128 rows, then adds them up in LDS; in the end they
+// go to memory, one row of them a workgroup, for a second launch to join in a fixed
+// order.  z is rounded
 // where it is stored, not where n is made of it.
 //
 // Bound: HBM.  32768 x 4096 in bf16, vectors for all three: forward 212 us (5.1
@@ -166,7 +167,7 @@ constexpr bool kAhead = CH == 1;
 // bf16 166 us, held, with spills, 484; of 16384 224 / 503; 2048 rows of 16384 in
 // f32 300 / 495; 4096 of 8192, which fit, 161 held and 211 read again).
 template <typename T, int CH>
-constexpr bool kHeld = CH * sizeof(u32x4) / sizeof(T) <= 8;
+constexpr bool kHeld = block_held(CH, sizeof(T));
 
 // What a thread has of its rows: CH chunks, LANES chunks apart.
 template <typename T, int LANES, int CH>
@@ -321,9 +322,11 @@ __device__ inline void finish_column(const BlockFinish& a, int which, int col, d
   }
 }
 
-template <typename T, int LANES, int CH>
+// SECOND: there is a second norm (a.w_pre), known beforehand.
+template <typename T, int LANES, int CH, bool SECOND = false>
 __global__ __launch_bounds__(kThreads<LANES>, (kWaves<LANES, CH>)) void block_bwd_kernel(const BlockArgs a) {
   constexpr int N = Chunk<T>::N;
+  const bool second = SECOND || a.w_pre;
   constexpr bool HELD = kHeld<T, CH>;
   __shared__ float part[2][3][RowSum<LANES, 3>::W];
   RowSum<LANES, 3> sum{part};
@@ -359,6 +362,30 @@ __global__ __launch_bounds__(kThreads<LANES>, (kWaves<LANES, CH>)) void block_bw
       leave(post[i], CH + i);
     }
   }
+  // No second norm or no dn: dw_pre is 0, not the sum of 0 times what r holds.
+  auto first = [&](int i, int j) { return second ? pre[i][j] : 0.f; };
+  // The columns' sums go on to LDS and begin again after every kBlockJoin rows: one f32
+  // sum of many rows would lose what is small next to all of them.  (Where LDS holds
+  // the sums themselves the plan has a workgroup for as many rows.)
+  float* const out = a.partial + (int64_t)blockIdx.x * 2 * a.c;
+  __shared__ float join[2][HELD ? CH * N : 1][HELD ? kThreads<LANES> : 1];
+  int since = 0;
+  bool more = false;
+  auto pass_on = [&]() {
+    int tid = LANES > 64 ? rows.lane : (int)threadIdx.x;
+    asm volatile("" : "+v"(tid));  // no addresses in registers through the loop over rows
+#pragma unroll
+    for (int i = 0; i < CH; i++)
+#pragma unroll
+      for (int j = 0; j < N; j++) {
+        float &u = join[0][i * N + j][tid], &v = join[1][i * N + j][tid];
+        u = more ? u + first(i, j) : first(i, j);
+        v = more ? v + post[i][j] : post[i][j];
+        pre[i][j] = post[i][j] = 0.f;
+      }
+    more = true;
+    since = 0;
+  };
   Chunk<T> r[CH], y[CH], g[CH], dz[CH], dn[CH];
   float ry1 = 1.f, rz1 = 1.f;
   Rows<T, LANES, CH>::zero(y);
@@ -368,12 +395,12 @@ __global__ __launch_bounds__(kThreads<LANES>, (kWaves<LANES, CH>)) void block_bw
     rows.load(r[i], a.r, row * a.ldr, i);
     if (a.y) rows.load(y[i], a.y, row * a.ldy, i);
     if (a.dz) rows.load(dz[i], a.dz, row * a.lddz, i);
-    if (a.dn) rows.load(dn[i], a.dn, row * a.lddn, i);
+    if (SECOND || a.dn) rows.load(dn[i], a.dn, row * a.lddn, i);
     if (a.gate_rows) rows.load(g[i], a.gate, row * a.ldgate, i);
   };
   auto statistics = [&](int64_t row) {
     if (a.w_post) ry1 = a.stats[2 * row];
-    if (a.w_pre) rz1 = a.stats[2 * row + 1];
+    if (second) rz1 = a.stats[2 * row + 1];
   };
   auto fetch_all = [&](int64_t row) {
 #pragma unroll
@@ -434,8 +461,8 @@ __global__ __launch_bounds__(kThreads<LANES>, (kWaves<LANES, CH>)) void block_bw
     if (kAhead<CH> && row + rows.step < a.rows) fetch_all(row + rows.step);
     sum(s);
     // (Where there is no norm, nothing is taken off: not 0 times infinity.)
-    const float along = a.w_pre ? rz * s[0] * inv_c : 0.f;                 // of zn in dz'
-    const float back = (a.w_pre ? s[1] - along * s[2] : s[1]) * inv_c;  // of yn in dy
+    const float along = second ? rz * s[0] * inv_c : 0.f;                 // of zn in dz'
+    const float back = (second ? s[1] - along * s[2] : s[1]) * inv_c;  // of yn in dy
 #pragma unroll
     for (int i = 0; i < CH; i++) {
       if (!HELD) {
@@ -446,7 +473,7 @@ __global__ __launch_bounds__(kThreads<LANES>, (kWaves<LANES, CH>)) void block_bw
       float fr[N], fy[N], fg[N];
 #pragma unroll
       for (int j = 0; j < N; j++) {
-        fr[j] = a.w_pre ? __builtin_fmaf(-along, zn[i][j], e[i][j]) : e[i][j];
+        fr[j] = second ? __builtin_fmaf(-along, zn[i][j], e[i][j]) : e[i][j];
         const float da = a.scale * fr[j], dg = da * gr[i].get(j), w = wq[i].get(j);
         fg[j] = da * yn[i][j] * w;
         post[i][j] = __builtin_fmaf(a.gate_rows ? dg : da, yn[i][j], post[i][j]);
@@ -461,23 +488,15 @@ __global__ __launch_bounds__(kThreads<LANES>, (kWaves<LANES, CH>)) void block_bw
       if (a.dgate) rows.store(o_g, a.dgate, row * a.lddgate, i);
       if (!HELD) __builtin_amdgcn_sched_barrier(0);
     }
+    if constexpr (HELD)
+      if (++since == kBlockJoin && a.partial) pass_on();
   }
   const bool alone = gridDim.x == 1;  // no one to join
   if (!a.partial) return;
-  // No second norm or no dn: dw_pre is 0, not the sum of 0 times what r holds.
-  auto first = [&](int i, int j) { return a.w_pre ? pre[i][j] : 0.f; };
-  float* const out = a.partial + (int64_t)blockIdx.x * 2 * a.c;
+  if constexpr (HELD) pass_on();
   if constexpr (LANES <= 64) {
     // The groups' sums, joined in their order.
     constexpr int G = 256 / LANES, COLS = LANES * CH * N;
-    __shared__ float join[2][CH * N][256];
-#pragma unroll
-    for (int i = 0; i < CH; i++)
-#pragma unroll
-      for (int j = 0; j < N; j++) {
-        join[0][i * N + j][threadIdx.x] = first(i, j);
-        join[1][i * N + j][threadIdx.x] = post[i][j];
-      }
     __syncthreads();
     for (int k = threadIdx.x; k < 2 * COLS; k += 256) {
       const int which = k / COLS, col = k % COLS, i = col / (N * LANES), lane = col / N % LANES, j = col % N;
@@ -491,26 +510,30 @@ __global__ __launch_bounds__(kThreads<LANES>, (kWaves<LANES, CH>)) void block_bw
           out[which * a.c + col] = s;
       }
     }
-    return;
-  }
+  } else {
+    int lane = rows.lane;
+    asm volatile("" : "+v"(lane));  // (as above)
 #pragma unroll
-  for (int i = 0; i < CH; i++) {
-    const int at = N * (rows.lane + LANES * i);
-    if (!HELD) {
-      take(pre[i], i);
-      take(post[i], CH + i);
-    }
-#pragma unroll
-    for (int j = 0; j < N; j++)
-      if (at + j < a.c) {
-        if (alone) {
-          finish_column(a.finish, 0, at + j, first(i, j));
-          finish_column(a.finish, 1, at + j, post[i][j]);
-        } else {
-          out[at + j] = first(i, j);
-          out[a.c + at + j] = post[i][j];
-        }
+    for (int i = 0; i < CH; i++) {
+      const int at = N * (lane + LANES * i);
+      if (!HELD) {
+        take(pre[i], i);
+        take(post[i], CH + i);
       }
+#pragma unroll
+      for (int j = 0; j < N; j++)
+        if (at + j < a.c) {
+          const float u = HELD ? join[0][HELD ? i * N + j : 0][lane] : first(i, j);
+          const float v = HELD ? join[1][HELD ? i * N + j : 0][lane] : post[i][j];
+          if (alone) {
+            finish_column(a.finish, 0, at + j, u);
+            finish_column(a.finish, 1, at + j, v);
+          } else {
+            out[at + j] = u;
+            out[a.c + at + j] = v;
+          }
+        }
+    }
   }
 }
 
@@ -535,8 +558,13 @@ __global__ __launch_bounds__(FINISH) void block_finish_kernel(const BlockFinish 
 }
 
 template <typename T, bool BWD>
-const void* pick(BlockShape s) {
+const void* pick(BlockShape s, bool second) {
   constexpr int F = sizeof(T) / 2;
+  // bf16 rows that are read twice, which are short of registers, with a second norm:
+  // 4096 x 10240 166 us, with the question left open 172 (f32, 2048 x 16384, which
+  // spills: 318 / 308).
+  if constexpr (BWD && F == 1)
+    if (second && !block_held(s.chunks, sizeof(T))) return (const void*)&block_bwd_kernel<T, 1024, 2, true>;
 #define CBD_BLOCK(L, C) \
   if (s.lanes == L && s.chunks == C) return BWD ? (const void*)&block_bwd_kernel<T, L, C> : (const void*)&block_forward_kernel<T, L, C>;
   CBD_BLOCK(8, 1)
@@ -557,7 +585,7 @@ const void* pick(BlockShape s) {
 
 template <bool BWD>
 int launch(const BlockArgs& a, BlockShape s, int dtype, int64_t grid, void* stream) {
-  const void* k = dtype == CBD_F32 ? pick<float, BWD>(s) : pick<uint16_t, BWD>(s);
+  const void* k = dtype == CBD_F32 ? pick<float, BWD>(s, a.w_pre) : pick<uint16_t, BWD>(s, a.w_pre);
   void* args[] = {const_cast<BlockArgs*>(&a)};
   return (int)hipLaunchKernel(k, dim3((unsigned)grid), dim3(block_threads(s)), args, 0,
                               (hipStream_t)stream);

@@ -514,8 +514,9 @@ cbd_status cbd_expert_gated_info(const cbd_expert_plan_t* plan, int32_t bwd, cbd
  * Everything is computed in f32 from the inputs, sums included (a row whose
  * squares pass f32's range has norm(v) = 0), and each result is rounded once;
  * n is made of the unrounded z.  A row's results do not depend on other rows.
- * The vectors' gradients add up f32 sums of rows in a fixed order: the same
- * inputs give the same bits.  No rows: they are 0.  z may be r itself, n y
+ * The vectors' gradients add up f32 sums of at most 128 rows (past 8192 elements a
+ * row and 2^19 rows: a 4096th of them) in a fixed order: the same inputs give the
+ * same bits.  No rows: they are 0.  z may be r itself, n y
  * itself, dr dz itself and dy dn itself (the same address and row stride). */
 typedef enum { CBD_GATE_NONE = 0, CBD_GATE_CHANNEL = 1, CBD_GATE_ROW = 2 } cbd_gate_kind;
 

@@ -341,6 +341,27 @@ def test_wide_rows(dtype, c):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,rows,c", [("bf16", 1 << 19, 4096), ("bf16", 1 << 22, 512), ("f32", 1 << 21, 512), ("bf16", 1 << 19, 8200),
+                                          ("bf16", 1 << 24, 64)])
+def test_sums_of_many_rows(dtype, rows, c):
+    """A column's sum of equal terms just below 1, which one f32 sum of 2048 rows
+    would take as 1 from the 512th on: 3 / 4 of 2.99e-5 off.  128 rows at a time,
+    a term is in at most 128 additions of its thread's, one for each 128 rows, 32
+    of a workgroup's and one rounding, each off by at most 2^-24 of the sum."""
+    print("[block] many rows", dtype, rows, c, flush=True)
+    p = cbd.block_plan(rows, c, dtype, "f32", scale=1 - 2.99e-5)
+    ones = torch.ones(rows, c, dtype=TORCH[dtype], device="cuda")
+    w, stats = torch.ones(c, dtype=TORCH[dtype], device="cuda"), torch.ones(rows, 2, device="cuda")
+    stats[:, 1] = 1 - 2.99e-5
+    tol = (128 + rows / 256 / 128 + 32 + 1) * 2.0 ** -24 * rows
+    # zn = r / rms and dn = 1; then scale * dz * y.
+    dw = cbd.block_bwd(p, None, ones, ones, stats=stats, w_pre=w, output_mask=(0, 0, 0, 0, 1))[4]
+    assert float((dw.double() - rows * stats[0, 1].double()).abs().max()) <= tol
+    dgate = cbd.block_bwd(p, ones, None, ones, ones, gate=w, output_mask=(0, 0, 0, 1, 0))[3]
+    assert float((dgate.double() - rows * torch.tensor(p.scale).float().double().cuda()).abs().max()) <= tol
+
+
+@pytest.mark.gpu
 def test_masks_and_empty():
     b = Block(17, 80, gate="row")
     whole = b.bwd()
