@@ -28,14 +28,15 @@
 // 8), so that reads of 32 rows spread over the banks.
 //
 // Bound: large matrices by the matrix instructions, at the rate that the card's
-// power allows.  8 x 4096 x 2048, a step: A 303 + 76 us (7 matrices in tiles of
-// 256, one in tiles of 128 for the units that those leave idle), B 174 + 48, X 655
-// (1.26 PFLOP/s of halves; a library product of 8192 x 8192 x 8192 in bf16 reaches
-// 1.26), the last 607 (1.36: it writes a quarter of the bytes); five steps with
-// norm (31 us, 4.3 TB/s) and split (115, 5.8 TB/s, two directions of 4 bytes
-// written) 6.3 - 6.6 ms.  Results leave through LDS in whole columns of blocks: 0.3 ms less
-// than block by block.  Small ones by latency: 16 x 256 x 512 takes 7 to 11 us a
-// launch for 8 to 16 runs.
+// power allows.  8 x 4096 x 2048 in bf16, a step: A 306 + 79 us (7 matrices in tiles
+// of 256, one in tiles of 128 for the units that those leave idle), B 176 + 49, X 675
+// (1.22 PFLOP/s of halves; a library product of 8192 x 8192 x 8192 in bf16 reaches
+// 1.26), the last 620 (1.33: it writes a quarter of the bytes); five steps with
+// norm (31 us, 4.3 TB/s) and split (103, 6.5 TB/s, two directions of 4 bytes
+// written) 6.3 - 6.6 ms.  In f32 A 362 + 79, B 198 + 49, X 760, the last 718, 7.3 ms.
+// Results leave through LDS in whole columns of blocks: 0.3 ms less than block by
+// block.  Small ones by latency: 16 x 256 x 512 takes 7 to 11 us a launch for 8 to 16
+// runs.
 //
 // Stages: one workgroup of 64 x 64 a compute unit waits for every load and LDS
 // read, so four runs are in flight and one in registers (5 / 3 / 2 stages: A of
@@ -45,7 +46,7 @@
 // products a run to hide their loads.  Tiles of 256 that sum twice have 64 products a
 // run and more to read for each: five stages of one operand, all of the LDS, where
 // each is filled again as soon as it is free, 7.26 ms for 8 x 4096 x 2048 in f32, two
-// of both 7.42 (the joined sums of bf16 6.37); matrix units busy 61 - 74 % of the
+// of both 7.42 (one set of sums for both kinds 6.37); matrix units busy 61 - 74 % of the
 // clocks instead of 74 - 86, for half as many LDS reads again and 64-byte lines in the
 // second turn.
 #include <type_traits>
@@ -709,8 +710,8 @@ __global__ __launch_bounds__(THREADS) void ortho_split_kernel(const OrthoSplit a
       u[j] = __builtin_amdgcn_perm(tile[row][e + 2 * j + 1], tile[row][e + 2 * j], sel);
       v[j] = __builtin_amdgcn_perm(tile[e + 2 * j + 1][row], tile[e + 2 * j][row], sel);
     }
-    // Past the caches: 8 matrices of 4096 x 2048 161 us, otherwise 195; 16 of 256 x
-    // 512 alike.
+    // Past the caches: 8 matrices of 4096 x 2048 in bf16 103 us, otherwise 113, in f32
+    // 124 / 134; 16 of 256 x 512 alike.
     __builtin_nontemporal_store(u, (u32x4*)(x + (int64_t)row * a.ldx));
     __builtin_nontemporal_store(v, (u32x4*)(xt + (int64_t)row * a.ldxt));
   }
