@@ -493,8 +493,8 @@ __global__ __launch_bounds__(kThreads<LANES>, (kWaves<LANES, CH>)) void block_bw
   }
   const bool alone = gridDim.x == 1;  // no one to join
   if (!a.partial) return;
-  if constexpr (HELD) pass_on();
   if constexpr (LANES <= 64) {
+    pass_on();
     // The groups' sums, joined in their order.
     constexpr int G = 256 / LANES, COLS = LANES * CH * N;
     __syncthreads();
@@ -523,8 +523,11 @@ __global__ __launch_bounds__(kThreads<LANES>, (kWaves<LANES, CH>)) void block_bw
 #pragma unroll
       for (int j = 0; j < N; j++)
         if (at + j < a.c) {
-          const float u = HELD ? join[0][HELD ? i * N + j : 0][lane] : first(i, j);
-          const float v = HELD ? join[1][HELD ? i * N + j : 0][lane] : post[i][j];
+          float u = first(i, j), v = post[i][j];
+          if (HELD && more) {
+            u += join[0][HELD ? i * N + j : 0][lane];
+            v += join[1][HELD ? i * N + j : 0][lane];
+          }
           if (alone) {
             finish_column(a.finish, 0, at + j, u);
             finish_column(a.finish, 1, at + j, v);
