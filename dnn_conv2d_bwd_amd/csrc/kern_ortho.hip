@@ -46,8 +46,8 @@
 // products a run to hide their loads.  Tiles of 256 that sum twice have 64 products a
 // run and more to read for each: five stages of one operand, all of the LDS, where
 // each is filled again as soon as it is free, 7.26 ms for 8 x 4096 x 2048 in f32, two
-// of both 7.42 (one set of sums for both kinds 6.37); matrix units busy 61 - 74 % of the
-// clocks instead of 74 - 86, for half as many LDS reads again and 64-byte lines in the
+// of both 7.42 (one set of sums for both kinds 6.37); matrix units busy 54 - 64 % of the
+// clocks instead of 60 - 78, for half as many LDS reads again and 64-byte lines in the
 // second turn.
 #include <type_traits>
 
