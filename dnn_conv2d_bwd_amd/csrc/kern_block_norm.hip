@@ -19,8 +19,7 @@
 // ..., loads the next one before it joins the sums of this one, and keeps its
 // columns' sums in registers for 128 rows, then adds them up in LDS; in the end they
 // go to memory, one row of them a workgroup, for a second launch to join in a fixed
-// order.  z is rounded
-// where it is stored, not where n is made of it.
+// order.  z is rounded where it is stored, not where n is made of it.
 //
 // Bound: HBM.  32768 x 4096 in bf16, vectors for all three: forward 212 us (5.1
 // TB/s; a copy on this card reaches 4.7), backward 302 (5.3) and 5 for the
@@ -461,7 +460,7 @@ __global__ __launch_bounds__(kThreads<LANES>, (kWaves<LANES, CH>)) void block_bw
     if (kAhead<CH> && row + rows.step < a.rows) fetch_all(row + rows.step);
     sum(s);
     // (Where there is no norm, nothing is taken off: not 0 times infinity.)
-    const float along = second ? rz * s[0] * inv_c : 0.f;                 // of zn in dz'
+    const float along = second ? rz * s[0] * inv_c : 0.f;               // of zn in dz'
     const float back = (second ? s[1] - along * s[2] : s[1]) * inv_c;  // of yn in dy
 #pragma unroll
     for (int i = 0; i < CH; i++) {

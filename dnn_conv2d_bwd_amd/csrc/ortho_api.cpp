@@ -163,7 +163,7 @@ cbd_status make_plan(const cbd_ortho_problem* q, cbd_ortho_plan_t** out) {
   // Tiles of 256 take 1.14 times as long where lo is scaled, which makes them sum hi
   // lo and lo hi, then hi hi (5 steps of 8 matrices of 4096 x 2048 7.26 ms, 6.37).  So
   // bf16 updates with such tiles go without: their values have 22 bits down to 2^-17
-  // of the bounds below, not to 2^-28, and are off by 2^-39 of them at most, where
+  // of the bounds above, not to 2^-28, and are off by 2^-39 of them at most, where
   // the results have 8 bits.
   p->lo_up = q->dtype == CBD_BF16 && pad == 256 ? 1.f : 2048.f;
   p->sp = up_to(p->s, pad);
